@@ -5,7 +5,9 @@ Argument marshalling only.  Every step of the path (layout, dispatch,
 combine) runs in the HIP kernels of libep.so; torch provides device memory
 and the current stream.  The raw functions below carry the C names of
 include/ep.h and take preallocated torch tensors; ``EpBuffers`` allocates
-the tensors for one configuration and chains the three calls.
+the tensors for one configuration and chains the three calls.  The router
+and the experts' products of include/ep_moe.h are in ``moe`` and exported
+here too.
 
 There is no fallback: if libep.so is missing or cannot be loaded, every call
 raises.  Build it with ``python -m combine_get_dispatch_amd._build``.
@@ -19,13 +21,15 @@ import re
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libep.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "ep.h")
-HEADER_PATHS = [HEADER_PATH, os.path.join(os.path.dirname(_PKG), "include", "ep_probe.h")]
+HEADER_PATHS = [os.path.join(os.path.dirname(_PKG), "include", h)
+                for h in ("ep.h", "ep_moe.h", "ep_probe.h")]
 
 (EP_OK, EP_ERR_INVALID_ARG, EP_ERR_INVALID_ROUTE, EP_ERR_CAPACITY, EP_ERR_WORKSPACE, EP_ERR_HIP,
- EP_ERR_NONFINITE) = range(7)
+ EP_ERR_NONFINITE, EP_ERR_SEQS) = range(8)
 EP_STATUS_BIT_ROUTE, EP_STATUS_BIT_CAPACITY, EP_STATUS_BIT_WORKSPACE, EP_STATUS_BIT_NONFINITE = (
     0x1, 0x2, 0x4, 0x8)
-EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3 = 0, 1
+EP_STATUS_BIT_SEQS = 0x10
+EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3, EP_DTYPE_F32 = 0, 1, 2
 
 
 class EpError(RuntimeError):
@@ -109,6 +113,7 @@ def lib() -> ctypes.CDLL:
               "ep_ranked_capacity_rows", "ep_dispatch_ranked", "ep_expand", "ep_combine_ranked",
               "ep_hbm_probe", "ep_time_next_kernel", "ep_layout_dispatch_noalloc"):
         getattr(L, f).restype = ctypes.c_int
+    moe.register(L)
     _lib = L
     return L
 
@@ -668,6 +673,21 @@ class EpBuffers:
             self.row_src, self.status, stream=stream, zero_padding=self.zero_padding)
         return self.handle
 
+    def expert_product(self, experts, x=None, out=None, rank=None, stream=None):
+        """The experts' product (W4Experts) on the receive rows, or on bf16
+        rows x in their places: bf16 [capacity, out_features].  The weights
+        are all experts', or with ``rank`` that rank's (its rows alone are
+        written)."""
+        offs, counts = self.expert_offsets, self.num_tokens_per_expert
+        if rank is not None:
+            if not 0 <= rank < self.cfg.num_ranks:
+                raise ValueError(f"rank {rank} outside [0, {self.cfg.num_ranks})")
+            n = self.cfg.num_experts // self.cfg.num_ranks
+            offs, counts = offs[rank * n:(rank + 1) * n + 1], counts[rank * n:(rank + 1) * n]
+        scales = self.recv_scales if x is None else None
+        return experts.product(self.recv_x if x is None else x, scales, offs, counts, out=out,
+                               stream=stream)
+
     def combine(self, expert_out, topk_weights, out=None, stream=None):
         import torch
 
@@ -758,3 +778,9 @@ class EpBuffers:
 
     def check_status(self, stream=None):
         ep_read_status(self.status, stream=stream)
+
+
+from . import moe  # noqa: E402  (needs the names above)
+from .moe import (EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, EpRouter, W4Experts,  # noqa: E402,F401
+                  ep_balance_loss, ep_balance_workspace_bytes, ep_expert_product_w4, ep_route,
+                  ep_route_backward, ep_router_t, ep_w4_pack, ep_w4_packed_sizes, ep_w4_t)

@@ -2,8 +2,8 @@
 
     python -m combine_get_dispatch_amd._build
 
-Flags: -O3; -ffp-contract=off so that only the explicit fused multiply-adds
-of combine contract; packed fp32 instructions disabled; fp32 division stays
+Flags: -O3; -ffp-contract=off so that only explicit fused multiply-adds
+contract; packed fp32 instructions disabled; fp32 division stays
 correctly rounded (the HIP default), which the FP8 quantiser relies on.
 """
 from __future__ import annotations
@@ -15,7 +15,9 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("ep_kernels.hip", "ep_api.hip", "hbm_probe.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f)
+           for f in ("ep_kernels.hip", "ep_api.hip", "hbm_probe.hip", "ep_router.hip",
+                     "ep_w4.hip")]
 LIB = os.path.join(PKG, "libep.so")
 
 HIPCC_FLAGS = [

@@ -123,7 +123,7 @@ ep_status_t check_workspace(const ep_config_t *c, const void *workspace, size_t 
 }  // namespace
 
 namespace ep {
-// Lets the probe entry point (hbm_probe.hip) report through ep_last_error().
+// Lets the entry points of other files report through ep_last_error().
 ep_status_t set_error(ep_status_t st, const char *message) { return fail(st, "%s", message); }
 }  // namespace ep
 
@@ -137,7 +137,9 @@ const char *ep_status_string(ep_status_t status) {
     case EP_ERR_CAPACITY: return "receive buffer too small";
     case EP_ERR_WORKSPACE: return "workspace not written by a layout of this configuration and route";
     case EP_ERR_HIP: return "HIP runtime error";
-    case EP_ERR_NONFINITE: return "a hidden value or a valid selection's gate is inf or NaN";
+    case EP_ERR_NONFINITE:
+      return "a hidden value or a valid selection's gate is inf or NaN, or a logit NaN or +inf";
+    case EP_ERR_SEQS: return "sequence offsets do not ascend from 0 to the token count";
   }
   return "unknown status";
 }
@@ -190,7 +192,10 @@ ep_status_t ep_read_status(const int32_t *status, hipStream_t stream) {
     return fail(EP_ERR_WORKSPACE, "dispatch workspace does not match its configuration or route");
   if (host & EP_STATUS_BIT_NONFINITE)
     return fail(EP_ERR_NONFINITE,
-                "a hidden value or the gate of a valid selection is an infinity or NaN");
+                "a hidden value or the gate of a valid selection is an infinity or NaN, "
+                "or a router's logit or key is NaN or infinite");
+  if (host & EP_STATUS_BIT_SEQS)
+    return fail(EP_ERR_SEQS, "sequence offsets do not ascend from 0 to the token count");
   return EP_OK;
 }
 

@@ -17,7 +17,8 @@
  * call, one launch for batches of at most 256 tokens), ep_dispatch_fp8_input
  * (pre-quantised rows), ep_dispatch_backward and ep_combine_backward, and
  * the non-expanded path ep_dispatch_ranked -> ep_expand ->
- * ep_combine_ranked.  A measurement aid is declared apart, in ep_probe.h.
+ * ep_combine_ranked.  The router in front of the path and the experts'
+ * products behind it are declared in ep_moe.h, a measurement aid in ep_probe.h.
  *
  * Pages cited: "GPU microarchitecture: DeepEP first principles"
  * (backyes.github.io) and "Deep Dive - DeepEP" (leetllm.com), by section.
@@ -66,7 +67,9 @@ typedef enum ep_status {
   EP_ERR_WORKSPACE = 4,     /* workspace not written by a layout of this config
                                and this route */
   EP_ERR_HIP = 5,           /* a HIP runtime call failed */
-  EP_ERR_NONFINITE = 6      /* a hidden value or a valid selection's gate is inf or NaN */
+  EP_ERR_NONFINITE = 6,     /* a hidden value or a valid selection's gate is inf or NaN,
+                               or a router's logit is NaN or +inf */
+  EP_ERR_SEQS = 7           /* sequence offsets do not ascend from 0 to T */
 } ep_status_t;
 
 /* Bits the kernels OR into the device status word. */
@@ -74,10 +77,12 @@ typedef enum ep_status {
 #define EP_STATUS_BIT_CAPACITY 0x2
 #define EP_STATUS_BIT_WORKSPACE 0x4
 #define EP_STATUS_BIT_NONFINITE 0x8
+#define EP_STATUS_BIT_SEQS 0x10
 
 typedef enum ep_dtype {
   EP_DTYPE_BF16 = 0,     /* rows are bf16, copied bit for bit */
-  EP_DTYPE_FP8_E4M3 = 1  /* OCP E4M3 ("FN", max 448) codes + one fp32 scale per 128 values */
+  EP_DTYPE_FP8_E4M3 = 1, /* OCP E4M3 ("FN", max 448) codes + one fp32 scale per 128 values */
+  EP_DTYPE_F32 = 2       /* fp32 (router logits only, ep_moe.h) */
 } ep_dtype_t;
 
 /* Limits of this implementation (checked; EP_ERR_INVALID_ARG beyond them). */

@@ -1,0 +1,382 @@
+"""The router, its balance loss and their gradient on the GPU against the
+plain 64-bit implementations of tests/moe_reference.py.
+
+Tolerances, in half steps of fp32 (2^-24): an exponential of x - m is off by
+2 (the function) and |x - m| (the argument's rounding), a score or weight made
+of two of them, a sum of up to 2^10 terms in a tree (10 + 6), a quotient and
+a product by  2 (2 + |x - m|) + 18;  a sum over tokens adds one per addition."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import combine_get_dispatch_amd as ep  # noqa: E402
+from tests import moe_reference as ref  # noqa: E402
+from tests.gpu_backend import dev, say  # noqa: E402
+
+U32, UBF16 = ref.U32, ref.UBF16
+
+
+def draw_logits(rng, T, E, bf16, spread=1.5):
+    x = (rng.normal(size=(T, E)) * spread).astype(np.float32)
+    t = torch.from_numpy(x)
+    if bf16:
+        t = t.bfloat16()
+    return t.float().numpy(), t
+
+
+def score_steps(x):
+    """Half steps a weight or probability of each row may be off by.  Distances
+    count up to 110: exp(-110) < 2e-48, so a term further off is zero within
+    the absolute 1e-37 that every comparison allows (fp32 holds no more of it)."""
+    fin = np.where(np.isfinite(x), x, 0.0).astype(np.float64)
+    d = np.minimum(np.abs(fin - fin.max(axis=1, keepdims=True)), 110) + np.minimum(
+        np.abs(fin).max(axis=1, keepdims=True), 110)
+    return 2 * (2 + d.max(axis=1)) + 18
+
+
+def check_route(got, x, k, **kw):
+    idx, w = got[0].cpu().numpy(), got[1].cpu().numpy()
+    ids, ww, bad = ref.route(x, k, **kw)
+    assert np.array_equal(idx, ids)
+    tol = np.abs(ww) * (score_steps(x) * U32)[:, None] + 1e-37
+    assert np.all(np.abs(w - ww) <= tol), np.max(np.abs(w - ww) / tol)
+    return bad
+
+
+SIZES = [(1, 1, 1), (1, 2, 2), (3, 7, 3), (5, 8, 8), (17, 60, 4), (33, 64, 6), (16, 65, 5),
+         (40, 100, 32), (64, 128, 8), (31, 200, 7), (129, 256, 8), (9, 257, 9), (12, 512, 16),
+         (7, 1000, 32), (4, 1024, 10)]
+
+
+@pytest.mark.parametrize("T,E,k", SIZES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_sizes(T, E, k, score, bf16):
+    rng = np.random.default_rng(T * 1000 + E)
+    x, t = draw_logits(rng, T, E, bf16)
+    for normalize, scale in ((True, 1.0), (False, 2.5)):
+        say(f"route T={T} E={E} k={k} {score} bf16={bf16} normalize={normalize}")
+        r = ep.EpRouter(T, E, k, score=score, normalize=normalize, scale=scale,
+                        logits_dtype=t.dtype)
+        got = r.route(t.cuda())
+        r.check_status()
+        check_route(got, x, k, score=score, normalize=normalize, scale=scale)
+
+
+@pytest.mark.parametrize("E,G,tg,topn,k", [(8, 2, 1, 1, 3), (8, 8, 3, 2, 3), (60, 5, 2, 2, 6),
+                                           (64, 8, 4, 1, 6), (64, 64, 9, 2, 9), (96, 3, 1, 2, 32),
+                                           (128, 16, 4, 2, 8), (256, 8, 4, 1, 8),
+                                           (256, 8, 4, 2, 8), (256, 64, 7, 2, 8), (320, 5, 2, 2, 8),
+                                           (1024, 32, 4, 1, 12), (1024, 2, 1, 2, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_groups_and_bias(E, G, tg, topn, k, score, biased, bf16):
+    T = 37
+    rng = np.random.default_rng(E * 100 + G)
+    x, t = draw_logits(rng, T, E, bf16)
+    bias = (rng.normal(size=E) * 0.1).astype(np.float32) if biased else None
+    say(f"route groups E={E} G={G} keep={tg} topn={topn} {score} bias={biased} bf16={bf16}")
+    r = ep.EpRouter(T, E, k, score=score, groups=G, topk_groups=tg, group_topn=topn,
+                    logits_dtype=t.dtype)
+    got = r.route(t.cuda(), bias=None if bias is None else dev(bias))
+    r.check_status()
+    check_route(got, x, k, score=score, bias=bias, groups=G, topk_groups=tg, group_topn=topn)
+
+
+def test_route_ties_go_to_the_lowest_index():
+    """Equal logits, equal keys, and keys that 32 bits cannot tell apart."""
+    T, E, k = 6, 256, 8
+    x = np.zeros((T, E), np.float32)
+    x[1] = np.repeat(np.arange(E // 4, dtype=np.float32) % 3, 4)
+    x[2, ::2] = -0.0
+    x[3] = np.float32(1) + (np.arange(E) % 5).astype(np.float32) * np.float32(2 ** -23)
+    x[4] = 30 + (np.arange(E) % 7).astype(np.float32) * np.float32(2 ** -19)  # sigmoid ~ 1
+    x[5] = -np.finfo(np.float32).max
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, np.zeros(E, np.float32)):
+            for G, tg, topn in ((1, 1, 1), (8, 4, 2), (16, 3, 1)):
+                say(f"ties {score} bias={bias is not None} G={G}")
+                r = ep.EpRouter(T, E, k, score=score, groups=G, topk_groups=tg, group_topn=topn,
+                                normalize=False)
+                idx, w = r.route(dev(x), bias=None if bias is None else dev(bias))
+                r.check_status()
+                ids, _, _ = ref.route(x, k, score, bias, groups=G, topk_groups=tg,
+                                      group_topn=topn, normalize=False)
+                assert np.array_equal(idx.cpu().numpy(), ids)
+
+
+def test_route_masked_experts_tokens_and_bad_rows():
+    """-inf logits and biases, fewer selectable experts than slots, whole rows
+    of -inf, the type's lowest values, masked tokens that hold NaN, and rows
+    that hold NaN or +inf."""
+    T, E, k = 12, 24, 4
+    rng = np.random.default_rng(5)
+    x, _ = draw_logits(rng, T, E, False)
+    x[0] = -np.inf
+    x[1, 2:] = -np.inf                       # two left
+    x[2] = np.finfo(np.float32).min
+    x[2, 7] = 0
+    x[3] = np.finfo(np.float32).min
+    x[4, ::3] = -np.inf
+    x[5] = np.nan                            # masked
+    x[6, 3] = np.inf                         # masked
+    x[7] = -200.0                            # sigmoid scores that underflow
+    x[7, 4] = -180.0
+    mask = np.ones(T, np.uint8)
+    mask[[5, 6, 11]] = 0
+    bias = (rng.normal(size=E) * 0.1).astype(np.float32)
+    bias[9] = -np.inf
+    for score in ("softmax", "sigmoid"):
+        for b in (None, bias):
+            for G, tg, topn in ((1, 1, 1), (4, 2, 1), (4, 2, 2), (12, 2, 2)):
+                say(f"masks {score} bias={b is not None} G={G} topn={topn}")
+                r = ep.EpRouter(T, E, k, score=score, groups=G, topk_groups=tg, group_topn=topn)
+                got = r.route(dev(x), bias=None if b is None else dev(b), token_mask=dev(mask))
+                r.check_status()
+                check_route(got, x, k, score=score, bias=b, mask=mask, groups=G, topk_groups=tg,
+                            group_topn=topn)
+    for col, v in ((0, np.nan), (23, np.inf)):
+        y = x.copy()
+        y[9, col] = v
+        r = ep.EpRouter(T, E, k)
+        idx, w = r.route(dev(y), token_mask=dev(mask))
+        with pytest.raises(ep.EpError) as err:
+            r.check_status()
+        assert err.value.status == ep.EP_ERR_NONFINITE
+        assert (idx[9] == -1).all() and (w[9] == 0).all() and (idx[8] >= 0).all()
+    for v in (np.nan, np.inf):
+        y = bias.copy()
+        y[3] = v
+        r = ep.EpRouter(T, E, k, score="sigmoid")
+        idx, w = r.route(dev(x), bias=dev(y), token_mask=dev(mask))
+        with pytest.raises(ep.EpError) as err:
+            r.check_status()
+        assert err.value.status == ep.EP_ERR_NONFINITE and (idx[8] == -1).all()
+
+
+def test_route_unaligned_rows():
+    """Logits that start in the middle of a 16-byte piece."""
+    rng = np.random.default_rng(6)
+    for E in (64, 61):
+        for bf16 in (False, True):
+            x, t = draw_logits(rng, 20, E, bf16)
+            buf = torch.zeros(20 * E + 1, dtype=t.dtype, device="cuda")
+            view = buf[1:].view(20, E)
+            view.copy_(t)
+            say(f"unaligned E={E} bf16={bf16}")
+            r = ep.EpRouter(20, E, 5, logits_dtype=t.dtype)
+            check_route(r.route(view), x, 5)
+            w = rng.normal(size=(20, 5)).astype(np.float32)
+            g = torch.empty(20 * E + 1, dtype=t.dtype, device="cuda")
+            out = r.backward(view, r.topk_idx, dev(w), grad_logits=g[1:].view(20, E))
+            check_grad(out, x, r.topk_idx.cpu().numpy(), w, bf16)
+
+
+# --------------------------------------------------------------------------
+
+def draw_route(rng, T, E, k, off=0.1):
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    ids[rng.random((T, k)) < off] = -1
+    ids[rng.random(T) < off] = -1
+    return ids
+
+
+def draw_offsets(rng, T, S):
+    cuts = np.sort(rng.integers(0, T + 1, size=S - 1))
+    return np.concatenate([[0], cuts, [T]]).astype(np.int32)
+
+
+BAL = [(1, 1, 1, 1), (1, 8, 2, 1), (7, 60, 3, 3), (64, 64, 6, 1), (65, 64, 6, 2), (63, 65, 5, 63),
+       (300, 256, 8, 1), (300, 256, 8, 7), (1000, 128, 4, 90), (200, 512, 3, 2), (77, 1000, 32, 5),
+       (3000, 8, 2, 4)]
+
+
+@pytest.mark.parametrize("T,E,k,S", BAL)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_balance(T, E, k, S, score, bf16):
+    rng = np.random.default_rng(T + E)
+    x, t = draw_logits(rng, T, E, bf16)
+    ids = draw_route(rng, T, E, k)
+    x[(ids < 0).all(axis=1)] = 0  # the reference's padding; the kernel gets NaN there
+    t = t.clone()
+    t[torch.from_numpy((ids < 0).all(axis=1))] = float("nan")
+    offsets = None if S == 1 else draw_offsets(rng, T, S)
+    say(f"balance T={T} E={E} k={k} S={S} {score} bf16={bf16}")
+    r = ep.EpRouter(T, E, k, score=score, logits_dtype=t.dtype, max_seqs=S + 1)
+    loss = r.balance_loss(t.cuda(), dev(ids), 0.7,
+                          seq_offsets=None if offsets is None else dev(offsets))
+    r.check_status()
+    l, counts, n, mean, q = ref.balance(x, ids, 0.7, score, offsets)
+    assert np.array_equal(r.counts.cpu().numpy(), counts)
+    assert np.array_equal(r.seq_tokens.cpu().numpy(), n)
+    # a tile's sum of probabilities: at most 128 additions in fp32, the rest in 64 bits
+    rel = (score_steps(x).max() + 128) * U32
+    assert np.all(np.abs(r.mean_probs.cpu().numpy() - mean) <= rel * mean + 1e-30)
+    assert np.all(np.abs(r.prob_grad.cpu().numpy() - q) <= 4 * U32 * q)
+    assert abs(loss.item() - l) <= rel * l + 1e-30
+
+
+def test_balance_empty_and_all_masked():
+    for T in (0, 5):
+        r = ep.EpRouter(T, 8, 2)
+        x = torch.full((T, 8), float("nan"), device="cuda")
+        ids = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+        say(f"balance of nothing T={T}")
+        assert r.balance_loss(x, ids, 1.0).item() == 0
+        r.check_status()
+        assert (r.counts == 0).all() and (r.prob_grad == 0).all() and (r.mean_probs == 0).all()
+        assert (r.seq_tokens == 0).all()
+        g = r.backward(x, ids, torch.zeros(T, 2, device="cuda"), prob_grad=r.prob_grad)
+        assert (g == 0).all() and g.shape == (T, 8)
+        r.route(x, token_mask=torch.zeros(T, dtype=torch.uint8, device="cuda"))
+        r.check_status()
+        assert (r.topk_idx == -1).all() and (r.topk_weights == 0).all()
+
+
+def test_bad_offsets_and_ids_are_reported():
+    T, E, k = 130, 8, 2
+    rng = np.random.default_rng(7)
+    x, t = draw_logits(rng, T, E, False)
+    ids = draw_route(rng, T, E, k)
+    for bad in ([0, 90, 20, T], [1, 20, 90, T], [0, 20, 90, T - 1], [0, -5, 90, T],
+                [0, 20, 10 ** 6, T], [0, 20, 90, 10 ** 6]):
+        say(f"bad offsets {bad}")
+        r = ep.EpRouter(T, E, k, max_seqs=3)
+        r.balance_loss(dev(x), dev(ids), 1.0, seq_offsets=dev(np.array(bad, np.int32)))
+        with pytest.raises(ep.EpError) as err:
+            r.check_status()
+        assert err.value.status == ep.EP_ERR_SEQS
+        r.backward(dev(x), dev(ids), None, r.prob_grad,
+                   seq_offsets=dev(np.array(bad, np.int32)))
+        torch.cuda.synchronize()
+    for v in (E, -2, 2 ** 31 - 1):
+        y = ids.copy()
+        y[3] = v
+        y[3, 0] = 1
+        say(f"bad id {v}")
+        r = ep.EpRouter(T, E, k)
+        r.balance_loss(dev(x), dev(y), 1.0)
+        with pytest.raises(ep.EpError) as err:
+            r.check_status()
+        assert err.value.status == ep.EP_ERR_INVALID_ROUTE
+        y[3, 1] = -1
+        counts = ref.balance(x, y, 1.0)[1]
+        assert np.array_equal(r.counts.cpu().numpy(), counts)
+        r = ep.EpRouter(T, E, k)
+        u = rng.normal(size=(T, k)).astype(np.float32)
+        z = y.copy()
+        z[3, 1] = v
+        g = r.backward(dev(x), dev(z), dev(u))
+        check_grad(g, x, y, u, False)
+        with pytest.raises(ep.EpError):
+            r.check_status()
+
+
+# --------------------------------------------------------------------------
+
+def check_grad(got, x, ids, u, bf16, **kw):
+    want, size = ref.grad(x, ids, u, **kw)
+    got = got.float().cpu().numpy()
+    # each term: a score or two (score_steps each), products and differences (8), and
+    # a sum over the experts (2^10 terms of a tree, 16, in each lane 16)
+    tol = size * ((2 * score_steps(x) + 40) * U32)[:, None] + 1e-37
+    if bf16:
+        tol = tol + np.abs(want) * UBF16 * (1 + 1e-6)
+    assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / tol)
+
+
+GRAD = [(1, 1, 1, 1), (1, 8, 2, 1), (3, 7, 7, 2), (17, 60, 4, 3), (33, 64, 6, 1), (16, 65, 5, 4),
+        (40, 100, 32, 1), (50, 256, 8, 9), (9, 512, 20, 2), (6, 1000, 32, 2), (5, 1024, 3, 1)]
+
+
+@pytest.mark.parametrize("T,E,k,S", GRAD)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_backward(T, E, k, S, score, normalize, bf16):
+    rng = np.random.default_rng(T + E)
+    x, t = draw_logits(rng, T, E, bf16)
+    ids = draw_route(rng, T, E, k)
+    off = (ids < 0).all(axis=1)
+    t = t.clone()
+    t[torch.from_numpy(off)] = float("nan")  # padding: not read into any result
+    u = rng.normal(size=(T, k)).astype(np.float32)
+    nan_u = np.where(ids < 0, np.float32(np.nan), u)
+    q = rng.normal(size=(S, E)).astype(np.float32)
+    offsets = None if S == 1 else draw_offsets(rng, T, S)
+    so = None if offsets is None else dev(offsets)
+    r = ep.EpRouter(T, E, k, score=score, normalize=normalize, scale=1.5, logits_dtype=t.dtype,
+                    max_seqs=S)
+    kw = dict(score=score, normalize=normalize, scale=1.5)
+    for name, uu, qq, gl in (("gates", nan_u, None, None), ("loss", None, q, 3.0),
+                             ("both", nan_u, q, 0.25), ("loss of 1", None, q, None)):
+        say(f"backward T={T} E={E} k={k} S={S} {score} normalize={normalize} bf16={bf16} {name}")
+        out = torch.full((T, E), 7.0, dtype=t.dtype, device="cuda")
+        g = r.backward(t.cuda(), dev(ids), None if uu is None else dev(uu),
+                       prob_grad=None if qq is None else dev(qq), seq_offsets=so,
+                       grad_loss=None if gl is None else torch.full((1,), gl, device="cuda"),
+                       grad_logits=out)
+        r.check_status()
+        check_grad(g, np.where(off[:, None], 0, x), ids, None if uu is None else u, bf16,
+                   prob_grad=qq, offsets=offsets, grad_loss=1.0 if gl is None else gl, **kw)
+
+
+def test_backward_masked_and_extreme_logits():
+    """-inf and lowest logits beside the selected ones, scores that underflow."""
+    T, E, k = 6, 16, 3
+    rng = np.random.default_rng(8)
+    x, _ = draw_logits(rng, T, E, False)
+    x[0, 3:] = -np.inf
+    x[1, 4:] = np.finfo(np.float32).min
+    x[2] -= 300
+    x[3] += 300
+    x[4, 0] = 90
+    ids = np.array([[0, 1, 2], [0, 1, 3], [5, 4, 9], [1, 2, 3], [0, 7, 2], [3, -1, 1]], np.int32)
+    u = rng.normal(size=(T, k)).astype(np.float32)
+    q = rng.normal(size=(1, E)).astype(np.float32)
+    for score in ("softmax", "sigmoid"):
+        for normalize in (True, False):
+            say(f"extreme {score} normalize={normalize}")
+            r = ep.EpRouter(T, E, k, score=score, normalize=normalize)
+            g = r.backward(dev(x), dev(ids), dev(u), prob_grad=dev(q))
+            r.check_status()
+            check_grad(g, x, ids, u, False, score=score, normalize=normalize, prob_grad=q)
+
+
+def test_backward_against_differences():
+    """The kernels' gradient against differences of the kernels' own forward:
+    a step h of the logits, error h^2 / 6 of a third derivative (order 1) and
+    fp32 forward values (2^-22) over h."""
+    T, E, k = 4, 12, 3
+    rng = np.random.default_rng(9)
+    # a quarter between neighbours: no step moves an expert in or out
+    x = np.array([rng.permutation(E) for _ in range(T)], np.float32) / 4 - 1.5
+    u = rng.normal(size=(T, k)).astype(np.float32)
+    h = 2.0 ** -6
+    for score in ("softmax", "sigmoid"):
+        r = ep.EpRouter(T, E, k, score=score)
+        idx = r.route(dev(x))[0].cpu().numpy()
+        r.balance_loss(dev(x), dev(idx), 1.0)
+        g = r.backward(dev(x), dev(idx), dev(u), prob_grad=r.prob_grad).cpu().numpy()
+        bias = np.zeros(E, np.float32)
+
+        def value(z):
+            # the ids stay: only their weights and the loss move
+            i, w = r.route(dev(z), bias=dev(bias))
+            i, w = i.cpu().numpy(), w.cpu().numpy().astype(np.float64)
+            assert np.array_equal(np.sort(i), np.sort(idx))
+            order = np.argsort(i, axis=1)
+            back = np.argsort(np.argsort(idx, axis=1), axis=1)
+            w = np.take_along_axis(np.take_along_axis(w, order, axis=1), back, axis=1)
+            return (w * u).sum() + r.balance_loss(dev(z), dev(idx), 1.0).item()
+
+        for t in range(T):
+            for e in range(E):
+                d = np.zeros_like(x)
+                d[t, e] = h
+                up, down = value(x + d), value(x - d)
+                assert abs(g[t, e] - (up - down) / (2 * h)) < h * h + 16 * 2.0 ** -22 / h

@@ -1,0 +1,447 @@
+"""The experts' products with 4-bit weights on the GPU.
+
+Where inputs are small integers and scales powers of two, every sum is exact
+in fp32 and the result has to be the bf16 rounding of the exact one, bit for
+bit.  Elsewhere a sum of K terms of fp32 is off by at most K half steps of the
+sum of magnitudes of what the matrix instruction adds (16 + q in 0..31 for
+each |q - z| of the weight), the output by a half step of bf16."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import combine_get_dispatch_amd as ep  # noqa: E402
+import ep_workloads as W  # noqa: E402
+from tests import moe_reference as ref  # noqa: E402
+from tests.gpu_backend import dev, dev_bf16, host_bf16, say  # noqa: E402
+
+U32, UBF16 = ref.U32, ref.UBF16
+
+
+def bf16(a):
+    return torch.from_numpy(np.asarray(a, np.float32)).bfloat16()
+
+
+def draw(rng, E, K, N, group, zeros, swiglu, exact):
+    rows = N * (2 if swiglu else 1)
+    q = rng.integers(0, 16, size=(E, rows, K)).astype(np.uint8)
+    if exact:
+        s = 2.0 ** rng.integers(-3, 2, size=(E, rows, K // group))
+    else:
+        s = (0.5 + rng.random((E, rows, K // group))) * 0.2 / np.sqrt(K)
+    s = bf16(s)
+    z = rng.integers(0, 16, size=(E, rows, K // group)).astype(np.uint8) if zeros else None
+    return q, s, z
+
+
+def packed(q, s, z, swiglu):
+    return ep.W4Experts.pack(dev(ref.pack_codes(q)), s.cuda(), None if z is None else dev(z),
+                             swiglu=swiglu)
+
+
+def draw_rows(rng, cap, K, fp8, exact):
+    """(x on the device, scales on the device or None, the values in 64 bits)"""
+    if exact:
+        v = rng.integers(-4, 5, size=(cap, K)).astype(np.float64)
+    else:
+        v = rng.normal(size=(cap, K))
+    if not fp8:
+        t = bf16(v)
+        return t.cuda(), None, t.double().numpy()
+    t = torch.from_numpy(v.astype(np.float32)).to(torch.float8_e4m3fn)
+    if exact:
+        s = (2.0 ** rng.integers(-2, 3, size=(cap, K // 128))).astype(np.float32)
+    else:
+        s = (rng.random((cap, K // 128)) + 0.1).astype(np.float32)
+    val = t.float().double().numpy() * np.repeat(s.astype(np.float64), 128, axis=1)
+    return t.view(torch.uint8).cuda(), dev(s), val
+
+
+def offsets_of(counts, gap=0):
+    return np.concatenate([[0], np.cumsum(np.asarray(counts) + gap)]).astype(np.int32)
+
+
+SHAPES = [  # E, K, N, group, counts
+    (1, 128, 1, 128, [1]), (1, 128, 16, 128, [16]), (2, 256, 17, 128, [3, 0]),
+    (3, 32, 40, 32, [0, 1, 17]), (2, 96, 33, 32, [5, 31]), (2, 192, 64, 64, [2, 40]),
+    (4, 1024, 100, 64, [0, 0, 7, 1]), (5, 640, 130, 128, [33, 1, 0, 64, 2]),
+    (1, 512, 200, 32, [130]), (8, 384, 96, 128, [9, 8, 7, 6, 5, 4, 3, 200]),
+]
+
+
+@pytest.mark.parametrize("E,K,N,group,counts", SHAPES)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_exact_and_rounded(E, K, N, group, counts, fp8, zeros, swiglu):
+    if fp8 and K % 128:
+        pytest.skip("FP8 rows come in blocks of 128")
+    rng = np.random.default_rng(K + N)
+    cap = int(sum(counts)) + 2 * E
+    off = offsets_of(counts, gap=2)
+    for exact in (True, False):
+        say(f"product E={E} K={K} N={N} group={group} counts={counts} fp8={fp8} zeros={zeros} "
+            f"swiglu={swiglu} exact={exact}")
+        q, s, z = draw(rng, E, K, N, group, zeros, swiglu, exact)
+        x, xs, xv = draw_rows(rng, cap, K, fp8, exact)
+        experts = packed(q, s, z, swiglu)
+        out = torch.full((cap, N), 99.0, dtype=torch.bfloat16, device="cuda")
+        experts.product(x, xs, dev(off), dev(np.array(counts, np.int32)), out)
+        got = out.float().cpu().numpy()
+        w = ref.weights(q, s.float().numpy(), z, group)
+        rows, _ = ref.product(xv, w, off, counts, swiglu)
+        _, size = ref.product(xv, np.repeat(np.abs(s.double().numpy()), group, axis=2) * 32.0, off,
+                              counts, swiglu)
+        for r in range(cap):
+            if r not in rows:
+                assert (got[r] == 99.0).all(), f"row {r} is no expert's and was written"
+                continue
+            want = rows[r]
+            if exact and not swiglu:
+                assert np.array_equal(got[r], bf16(want).float().numpy()), f"row {r}"
+                continue
+            e = int(np.searchsorted(off, r, side="right")) - 1
+            err = (0 if exact else K + 8) * U32 * size[r]
+            if swiglu:
+                # y = silu(a) b: silu has a slope of at most 1.1, the function and the
+                # two products are off by 12 half steps
+                ww = w[e] @ xv[r]
+                a, b = ww[:N], ww[N:]
+                sil = a / (1 + np.exp(-a))
+                err = 1.1 * err[:N] * (np.abs(b) + err[N:]) + np.abs(sil) * err[N:] \
+                    if not exact else 0.0
+                err = err + 12 * U32 * np.abs(want)
+            tol = err + (np.abs(want) + err) * UBF16 + 1e-37
+            assert np.all(np.abs(got[r] - want) <= tol), (r, np.max(np.abs(got[r] - want) / tol))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("K,N,counts", [(7168, 512, [4, 0, 1, 30]), (2048, 1000, [70, 129, 3, 0])])
+def test_product_long_sums(fp8, K, N, counts):
+    """At the sizes of a model: rounding to bf16 alone gives at most 2^-8 of the
+    result's norm, and sums of random signs add next to nothing."""
+    rng = np.random.default_rng(K)
+    q, s, _ = draw(rng, 4, K, N, 128, False, False, False)
+    cap = sum(counts)
+    off = offsets_of(counts)
+    x, xs, xv = draw_rows(rng, cap, K, fp8, False)
+    say(f"long sums K={K} N={N} fp8={fp8}")
+    out = packed(q, s, None, False).product(x, xs, dev(off), dev(np.array(counts, np.int32)))
+    rows, _ = ref.product(xv, ref.weights(q, s.float().numpy(), None, 128), off, counts, False)
+    want = np.stack([rows[r] for r in range(cap)])
+    d = np.linalg.norm(out.float().cpu().numpy() - want, axis=1)
+    assert np.all(d <= UBF16 * np.linalg.norm(want, axis=1))
+
+
+def test_pack_matches_the_layout():
+    """ep_w4_pack against the layout's definition, nibble by nibble."""
+    rng = np.random.default_rng(1)
+    for E, K, N, group, swiglu in ((2, 160, 19, 32, True), (1, 256, 16, 128, False),
+                                   (3, 64, 5, 64, True)):
+        q, s, z = draw(rng, E, K, N, group, True, swiglu, True)
+        halves = 2 if swiglu else 1
+        say(f"pack E={E} K={K} N={N} group={group}")
+        p = packed(q, s, z, swiglu)
+        assert np.array_equal(p.w_codes.cpu().numpy(), ref.tile_codes(q, halves))
+        n16, G = -(-N // 16), K // group
+
+        def tiles(v):
+            full = np.zeros((E, halves, n16 * 16, G), v.dtype)
+            full[:, :, :N] = v.reshape(E, halves, N, G)
+            return full.reshape(E, halves, n16, 16, G).transpose(0, 1, 2, 4, 3)
+
+        assert np.array_equal(host_bf16(p.w_scales), tiles(host_bf16(s)))
+        assert np.array_equal(p.w_zeros.cpu().numpy(), tiles(z))
+
+
+def test_every_code_and_row_value():
+    """Each of the 16 codes against each power of two and each FP8 code, one
+    product at a time: exact, subnormal codes included."""
+    K, N = 128, 16
+    q = np.broadcast_to(np.arange(16, dtype=np.uint8)[None, :, None], (1, N, K)).copy()
+    s = bf16(np.ones((1, N, 1)))
+    codes = np.array([c for c in range(256) if c & 127 != 127], np.uint8)
+    x = np.zeros((len(codes), K), np.uint8)
+    x[np.arange(len(codes)), np.arange(len(codes)) % K] = codes
+    say("every FP8 code")
+    out = packed(q, s, None, False).product(dev(x), torch.ones(len(codes), 1, device="cuda"),
+                                            dev(np.array([0], np.int32)),
+                                            dev(np.array([len(codes)], np.int32)))
+    v = torch.from_numpy(codes).view(torch.float8_e4m3fn).float().numpy()
+    want = bf16(v[:, None] * (np.arange(16) - 8)[None]).float().numpy()
+    assert np.array_equal(out.float().cpu().numpy(), want)
+    pw = np.arange(-100, 100)
+    xb = np.zeros((len(pw), K), np.float32)
+    xb[np.arange(len(pw)), np.arange(len(pw)) % K] = 2.0 ** pw
+    say("powers of two")
+    out = packed(q, s, None, False).product(bf16(xb).cuda(), None, dev(np.array([0], np.int32)),
+                                            dev(np.array([len(pw)], np.int32)))
+    assert np.array_equal(out.float().cpu().numpy(),
+                          (2.0 ** pw)[:, None] * (np.arange(16) - 8)[None])
+
+
+def test_rows_past_the_capacity_and_bad_offsets_are_left_alone():
+    rng = np.random.default_rng(2)
+    E, K, N = 4, 128, 32
+    q, s, _ = draw(rng, E, K, N, 128, False, False, True)
+    p = packed(q, s, None, False)
+    x, _, xv = draw_rows(rng, 10, K, False, True)
+    out = torch.full((14, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    off, cnt = [0, 4, -3, 2 ** 31 - 1], [3, 100, 5, 7]
+    say("rows past the capacity")
+    p.product(x, None, dev(np.array(off, np.int32)), dev(np.array(cnt, np.int32)), out)
+    got = out.float().cpu().numpy()
+    rows, _ = ref.product(xv, ref.weights(q, s.float().numpy(), None, 128), [0, 4], [3, 100],
+                          False)
+    assert sorted(rows) == [0, 1, 2] + list(range(4, 10))
+    for r in range(14):
+        if r in rows:
+            assert np.array_equal(got[r], bf16(rows[r]).float().numpy())
+        else:
+            assert (got[r] == 5.0).all()
+    say("no rows at all")
+    p.product(x[:0], None, dev(np.array(off, np.int32)), dev(np.array(cnt, np.int32)), out)
+    p.product(x, None, dev(np.zeros(4, np.int32)), dev(np.zeros(4, np.int32)), out)
+    assert np.array_equal(out.float().cpu().numpy(), got)
+
+
+def test_python_refusals():
+    rng = np.random.default_rng(3)
+    q, s, _ = draw(rng, 2, 128, 32, 128, False, False, True)
+    p = packed(q, s, None, False)
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out = torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(x=x[:, :64]), dict(x=x.float()), dict(off=off[:1]), dict(cnt=off[:1]),
+                dict(out=out[:3]), dict(out=out.float()), dict(x=x.t().contiguous().t()),
+                dict(xs=torch.ones(4, 1, device="cuda")), dict(cnt=off.long()),
+                dict(x=x.cpu())):
+        a = dict(x=x, xs=None, off=off, cnt=off, out=out)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            p.product(a["x"], a["xs"], a["off"], a["cnt"], a["out"])
+
+
+# --------------------------------------------------------------------------
+# The operators together, as a layer uses them
+# --------------------------------------------------------------------------
+
+def layer_inputs(rng, T, H, E, inner):
+    x = W.normal_bf16(rng, (T, H))
+    centroids = (rng.normal(size=(H, E)) / np.sqrt(H)).astype(np.float32)
+    q1, s1, _ = draw(rng, E, H, inner, 128, False, True, False)
+    q2, s2, z2 = draw(rng, E, inner, H, 64, True, False, False)
+    return x, centroids, (q1, s1), (q2, s2, z2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_layer_forward(T, fp8):
+    """route -> layout -> dispatch -> gate/up with SwiGLU -> down -> combine,
+    all on the device without a synchronisation, against the same in 64 bits
+    from the rounded intermediate rows."""
+    rng = np.random.default_rng(T)
+    H, E, k, R, inner, A = 256, 16, 4, 4, 192, 4
+    x, cen, (q1, s1), (q2, s2, z2) = layer_inputs(rng, T, H, E, inner)
+    xd = dev_bf16(x)
+    logits = xd.float() @ dev(cen)
+    mask = np.ones(T, np.uint8)
+    mask[T // 2:T // 2 + T // 8] = 0
+    bias = (rng.normal(size=E) * 0.05).astype(np.float32)
+    router = ep.EpRouter(T, E, k, score="sigmoid", groups=4, topk_groups=2, group_topn=2,
+                         scale=2.5)
+    b = ep.EpBuffers(T, H, k, E, R, A, fp8=fp8)
+    up, down = packed(q1, s1, None, True), packed(q2, s2, z2, False)
+    mid = torch.zeros(b.capacity, inner, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(b.capacity, H, dtype=torch.bfloat16, device="cuda")
+    say(f"layer T={T} fp8={fp8}")
+    idx, w = router.route(logits, bias=dev(bias), token_mask=dev(mask))
+    b.layout(idx)
+    b.dispatch(xd, idx, w)
+    b.expert_product(up, out=mid)
+    b.expert_product(down, x=mid, out=y)
+    out = b.combine(y, w).float().cpu().numpy()
+    b.check_status()
+    router.check_status()
+    ids, ww, _ = ref.route(logits.cpu().numpy(), k, "sigmoid", bias, mask, 4, 2, 2, True, 2.5)
+    assert np.array_equal(idx.cpu().numpy(), ids)
+    off, cnt = b.expert_offsets.cpu().numpy(), b.num_tokens_per_expert.cpu().numpy()
+    if fp8:
+        xv = b.recv_x.view(torch.float8_e4m3fn).float().cpu().double().numpy() * np.repeat(
+            b.recv_scales.cpu().double().numpy(), 128, axis=1)
+    else:
+        xv = b.recv_x.cpu().double().numpy()
+    w1 = ref.weights(q1, s1.float().numpy(), None, 128)
+    w2 = ref.weights(q2, s2.float().numpy(), z2, 64)
+    rows, _ = ref.product(xv, w1, off, cnt, True)
+    m = mid.cpu().double().numpy()
+    for r, want in rows.items():
+        assert np.linalg.norm(m[r] - want) <= UBF16 * np.linalg.norm(want)
+    rows, _ = ref.product(m, w2, off, cnt, False)
+    yy = y.cpu().double().numpy()
+    for r, want in rows.items():
+        assert np.linalg.norm(yy[r] - want) <= UBF16 * np.linalg.norm(want)
+    slot = b.tok_slot_row.cpu().numpy()
+    for t in range(T):
+        want = np.zeros(H)
+        big = np.zeros(H)
+        for j in range(k):
+            if slot[t, j] >= 0:
+                want += ww[t, j] * yy[slot[t, j]]
+                big += np.abs(ww[t, j] * yy[slot[t, j]])
+        # gates within 60 half steps, a sum of k terms, one rounding
+        assert np.all(np.abs(out[t] - want) <= UBF16 * np.abs(want) + big * (64 + k) * U32 * 2)
+
+
+def test_one_rank_at_a_time():
+    """Each rank's weights on its own rows give what all weights give at once."""
+    rng = np.random.default_rng(11)
+    T, H, E, k, R = 50, 128, 8, 3, 4
+    idx = dev(W.random_routes(rng, T, E, k, 0.1))
+    b = ep.EpBuffers(T, H, k, E, R, 2)
+    b.layout(idx)
+    b.dispatch(dev_bf16(W.normal_bf16(rng, (T, H))), idx, None)
+    q, s, _ = draw(rng, E, H, 48, 128, False, False, False)
+    whole = torch.zeros(b.capacity, 48, dtype=torch.bfloat16, device="cuda")
+    parts = torch.zeros_like(whole)
+    b.expert_product(packed(q, s, None, False), out=whole)
+    for r in range(R):
+        b.expert_product(packed(q[2 * r:2 * r + 2], s[2 * r:2 * r + 2], None, False), out=parts,
+                         rank=r)
+    assert torch.equal(whole, parts) and whole.abs().sum() > 0
+    with pytest.raises(ValueError):
+        b.expert_product(packed(q, s, None, False), rank=R)
+
+
+def test_training_step():
+    """Forward and backward of the path with the router: the gates' gradient of
+    combine_backward and the balance loss reach the logits."""
+    rng = np.random.default_rng(12)
+    T, H, E, k, R = 60, 64, 8, 3, 2
+    x, xl = W.normal_bf16(rng, (T, H)), rng.normal(size=(T, E)).astype(np.float32)
+    offsets = np.array([0, 25, T], np.int32)
+    router = ep.EpRouter(T, E, k, max_seqs=2)
+    b = ep.EpBuffers(T, H, k, E, R)
+    logits = dev(xl)
+    idx, w = router.route(logits)
+    loss = router.balance_loss(logits, idx, 0.1, seq_offsets=dev(offsets))
+    b.layout(idx)
+    b.dispatch(dev_bf16(x), idx, w)
+    b.combine(b.recv_x, w)  # experts that return their rows
+    gout = dev_bf16(W.normal_bf16(rng, (T, H)))
+    gw = torch.empty(T, k, device="cuda")
+    b.combine_backward(gout, w, b.recv_x, grad_weights=gw)
+    g = router.backward(logits, idx, gw, prob_grad=router.prob_grad, seq_offsets=dev(offsets),
+                        grad_loss=torch.ones(1, device="cuda"))
+    b.check_status()
+    router.check_status()
+    ids = idx.cpu().numpy()
+    want, size = ref.grad(xl, ids, gw.cpu().numpy(), "softmax", True, 1.0,
+                          router.prob_grad.cpu().numpy(), offsets)
+    assert np.all(np.abs(g.cpu().numpy() - want) <= size * 120 * U32)
+    assert np.isclose(loss.item(), ref.balance(xl, ids, 0.1, "softmax", offsets)[0], rtol=1e-5)
+    per_expert = router.counts.sum(dim=0).to(torch.int32)
+    assert torch.equal(per_expert, b.num_tokens_per_expert)
+
+
+def test_layer_in_a_graph():
+    """The whole layer captured once and replayed on new inputs, with eager
+    calls between, two graphs of two routers and buffers among them."""
+    rng = np.random.default_rng(13)
+    T, H, E, k, R, inner = 24, 256, 16, 4, 4, 128
+    x, cen, (q1, s1), (q2, s2, z2) = layer_inputs(rng, T, H, E, inner)
+    up, down = packed(q1, s1, None, True), packed(q2, s2, z2, False)
+    offsets = dev(np.array([0, 10, T], np.int32))
+
+    def build():
+        st = dict(x=torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"),
+                  logits=torch.zeros(T, E, device="cuda"),
+                  gw=torch.zeros(T, k, device="cuda"))
+        st["router"] = ep.EpRouter(T, E, k, score="sigmoid", max_seqs=2)
+        st["b"] = ep.EpBuffers(T, H, k, E, R)
+        st["mid"] = torch.zeros(st["b"].capacity, inner, dtype=torch.bfloat16, device="cuda")
+        st["y"] = torch.zeros(st["b"].capacity, H, dtype=torch.bfloat16, device="cuda")
+        return st
+
+    def step(st):
+        r, b = st["router"], st["b"]
+        idx, w = r.route(st["logits"])
+        r.balance_loss(st["logits"], idx, 0.1, seq_offsets=offsets)
+        b.layout(idx)
+        b.dispatch(st["x"], idx, w)
+        b.expert_product(up, out=st["mid"])
+        b.expert_product(down, x=st["mid"], out=st["y"])
+        b.combine(st["y"], w)
+        r.backward(st["logits"], idx, st["gw"], prob_grad=r.prob_grad, seq_offsets=offsets)
+
+    def outputs(st):
+        r, b = st["router"], st["b"]
+        return [v.clone() for v in (r.topk_idx, r.topk_weights, r.loss, r.counts, r.mean_probs,
+                                    r.prob_grad, b.out, r.grad_logits)]
+
+    def fill(st, seed):
+        g = np.random.default_rng(seed)
+        st["x"].copy_(dev_bf16(W.normal_bf16(g, (T, H))))
+        st["logits"].copy_(dev(g.normal(size=(T, E)).astype(np.float32)))
+        st["gw"].copy_(dev(g.normal(size=(T, k)).astype(np.float32)))
+
+    states = [build(), build()]
+    eager = build()
+    graphs = []
+    for i, st in enumerate(states):
+        fill(st, i)
+        step(st)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        say(f"capture {i}")
+        with torch.cuda.graph(g):
+            step(st)
+        graphs.append(g)
+    for n in range(4):
+        say(f"replay {n}")
+        for i, (g, st) in enumerate(zip(graphs, states)):
+            fill(st, 10 * n + i)
+            g.replay()
+        torch.cuda.synchronize()
+        for i, st in enumerate(states):
+            got = outputs(st)
+            fill(eager, 10 * n + i)
+            step(eager)
+            torch.cuda.synchronize()
+            for a, c in zip(got, outputs(eager)):
+                assert torch.equal(a, c)
+            st["b"].check_status()
+            st["router"].check_status()
+
+
+def test_two_streams_and_repeats_are_bit_equal():
+    """Calls of separate buffers on two streams at once, and repeated calls."""
+    rng = np.random.default_rng(14)
+    E, K, N = 8, 512, 160
+    q, s, _ = draw(rng, E, K, N, 128, False, True, False)
+    p = packed(q, s, None, True)
+    cnt = np.array([5, 0, 40, 1, 17, 16, 2, 33], np.int32)
+    off = dev(offsets_of(cnt))
+    x, _, _ = draw_rows(rng, int(cnt.sum()), K, False, False)
+    T, G = 500, 64
+    logits = dev(rng.normal(size=(T, G)).astype(np.float32))
+    cnt = dev(cnt)
+    first = p.product(x, None, off, cnt)
+    r0 = ep.EpRouter(T, G, 6)
+    r0.balance_loss(logits, r0.route(logits)[0], 1.0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    routers = [ep.EpRouter(T, G, 6) for _ in streams]
+    outs = [[] for _ in streams]
+    for _ in range(3):
+        for i, (st, r) in enumerate(zip(streams, routers)):
+            with torch.cuda.stream(st):
+                outs[i].append(p.product(x, None, off, cnt))
+                r.balance_loss(logits, r.route(logits)[0], 1.0)
+    torch.cuda.synchronize()
+    for i, r in enumerate(routers):
+        for o in outs[i]:
+            assert torch.equal(o, first)
+        assert torch.equal(r.topk_idx, r0.topk_idx) and torch.equal(r.loss, r0.loss)
+        assert torch.equal(r.mean_probs, r0.mean_probs)
