@@ -38,9 +38,7 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t v) {
 
 // Nearest even; NaN stays NaN.
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) {
-  const uint32_t u = __float_as_uint(v);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
-  return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+  return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 // By exp(-|y|): exp(-y) of a y below -88 is infinite while silu(y) is still a
@@ -95,6 +93,8 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(PackArgs a) {
 // Product
 // --------------------------------------------------------------------------
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 struct ProductArgs {
   const void *x;
   const float *x_scales;
@@ -106,23 +106,33 @@ struct ProductArgs {
   int32_t N, K, N16, K128;
 };
 
-// Rows of expert e inside the buffers.
-__device__ __forceinline__ void expert_rows(const ProductArgs &a, int e, int64_t *first,
-                                            int64_t *rows) {
-  const int64_t o = a.offsets[e], c = a.counts[e];
-  *first = o;
+// Rows of an expert inside the buffers.
+__device__ __forceinline__ void rows_between(int32_t offset, int32_t count, int64_t capacity,
+                                             int64_t *first, int64_t *rows) {
+  *first = offset;
   *rows = 0;
-  if (o < 0 || c <= 0 || o >= a.capacity) return;
-  *rows = c < a.capacity - o ? c : a.capacity - o;
+  if (offset < 0 || count <= 0 || offset >= capacity) return;
+  *rows = count < capacity - offset ? count : capacity - offset;
 }
 
-// The pairs of codes of one word as bf16 pairs 1 + q/16.
+// The same for an expert that the whole wave works on.
+__device__ __forceinline__ void expert_rows(const ProductArgs &a, int e, int64_t *first,
+                                            int64_t *rows) {
+  rows_between(uniform(a.offsets[e]), uniform(a.counts[e]), a.capacity, first, rows);
+}
+
+// The pairs of codes of one word as bf16 pairs 1 + q/16: a shift and one
+// and-or each.  The instruction takes one constant from a scalar register and
+// none from its own encoding, so the other is kept in a vector register.
 __device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
+  uint32_t mask = 0x00780078u, one = 0x3F803F80u;
+  asm("" : "+s"(mask));
+  asm("" : "+v"(one));
   u32x4 v;
-  v[0] = ((w << 3) & 0x00780078u) | 0x3F803F80u;
-  v[1] = ((w >> 1) & 0x00780078u) | 0x3F803F80u;
-  v[2] = ((w >> 5) & 0x00780078u) | 0x3F803F80u;
-  v[3] = ((w >> 9) & 0x00780078u) | 0x3F803F80u;
+  v[0] = ((w << 3) & mask) | one;
+  v[1] = ((w >> 1) & mask) | one;
+  v[2] = ((w >> 5) & mask) | one;
+  v[3] = ((w >> 9) & mask) | one;
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -139,22 +149,77 @@ __device__ __forceinline__ long rows_fp8(uint2 v) {
   return (long)(lo | hi << 32);
 }
 
-// One workgroup: 16 rows of x at a time against kTiles column tiles of one
-// expert (with SwiGLU the first half of them gate, the other half up).  Its
-// four waves take every fourth piece of the sum and add theirs at the end
-// in LDS.
-template <bool FP8, int GROUP, bool ZEROS, bool SWIGLU, int kTiles>
-__global__ __launch_bounds__(256) void product_kernel(ProductArgs a) {
+// A wave's part of one weight tile's work: eight columns of x per lane and
+// matrix instruction.
+template <bool FP8>
+struct Frag {
+  typedef bf16x8 X;
+  static __device__ __forceinline__ f32x4 mul(X x, X w, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ X codes(uint32_t w) { return codes_bf16(w); }
+  static __device__ __forceinline__ X ones() {
+    return __builtin_bit_cast(X, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+  }
+  static constexpr int kBytes = 2;
+  static __device__ __forceinline__ X load(const uint8_t *x, uint32_t at) {
+    return __builtin_bit_cast(
+        X, *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(x) + at));
+  }
+  // dot of codes = kUnit * (dot of what codes() makes - zero_of(z) * sum of x)
+  static constexpr float kUnit = 0x1p4f;
+  static __device__ __forceinline__ float zero_of(float z) { return 1.0f + z * 0x1p-4f; }
+};
+
+template <>
+struct Frag<true> {
+  typedef long X;
+  static __device__ __forceinline__ f32x4 mul(X x, X w, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(x, w, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ X codes(uint32_t w) { return codes_fp8(w); }
+  static __device__ __forceinline__ X ones() { return 0x3838383838383838l; }
+  static constexpr int kBytes = 1;
+  static __device__ __forceinline__ X load(const uint8_t *x, uint32_t at) {
+    return rows_fp8(*reinterpret_cast<const uint2 *>(x + at));
+  }
+  static constexpr float kUnit = 0x1p9f;
+  static __device__ __forceinline__ float zero_of(float z) { return z * 0x1p-9f; }
+};
+
+// Experts with at most kStreamRows rows are streamed (product_stream_kernel),
+// the others tiled (product_tile_kernel).
+constexpr int kStreamRows = 32;
+constexpr int kStreamWaves = 8;
+constexpr int64_t kInfinityCache = int64_t{256} << 20;
+
+// Few rows: the weights are read once, straight into registers, and their
+// reading is the bound.  One workgroup: kTiles column tiles of one expert
+// (with SwiGLU half of them gate, half up) and all its rows, 16 at a time;
+// its waves take every eighth piece of the sum and add theirs in LDS at the
+// end.  No rows are staged and no wave waits for another before that; the
+// loads in flight are those of 16 waves per compute unit.  (Holding a second
+// piece in flight per wave measured slower: its registers halve the waves.)
+//
+// ONCE (non-temporal loads): where a call's weights exceed the Infinity Cache
+// nothing of them is found there again.  480 MB per call: 80 us with, 87
+// without; 34 MB per call, 100 MB in turn: 14.0 with, 12.0 without.
+// 480 MB (32 experts, 7168 x 2 x 2048, 4 rows each, FP8): 75 us, 6.4 TB/s of
+// the 6.9 that reading alone reaches.
+template <bool FP8, int GROUP, bool ZEROS, bool SWIGLU, int kTiles, bool ONCE>
+__global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(ProductArgs a) {
+  typedef Frag<FP8> F;
   constexpr int kHalves = SWIGLU ? 2 : 1;
-  constexpr int kOut = kTiles / kHalves;       // column tiles of the output
-  constexpr int kGroups = kTileK / GROUP;      // groups in a tile
-  constexpr int kPer = GROUP / 32;             // matrix instructions per group
-  __shared__ float part[4][kTiles][kRows * kTileN];
+  constexpr int kOut = kTiles / kHalves;   // column tiles of the output
+  constexpr int kGroups = kTileK / GROUP;  // groups in a tile
+  constexpr int kPer = GROUP / 32;         // matrix instructions per group
+  __shared__ float part[kStreamWaves][kTiles][kRows * kTileN];
   const int e = blockIdx.y;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   int64_t first, rows;
   expert_rows(a, e, &first, &rows);
+  if (rows == 0 || rows > kStreamRows) return;
   const int G = a.K / GROUP;
   const int ot = blockIdx.x * kOut;
   int64_t tile_row[kTiles];
@@ -164,91 +229,339 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs a) {
     n = n < a.N16 ? n : a.N16 - 1;
     tile_row[i] = ((int64_t)e * kHalves + i / kOut) * a.N16 + n;
   }
+  struct Piece {
+    u32x4 w[kTiles];
+    uint16_t s[kTiles][kGroups];
+    uint8_t z[kTiles][kGroups];
+    typename F::X x[4];
+    f32x4 sx;
+  };
   for (int64_t r0 = 0; r0 < rows; r0 += kRows) {
+    const int left = (int)(rows - r0);
+    // this lane's row of x and its four rows of scales, from the first row on
+    const uint8_t *x0 = static_cast<const uint8_t *>(a.x) + (first + r0) * F::kBytes * a.K;
+    const uint32_t xat = (uint32_t)(col < left ? col : left - 1) * a.K + quad * 8;
+    const float *sx0 = FP8 ? a.x_scales + (first + r0) * a.K128 : nullptr;
     f32x4 acc[kTiles];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[i] = f32x4{0, 0, 0, 0};
-    const int64_t left = rows - r0;
-    const int64_t xrow = first + r0 + (col < left ? col : left - 1);
-    for (int kt = wave; kt < a.K128; kt += 4) {
-      u32x4 w[kTiles];
+    const auto load = [&](int kt, Piece &p) {
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        const u32x4 *w = reinterpret_cast<const u32x4 *>(
+                             a.w_codes + (tile_row[i] * a.K128 + kt) * kTileBytes) + lane;
+        p.w[i] = ONCE ? __builtin_nontemporal_load(w) : *w;
+      }
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
-        w[i] = *reinterpret_cast<const u32x4 *>(
-            a.w_codes + (tile_row[i] * a.K128 + kt) * kTileBytes + lane * 16);
-      f32x4 sx;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          // past the last group of a partial tile the last one's scale is read
+          const int gg = kt * kGroups + g < G ? kt * kGroups + g : G - 1;
+          const int64_t at = (tile_row[i] * G + gg) * kTileN;
+          p.s[i][g] = (a.w_scales + at)[col];
+          if (ZEROS) p.z[i][g] = (a.w_zeros + at)[col];
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = kt * kTileK + j * 32;
+        p.x[j] = typename F::X{};
+        if (GROUP == kTileK || c < a.K) p.x[j] = F::load(x0 + c * F::kBytes, xat);
+      }
       if (FP8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = quad * 4 + i;
-          const int64_t r = first + r0 + (m < left ? m : left - 1);
-          sx[i] = a.x_scales[r * a.K128 + kt];
+        for (int v = 0; v < 4; ++v) {
+          const int m = quad * 4 + v;
+          p.sx[v] = (sx0 + kt)[(uint32_t)(m < left ? m : left - 1) * a.K128];
         }
       }
+    };
+    const auto work = [&](const Piece &p) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const int c0 = kt * kTileK + g * GROUP;
-        if (kGroups > 1 && c0 >= a.K) break;
-        f32x4 sum = {0, 0, 0, 0}, dot[kTiles];
+        f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) dot[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int c = c0 + j * 32 + quad * 8;
-          if (FP8) {
-            const long xv = rows_fp8(*reinterpret_cast<const uint2 *>(
-                static_cast<const uint8_t *>(a.x) + xrow * a.K + c));
-            sum = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(xv, 0x3838383838383838l, sum, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-              dot[i] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(
-                  xv, codes_fp8(w[i][g * kPer + j]), dot[i], 0, 0, 0);
-          } else {
-            const bf16x8 xv = __builtin_bit_cast(
-                bf16x8, *reinterpret_cast<const u32x4 *>(
-                            static_cast<const uint16_t *>(a.x) + xrow * a.K + c));
-            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                xv, __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u,
-                                                     0x3F803F80u}),
-                sum, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-              dot[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  xv, codes_bf16(w[i][g * kPer + j]), dot[i], 0, 0, 0);
-          }
-        }
+        for (int j = 0; j < kPer; ++j) sum = F::mul(p.x[g * kPer + j], F::ones(), sum);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-          const int64_t at = (tile_row[i] * G + kt * kGroups + g) * kTileN + col;
-          const float s = bf16_to_f32(a.w_scales[at]);
-          const float z = ZEROS ? (float)a.w_zeros[at] : 8.0f;
-          const float zc = FP8 ? z * 0x1p-9f : 1.0f + z * 0x1p-4f;
+          f32x4 dot = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            dot = F::mul(p.x[g * kPer + j], F::codes(p.w[i][g * kPer + j]), dot);
+          const float s = bf16_to_f32(p.s[i][g]) * F::kUnit;
+          const float z = F::zero_of(ZEROS ? (float)p.z[i][g] : 8.0f);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const float d = __builtin_fmaf(-zc, sum[v], dot[i][v]);
-            acc[i][v] = __builtin_fmaf(FP8 ? s * 0x1p9f * sx[v] : s * 0x1p4f, d, acc[i][v]);
+            const float d = __builtin_fmaf(-z, sum[v], dot[v]);
+            acc[i][v] = __builtin_fmaf(FP8 ? s * p.sx[v] : s, d, acc[i][v]);
           }
         }
       }
+    };
+    for (int kt = wave; kt < a.K128; kt += kStreamWaves) {
+      Piece p;
+      load(kt, p);
+      work(p);
     }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v) part[wave][i][(quad * 4 + v) * kTileN + col] = acc[i][v];
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kOut; ++i) {
-      const int m = threadIdx.x >> 4, n = (ot + i) * kTileN + (threadIdx.x & 15);
+    for (int o = threadIdx.x; o < kOut * kRows * kTileN; o += kStreamWaves * 64) {
+      const int i = o / (kRows * kTileN), at = o % (kRows * kTileN);
+      const int m = at / kTileN, n = (ot + i) * kTileN + at % kTileN;
       float y = 0.0f, up = 0.0f;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        y += part[s][i][threadIdx.x];
-        if (SWIGLU) up += part[s][kOut + i][threadIdx.x];
+      for (int s = 0; s < kStreamWaves; ++s) {
+        y += part[s][i][at];
+        if (SWIGLU) up += part[s][kOut + i][at];
       }
       if (SWIGLU) y = silu(y) * up;
       if (m < left && n < a.N) a.out[(first + r0 + m) * a.N + n] = f32_to_bf16(y);
     }
     __syncthreads();
+  }
+}
+
+constexpr int kBlockRows = 64;   // rows of a block
+constexpr int kBlockTiles = 8;   // weight column tiles of a block
+constexpr int kTileWaves = 3;    // waves per SIMD that fit
+constexpr int kTileGrid = 256 * kTileWaves;  // persistent workgroups, all resident
+
+// Many rows: blocks of 64 rows x 128 weight columns (with SwiGLU 64 gate and
+// the same 64 up), taken in turn by persistent workgroups; the blocks of an
+// expert's rows follow its row count, which only the device knows.  Each of
+// the four waves has all rows and two column tiles.  A piece's rows go through
+// registers to LDS, in the order the matrix instructions take them, one
+// piece ahead of its use and one behind its load; on the way a wave sums
+// its 16 rows over the groups.  So a piece needs one barrier.
+template <bool FP8, int GROUP, bool ZEROS, bool SWIGLU>
+__global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductArgs a, int E) {
+  typedef Frag<FP8> F;
+  constexpr int kHalves = SWIGLU ? 2 : 1;
+  constexpr int kTiles = kBlockTiles / 4;       // of a wave
+  constexpr int kOut = kTiles / kHalves;        // output tiles of a wave
+  constexpr int kGroups = kTileK / GROUP;
+  constexpr int kPer = GROUP / 32;
+  constexpr int kMT = kBlockRows / kRows;       // row tiles of a block
+  static_assert(kMT == 4, "one row tile per wave is staged");
+  __shared__ __align__(16) typename F::X xs[2][kMT][4][64];
+  __shared__ float sums[2][kMT][kGroups][kRows];  // of x over a group
+  __shared__ float sxs[2][kMT][kRows];            // FP8: scales of the rows
+  __shared__ int32_t starts[EP_MAX_EXPERTS + 1];  // first block of each expert
+  __shared__ int32_t scan[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int col = lane & 15, quad = lane >> 4;
+  const int G = a.K / GROUP;
+
+  // blocks of rows per expert, and their prefix sums
+  {
+    int32_t mine[4], total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = tid * 4 + i;
+      int64_t first = 0, rows = 0;
+      if (e < E) rows_between(a.offsets[e], a.counts[e], a.capacity, &first, &rows);
+      mine[i] = rows > kStreamRows ? (int32_t)((rows + kBlockRows - 1) / kBlockRows) : 0;
+      total += mine[i];
+    }
+    scan[tid] = total;
+    __syncthreads();
+    for (int d = 1; d < 256; d *= 2) {
+      const int32_t v = tid >= d ? scan[tid - d] : 0;
+      __syncthreads();
+      scan[tid] += v;
+      __syncthreads();
+    }
+    int32_t at = tid > 0 ? scan[tid - 1] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (tid * 4 + i <= E) starts[tid * 4 + i] = at;
+      at += mine[i];
+    }
+    if (tid == 255 && E == EP_MAX_EXPERTS) starts[E] = at;
+    __syncthreads();
+  }
+  const int nblocks = (a.N16 + kBlockTiles / kHalves - 1) / (kBlockTiles / kHalves);
+  const int64_t items = (int64_t)starts[E] * nblocks;
+  // The items of an XCD (workgroups id % 8) are consecutive, so that the
+  // workgroups that share its L2 share their rows.
+  const int64_t per_xcd = (items + 7) / 8;
+  const int64_t from = (blockIdx.x % 8) * per_xcd;
+  const int64_t to = from + per_xcd < items ? from + per_xcd : items;
+
+  for (int64_t item = from + blockIdx.x / 8; item < to; item += gridDim.x / 8) {
+    const int mb = uniform((int)(item / nblocks)), nb = uniform((int)(item % nblocks));
+    int e = 0, hi = E - 1;
+    while (e < hi) {  // the last expert that starts at or before the block
+      const int mid = (e + hi + 1) / 2;
+      if (starts[mid] <= mb)
+        e = mid;
+      else
+        hi = mid - 1;
+    }
+    e = uniform(e);
+    int64_t first, rows;
+    expert_rows(a, e, &first, &rows);
+    const int blocks = (int)((rows + kBlockRows - 1) / kBlockRows);
+    const int64_t per = ((rows + kRows - 1) / kRows + blocks - 1) / blocks * kRows;
+    const int64_t r0 = (mb - uniform(starts[e])) * per;
+    const int left = (int)(rows - r0 < per ? rows - r0 : per);  // <= 0: a last block of none
+    const int mts = left > 0 ? (left + kRows - 1) / kRows : 0;
+    if (mts == 0) continue;
+    const int ot = (nb * 4 + wave) * kOut;
+    int64_t tile_row[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      int n = ot + i % kOut;
+      n = n < a.N16 ? n : a.N16 - 1;
+      tile_row[i] = ((int64_t)e * kHalves + i / kOut) * a.N16 + n;
+    }
+    // this lane's row of the wave's row tile
+    const int mine = wave * kRows + col;
+    const uint8_t *x0 = static_cast<const uint8_t *>(a.x) + (first + r0) * F::kBytes * a.K;
+    const uint32_t xat = (uint32_t)(mine < left ? mine : left - 1) * a.K + quad * 8;
+    const float *sx0 = FP8 ? a.x_scales + (first + r0) * a.K128 : nullptr;
+    const uint32_t sxat = (uint32_t)(mine < left ? mine : left - 1) * a.K128;
+    typename F::X stage[4];
+    float row_scale = 0.0f;
+    const auto load_x = [&](int kt) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = kt * kTileK + j * 32;
+        stage[j] = typename F::X{};
+        if (GROUP == kTileK || c < a.K) stage[j] = F::load(x0 + (int64_t)c * F::kBytes, xat);
+      }
+      if (FP8) row_scale = (sx0 + kt)[sxat];
+    };
+    const auto stage_x = [&](int buf) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xs[buf][wave][j][lane] = stage[j];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum = F::mul(stage[g * kPer + j], F::ones(), sum);
+        if (!ZEROS) sum *= -F::zero_of(8.0f);
+        if (col == 0) *reinterpret_cast<f32x4 *>(&sums[buf][wave][g][quad * 4]) = sum;
+      }
+      if (FP8 && quad == 0) sxs[buf][wave][col] = row_scale;
+    };
+    u32x4 codes[kTiles];
+    uint16_t scale[kTiles][kGroups];
+    uint8_t zero[kTiles][kGroups];
+    const auto load_w = [&](int kt) {
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+        codes[i] = reinterpret_cast<const u32x4 *>(
+            a.w_codes + (tile_row[i] * a.K128 + kt) * kTileBytes)[lane];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const int gg = kt * kGroups + g < G ? kt * kGroups + g : G - 1;
+          const int64_t at = (tile_row[i] * G + gg) * kTileN;
+          scale[i][g] = (a.w_scales + at)[col];
+          if (ZEROS) zero[i][g] = (a.w_zeros + at)[col];
+        }
+    };
+    // The block with the row tiles it has: all of a step's products are
+    // independent of each other, and its codes turn into numbers beside the
+    // matrix instructions of the step before.
+    const auto block = [&](auto count) {
+      constexpr int kM = decltype(count)::value;
+      f32x4 acc[kM][kTiles];
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) acc[m][i] = f32x4{0, 0, 0, 0};
+      // Past the last piece the last one is read again: no load is under a
+      // branch, after which every earlier load would have to be waited for.
+      const int last = a.K128 - 1;
+      load_x(0);
+      load_w(0);
+      stage_x(0);
+      load_x(last < 1 ? last : 1);
+      for (int kt = 0; kt <= last; ++kt) {
+        const int buf = kt & 1;
+        __syncthreads();  // this piece is in LDS, and the other buffer is free
+        stage_x(buf ^ 1);
+        load_x(kt + 2 < last ? kt + 2 : last);
+        u32x4 raw[kTiles];
+        float s[kTiles][kGroups], z[kTiles][kGroups];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          raw[i] = codes[i];
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            s[i][g] = bf16_to_f32(scale[i][g]) * F::kUnit;
+            z[i][g] = -F::zero_of(ZEROS ? (float)zero[i][g] : 8.0f);
+          }
+        }
+        load_w(kt + 1 < last ? kt + 1 : last);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          if (kGroups > 1 && kt * kGroups + g >= G) break;
+          f32x4 dot[kM][kTiles];
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            typename F::X w[kTiles];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) w[i] = F::codes(raw[i][g * kPer + j]);
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+              const typename F::X x = xs[buf][m][g * kPer + j][lane];
+              f32x4 sum;
+              if (j == 0) sum = *reinterpret_cast<const f32x4 *>(&sums[buf][m][g][quad * 4]);
+#pragma unroll
+              for (int i = 0; i < kTiles; ++i) {
+                if (j == 0) dot[m][i] = ZEROS ? sum * z[i][g] : sum;
+                dot[m][i] = F::mul(x, w[i], dot[m][i]);
+              }
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            f32x4 sx;
+            if (FP8) sx = *reinterpret_cast<const f32x4 *>(&sxs[buf][m][quad * 4]);
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                acc[m][i][v] = __builtin_fmaf(FP8 ? s[i][g] * sx[v] : s[i][g], dot[m][i][v],
+                                              acc[m][i][v]);
+          }
+        }
+      }
+      __syncthreads();  // the buffers are free for the next item
+      uint16_t *out0 = a.out + (first + r0) * a.N + ot * kTileN;
+      // kept here: worked out before the loop over items, the addresses of all
+      // stores would be held (and spilled) through it
+      uint32_t at = (uint32_t)(quad * 4) * a.N + col;
+      int32_t rows_left = left - quad * 4;
+      asm volatile("" : "+v"(at), "+v"(rows_left));
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (m * kRows + v >= rows_left) continue;
+          uint16_t *row = out0 + (int64_t)(m * kRows + v) * a.N;
+#pragma unroll
+          for (int i = 0; i < kOut; ++i) {
+            float y = acc[m][i][v];
+            if (SWIGLU) y = silu(y) * acc[m][kOut + i][v];
+            if ((ot + i) * kTileN + col < a.N) row[at + i * kTileN] = f32_to_bf16(y);
+          }
+        }
+      }
+    };
+    switch (mts) {
+      case 4: block(std::integral_constant<int, 4>{}); break;
+      case 3: block(std::integral_constant<int, 3>{}); break;
+      case 2: block(std::integral_constant<int, 2>{}); break;
+      default: block(std::integral_constant<int, 1>{}); break;
+    }
   }
 }
 
@@ -389,13 +702,25 @@ ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const vo
   a.K128 = (a.K + kTileK - 1) / kTileK;
   with_product(fp8, w4->group, w_zeros != nullptr, w4->swiglu != 0,
                [&](auto p, auto g, auto z, auto s) {
-                 constexpr int kTiles = 4;
+                 // groups of 32: half the tiles, as four scales each leave no room
+                 constexpr int kTiles = g.value == 32 ? 2 : 4;
                  constexpr int kOut = s.value ? kTiles / 2 : kTiles;
                  const dim3 grid((unsigned)((a.N16 + kOut - 1) / kOut),
                                  (unsigned)w4->num_experts);
-                 hipLaunchKernelGGL(
-                     (product_kernel<p.value, g.value, z.value, s.value, kTiles>), grid,
-                     dim3(256), 0, stream, a);
+                 const int64_t hit = capacity < w4->num_experts ? capacity : w4->num_experts;
+                 const int64_t bytes = hit * (s.value ? 2 : 1) * a.N16 * a.K128 * kTileBytes;
+                 if (bytes > kInfinityCache)
+                   hipLaunchKernelGGL(
+                       (product_stream_kernel<p.value, g.value, z.value, s.value, kTiles, true>),
+                       grid, dim3(kStreamWaves * 64), 0, stream, a);
+                 else
+                   hipLaunchKernelGGL(
+                       (product_stream_kernel<p.value, g.value, z.value, s.value, kTiles, false>),
+                       grid, dim3(kStreamWaves * 64), 0, stream, a);
+                 if (capacity > kStreamRows)
+                   hipLaunchKernelGGL((product_tile_kernel<p.value, g.value, z.value, s.value>),
+                                      dim3(kTileGrid), dim3(256), 0, stream, a,
+                                      w4->num_experts);
                });
   return launched("expert product launch");
 }
