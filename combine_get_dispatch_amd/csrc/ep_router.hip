@@ -6,6 +6,7 @@
 // element i of lane l is expert (i / 4) * 4 * LPT + 4 * l + i % 4.  Rows
 // stay in registers from the load to the result.
 #include <hip/hip_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <type_traits>
 #include <stdint.h>
@@ -34,6 +35,9 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float v) {
   return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
+__device__ __forceinline__ float logit_of(float v) { return v; }
+__device__ __forceinline__ float logit_of(uint16_t v) { return bf16_to_f32(v); }
+
 // LDS written by some lanes of a wave and read by others of the same wave: a
 // wave's LDS accesses complete in order, so only the compiler is held.
 __device__ __forceinline__ void wave_sync() {
@@ -47,40 +51,27 @@ __device__ __forceinline__ int expert_of(int l, int i) {
 }
 
 // One lane's part of a row; elements past E are -inf.  vec: rows are aligned
-// to a piece (E % 4 == 0 and an aligned base).
-template <int LPT, int V>
-__device__ __forceinline__ void load_row(const float *row, int E, int l, bool vec, float (&x)[V]) {
+// to a piece (E % 4 == 0 and an aligned base).  Past the end a lane reads the
+// row's last elements, so that no load is under a branch.
+template <int LPT, int V, typename L>
+__device__ __forceinline__ void load_row(const L *row, int E, int l, bool vec, float (&x)[V]) {
+  typedef L Piece __attribute__((ext_vector_type(4)));
 #pragma unroll
   for (int q = 0; q < V / kQuad; ++q) {
     const int e = expert_of<LPT, V>(l, q * kQuad);
+    Piece v;
     if (vec) {
-      f32x4 v = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (e < E) v = *reinterpret_cast<const f32x4 *>(row + e);
-#pragma unroll
-      for (int i = 0; i < kQuad; ++i) x[q * kQuad + i] = v[i];
+      v = *reinterpret_cast<const Piece *>(row + (e < E ? e : E - kQuad));
     } else {
+      // worked out here, not held through a caller's loop
+      int at = e;
+      asm volatile("" : "+v"(at));
 #pragma unroll
-      for (int i = 0; i < kQuad; ++i) x[q * kQuad + i] = e + i < E ? row[e + i] : -INFINITY;
+      for (int i = 0; i < kQuad; ++i) v[i] = row[at + i < E ? at + i : E - 1];
     }
-  }
-}
-
-template <int LPT, int V>
-__device__ __forceinline__ void load_row(const uint16_t *row, int E, int l, bool vec,
-                                         float (&x)[V]) {
 #pragma unroll
-  for (int q = 0; q < V / kQuad; ++q) {
-    const int e = expert_of<LPT, V>(l, q * kQuad);
-    if (vec) {
-      u16x4 v = {0xFF80, 0xFF80, 0xFF80, 0xFF80};
-      if (e < E) v = *reinterpret_cast<const u16x4 *>(row + e);
-#pragma unroll
-      for (int i = 0; i < kQuad; ++i) x[q * kQuad + i] = bf16_to_f32(v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kQuad; ++i)
-        x[q * kQuad + i] = e + i < E ? bf16_to_f32(row[e + i]) : -INFINITY;
-    }
+    for (int i = 0; i < kQuad; ++i)
+      x[q * kQuad + i] = e + i < E ? logit_of(v[i]) : -INFINITY;
   }
 }
 
@@ -119,39 +110,86 @@ __device__ __forceinline__ void store_row(uint16_t *row, int E, int l, bool vec,
   }
 }
 
-__device__ __forceinline__ float logit_at(const float *row, int e) { return row[e]; }
-__device__ __forceinline__ float logit_at(const uint16_t *row, int e) {
-  return bf16_to_f32(row[e]);
+// A value of another lane.  Step s of a reduction over LPT lanes pairs lanes
+// whose groups of 2^s lanes are still apart: inside 16 lanes by data-parallel
+// moves (neighbours, pairs, and mirrors of 8 and of 16 lanes: after the steps
+// before, all lanes of a half hold the same), beyond by a shuffle.
+template <int kStep>
+__device__ __forceinline__ int other_lane(int v) {
+  if constexpr (kStep == 0)
+    return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);
+  else if constexpr (kStep == 1)
+    return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);
+  else if constexpr (kStep == 2)
+    return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);
+  else if constexpr (kStep == 3)
+    return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);
+  else
+    return __shfl_xor(v, 1 << kStep);
+}
+
+template <int kStep>
+__device__ __forceinline__ float other_lane(float v) {
+  return __int_as_float(other_lane<kStep>(__float_as_int(v)));
+}
+
+template <int kStep>
+__device__ __forceinline__ uint32_t other_lane(uint32_t v) {
+  return (uint32_t)other_lane<kStep>((int)v);
+}
+
+template <int kStep>
+__device__ __forceinline__ double other_lane(double v) {
+  return __hiloint2double(other_lane<kStep>(__double2hiint(v)),
+                          other_lane<kStep>(__double2loint(v)));
+}
+
+// Calls f with steps 0, 1, ... of a reduction over LPT lanes.
+template <int LPT, int kStep = 0, typename F>
+__device__ __forceinline__ void each_step(F f) {
+  if constexpr ((1 << kStep) < LPT) {
+    f(std::integral_constant<int, kStep>{});
+    each_step<LPT, kStep + 1>(f);
+  }
 }
 
 // Reductions over the LPT lanes of a token: every lane gets the same result,
 // in a fixed order.
 template <int LPT, typename T>
 __device__ __forceinline__ T token_max(T v) {
-#pragma unroll
-  for (int m = 1; m < LPT; m *= 2) {
-    const T o = __shfl_xor(v, m);
+  each_step<LPT>([&](auto s) {
+    const T o = other_lane<s.value>(v);
     v = o > v ? o : v;
-  }
+  });
+  return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_max(float v) {
+  each_step<LPT>([&](auto s) { v = fmaxf(v, other_lane<s.value>(v)); });
   return v;
 }
 
 template <int LPT, typename T>
 __device__ __forceinline__ T token_sum(T v) {
-#pragma unroll
-  for (int m = 1; m < LPT; m *= 2) v += __shfl_xor(v, m);
+  each_step<LPT>([&](auto s) { v += other_lane<s.value>(v); });
   return v;
 }
 
 template <int LPT>
 __device__ __forceinline__ int token_or(int v) {
-#pragma unroll
-  for (int m = 1; m < LPT; m *= 2) v |= __shfl_xor(v, m);
+  each_step<LPT>([&](auto s) { v |= other_lane<s.value>(v); });
   return v;
 }
 
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+
+// exp of every score of a row: the hardware's exp2 of x log2(e), off by
+// (|x| + 3) 2^-24 of it.
+__device__ __forceinline__ float exp_fast(float v) {
+  return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f);
+}
 
 // sigmoid(x) / exp(m) with m = min(0, the largest x in play), so that scores
 // whose largest would underflow keep their ratios: for x <= 0,
@@ -160,6 +198,19 @@ __device__ __forceinline__ float sigmoid_over(float x, float m) {
   const float t = exp_of(-fabsf(x));
   const float num = x > 0.0f ? 1.0f : (m == 0.0f ? t : exp_of(x - m));
   return num / (1.0f + t);
+}
+
+// The sigmoid for every score of a row: exp overflows to inf and the quotient
+// to 0 below -88.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x));
+}
+
+// sigmoid_over for every score of a row.
+__device__ __forceinline__ float sigmoid_over_fast(float x, float m) {
+  const float t = exp_fast(-fabsf(x));
+  const float num = x > 0.0f ? 1.0f : exp_fast(x - m);
+  return num * __builtin_amdgcn_rcpf(1.0f + t);
 }
 
 template <typename K>
@@ -177,244 +228,659 @@ struct RouteArgs {
   int32_t *status;
   int64_t T;
   int32_t E, k, G, group_size, topk_groups, group_topn;
+  int32_t group_steps;  // log2(group_size / 4) for keep_even_groups, -1: keep_groups
   uint32_t group_inv;  // ceil(2^22 / group_size): e / group_size = e * group_inv >> 22
-  bool softmax, normalize, by_logit, vec;
+  bool softmax, normalize, vec;
   float scale;
 };
 
-// Groups of one token kept by its keys, as 64 bits.  Lane l reads the keys
-// of groups l, l + LPT, ... from LDS.  near: a kept and a dropped group are
-// within `margin` of each other.
-template <typename K, int LPT, int V>
-__device__ __forceinline__ uint64_t kept_groups(const RouteArgs &a, const K (&key)[V], int l,
-                                                K *row, K *group_key, K margin, bool *near) {
+// The two best of a set, as the set grows.
+template <typename K>
+struct Best2 {
+  K first, second;
+  __device__ __forceinline__ void add(K v) {
+    second = v > first ? first : (v > second ? v : second);
+    first = v > first ? v : first;
+  }
+  template <int kStep>
+  __device__ __forceinline__ void join() {
+    const K a = other_lane<kStep>(first), b = other_lane<kStep>(second);
+    const K low = a < first ? a : first, high = b > second ? b : second;
+    first = a > first ? a : first;
+    second = low > high ? low : high;
+  }
+  __device__ __forceinline__ K key(int topn) const {
+    return topn == 2 && second > K(-INFINITY) ? first + second : first;
+  }
+};
+
+// In 32 bits by the median of three (no NaN gets here).
+template <>
+struct Best2<float> {
+  float first, second;
+  __device__ __forceinline__ void add(float v) {
+    second = __builtin_amdgcn_fmed3f(first, second, v);
+    first = fmaxf(first, v);
+  }
+  template <int kStep>
+  __device__ __forceinline__ void join() {
+    const float a = other_lane<kStep>(first), b = other_lane<kStep>(second);
+    second = fmaxf(fminf(first, a), fmaxf(second, b));
+    first = fmaxf(first, a);
+  }
+  __device__ __forceinline__ float key(int topn) const {
+    return topn == 2 && second > -INFINITY ? first + second : first;
+  }
+};
+
+// The groups kept, as 64 bits, from the group keys in LDS (written by lanes of
+// this token, and read here after the wave has met).  Lane l ranks groups
+// l, l + LPT, ...; near: a kept and a dropped group are within `margin`.
+template <typename K, int LPT>
+__device__ __forceinline__ uint64_t kept_of(const RouteArgs &a, int l, K *group_key,
+                                            K margin, bool *near) {
   const K none = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = expert_of<LPT, V>(l, i);
-    if (e < a.E) row[e] = key[i];
-  }
+  if (l < (-a.G & 3)) group_key[a.G + l] = none;
   wave_sync();
-  for (int g = l; g < a.G; g += LPT) {
-    K best = none, second = none;
-    for (int i = 0; i < a.group_size; ++i) {
-      const K v = row[g * a.group_size + i];
-      second = v > best ? best : (v > second ? v : second);
-      best = v > best ? v : best;
-    }
-    group_key[g] = a.group_topn == 2 && second > none ? best + second : best;
-  }
-  wave_sync();
-  uint64_t kept = 0;
+  uint32_t kept[2] = {0, 0};
   K low = INFINITY, high = none;  // worst kept, best dropped
-  for (int g = 0; g < a.G; ++g) {
+  for (int g = l; g < a.G; g += LPT) {
     const K v = group_key[g];
-    int before = 0;
-    for (int h = 0; h < a.G; ++h) {
-      const K o = group_key[h];
-      before += o > v || (o == v && h < g);
-    }
     if (!(v > none)) continue;
+    int before = 0;
+    for (int h = 0; h < a.G; h += 4) {  // the keys are filled up to fours
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const K o = group_key[h + i];
+        before += o > v || (o == v && h + i < g);
+      }
+    }
     if (before < a.topk_groups) {
-      kept |= uint64_t{1} << g;
+      kept[g / 32] |= 1u << (g % 32);
       low = v < low ? v : low;
     } else {
       high = v > high ? v : high;
     }
   }
-  wave_sync();
-  if (near != nullptr && high > none && !(low - high > margin)) *near = true;
-  return kept;
+  if (near != nullptr) {
+    low = -token_max<LPT>(-low);
+    high = token_max<LPT>(high);
+    if (high > none && !(low - high > margin)) *near = true;
+  }
+  const uint32_t lo = token_or<LPT>((int)kept[0]);
+  const uint32_t hi = a.G > 32 ? token_or<LPT>((int)kept[1]) : 0;
+  return (uint64_t)hi << 32 | lo;
 }
 
-// The k best of one token's keys, in order; slot j is given to lane j % LPT
-// as its mine[j / LPT].  A key of -inf is never selected.  near: two
-// neighbours in the order, the first one not selected among them, are within
-// `margin`.
-template <typename K, int LPT, int V>
-__device__ __forceinline__ void best_experts(const RouteArgs &a, K (&key)[V], int l,
-                                             int (&mine)[2], K margin, bool *near) {
-  const K none = -INFINITY;
-  mine[0] = mine[1] = -1;
-  K last = INFINITY;
-  const int rounds = near != nullptr ? a.k + 1 : a.k;
-  for (int j = 0; j < rounds; ++j) {
-    K best = none;
+// Drops the keys of the groups that are not kept.  Groups of any size: each is
+// gathered from the lanes by itself.
+template <int LPT, int V>
+__device__ __forceinline__ void keep_groups(const RouteArgs &a, float (&key)[V], int l,
+                                            float *group_key, float margin, bool *near) {
+  const float none = -INFINITY;
+  for (int g = 0; g < a.G; ++g) {
+    Best2<float> best = {none, none};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = expert_of<LPT, V>(l, i) - g * a.group_size;
+      best.add(e >= 0 && e < a.group_size ? key[i] : none);
+    }
+    each_step<LPT>([&](auto s) { best.template join<s.value>(); });
+    if (l == 0) group_key[g] = best.key(a.group_topn);
+  }
+  const uint64_t kept = kept_of<float, LPT>(a, l, group_key, margin, near);
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int g = (int)(((uint32_t)expert_of<LPT, V>(l, i) * a.group_inv) >> 22);
+    if (g >= 64 || !((kept >> g) & 1)) key[i] = none;
+  }
+}
+
+// The same for groups of 2^n pieces of four experts that lie within one piece
+// per lane (a.group_steps = n): all groups of a piece at once, by n steps
+// between lanes.  256 experts in 8 groups: 100 instructions instead of 800.
+template <int LPT, int V>
+__device__ __forceinline__ void keep_even_groups(const RouteArgs &a, float (&key)[V], int l,
+                                                 float *group_key, float margin, bool *near) {
+  const float none = -INFINITY;
+  Best2<float> best[V / kQuad];
+#pragma unroll
+  for (int q = 0; q < V / kQuad; ++q) {
+    best[q] = {key[q * kQuad], none};
+#pragma unroll
+    for (int i = 1; i < kQuad; ++i) best[q].add(key[q * kQuad + i]);
+  }
+  each_step<LPT>([&](auto s) {
+    if (s.value < a.group_steps) {
+#pragma unroll
+      for (int q = 0; q < V / kQuad; ++q) best[q].template join<s.value>();
+    }
+  });
+  const bool leader = (l & ((1 << a.group_steps) - 1)) == 0;
+#pragma unroll
+  for (int q = 0; q < V / kQuad; ++q) {
+    const int g = (q * LPT + l) >> a.group_steps;
+    if (leader && g < a.G) group_key[g] = best[q].key(a.group_topn);
+  }
+  const uint64_t kept = kept_of<float, LPT>(a, l, group_key, margin, near);
+  wave_sync();
+#pragma unroll
+  for (int q = 0; q < V / kQuad; ++q) {
+    const int g = (q * LPT + l) >> a.group_steps;
+    if (g >= 64 || !((kept >> g) & 1)) {
+#pragma unroll
+      for (int i = 0; i < kQuad; ++i) key[q * kQuad + i] = none;
+    }
+  }
+}
+
+// The k best of one token's keys, in order, by k rounds of a search; slot j is
+// given to lane j % LPT as its mine[j / LPT].  A key of -inf is never selected.
+// near (kCheck): two neighbours in the order, the first one not selected
+// among them, are within `margin`.
+template <int LPT, int V, bool kCheck>
+__device__ __forceinline__ void best_by_rounds(const RouteArgs &a, float (&key)[V], int l,
+                                               int (&mine)[32 / (LPT < 32 ? LPT : 32)],
+                                               float margin, bool *near) {
+  const float none = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < 32 / (LPT < 32 ? LPT : 32); ++s) mine[s] = -1;
+  float last = INFINITY;
+#pragma unroll 1
+  for (int j = 0; j < (kCheck ? a.k + 1 : a.k); ++j) {
+    float best = none;
     int at = 1 << 20;
 #pragma unroll
-    for (int i = 0; i < V; ++i)  // experts ascend with i: the first of equals stays
-      if (key[i] > best) {
-        best = key[i];
-        at = expert_of<LPT, V>(l, i);
-      }
-#pragma unroll
-    for (int m = 1; m < LPT; m *= 2) {
-      const K o = __shfl_xor(best, m);
-      const int oat = __shfl_xor(at, m);
-      if (o > best || (o == best && oat < at)) {
-        best = o;
-        at = oat;
-      }
+    for (int i = 0; i < V; ++i) {  // experts ascend with i: the first of equals stays
+      at = key[i] > best ? expert_of<LPT, V>(l, i) : at;
+      best = key[i] > best ? key[i] : best;
     }
+    each_step<LPT>([&](auto s) {
+      const float o = other_lane<s.value>(best);
+      const int oat = other_lane<s.value>(at);
+      const bool take = o > best || (o == best && oat < at);
+      best = take ? o : best;
+      at = take ? oat : at;
+    });
     if (!(best > none)) break;
-    if (near != nullptr && !(last - best > margin)) *near = true;
+    if (kCheck && !(last - best > margin)) *near = true;
     last = best;
-    if (j < a.k && j % LPT == l) mine[j / LPT] = at;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (expert_of<LPT, V>(l, i) == at) key[i] = none;
+    for (int s = 0; s < 32 / (LPT < 32 ? LPT : 32); ++s)
+      if (j < a.k && j == s * LPT + l) mine[s] = at;
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = expert_of<LPT, V>(l, i) == at ? none : key[i];
   }
 }
 
-// Selection by keys of type K.
-template <typename K, int LPT, int V>
-__device__ __forceinline__ void select(const RouteArgs &a, K (&key)[V], int l, char *lds_row,
-                                       int (&mine)[2], K margin, bool *near) {
-  if (a.G > 1) {
-    K *row = reinterpret_cast<K *>(lds_row);
-    const uint64_t kept = kept_groups<K, LPT, V>(a, key, l, row, row + LPT * V, margin, near);
+// The front bits of a fp32 key, ordered as whole numbers, and its expert in the
+// last bits, so that one maximum moves both and the lowest expert is the
+// greatest of equals.  0: a key of -inf.
+template <int kBits>
+__device__ __forceinline__ uint32_t pack_key(float key, int e) {
+  constexpr uint32_t kMask = (1u << kBits) - 1;
+  const uint32_t u = __float_as_uint(key + 0.0f);  // -0 as +0
+  const uint32_t ordered = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  const uint32_t p = (ordered & ~kMask) | ((uint32_t)e ^ kMask);
+  return key > -INFINITY ? p : 0u;
+}
+
+template <int kBits>
+__device__ __forceinline__ int expert_in(uint32_t p) {
+  constexpr uint32_t kMask = (1u << kBits) - 1;
+  return p == 0 ? -1 : (int)((p & kMask) ^ kMask);
+}
+
+// The least (low) or the greatest key with these front bits.
+template <int kBits>
+__device__ __forceinline__ float key_in(uint32_t p, bool low) {
+  constexpr uint32_t kMask = (1u << kBits) - 1;
+  const uint32_t o = low ? p & ~kMask : p | kMask;
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+__device__ __forceinline__ void order(uint32_t &a, uint32_t &b) {
+  const uint32_t high = umax(a, b);
+  b = umin(a, b);
+  a = high;
+}
+
+constexpr int kList = 8;
+
+// Sorts a list that first rises or falls and then does the other; descending.
+__device__ __forceinline__ void sort_bitonic(uint32_t (&v)[kList]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int g = (int)(((uint32_t)expert_of<LPT, V>(l, i) * a.group_inv) >> 22);
-      if (g >= 64 || !((kept >> g) & 1)) key[i] = -INFINITY;
+  for (int d = kList / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int i = 0; i < kList; ++i)
+      if ((i & d) == 0) order(v[i], v[i + d]);
+}
+
+__device__ __forceinline__ void sort4(uint32_t *v) {
+  order(v[0], v[1]);
+  order(v[2], v[3]);
+  order(v[0], v[2]);
+  order(v[1], v[3]);
+  order(v[1], v[2]);
+}
+
+// 19 comparisons, the fewest for eight values.
+__device__ __forceinline__ void sort8(uint32_t *v) {
+  order(v[0], v[2]); order(v[1], v[3]); order(v[4], v[6]); order(v[5], v[7]);
+  order(v[0], v[4]); order(v[1], v[5]); order(v[2], v[6]); order(v[3], v[7]);
+  order(v[0], v[1]); order(v[2], v[3]); order(v[4], v[5]); order(v[6], v[7]);
+  order(v[2], v[4]); order(v[3], v[5]);
+  order(v[1], v[4]); order(v[3], v[6]);
+  order(v[1], v[2]); order(v[3], v[4]); order(v[5], v[6]);
+}
+
+// The eight best of one token's packed keys, in order, in every lane.  Each
+// lane sorts its own; joining two sorted lists of eight keeps the greater of
+// a[i] and b[7 - i], which are the eight best and rise and fall once.
+template <int LPT, int V>
+__device__ __forceinline__ void best_eight(uint32_t (&v)[V], uint32_t (&list)[kList]) {
+  if constexpr (V == 4) {
+    sort4(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      list[i] = v[i];
+      list[7 - i] = other_lane<0>(v[i]);
+    }
+    sort_bitonic(list);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += kList) sort8(v + i);
+#pragma unroll
+    for (int i = 0; i < kList; ++i) list[i] = v[i];
+#pragma unroll
+    for (int n = kList; n < V; n += kList) {
+#pragma unroll
+      for (int i = 0; i < kList; ++i) list[i] = umax(list[i], v[n + 7 - i]);
+      sort_bitonic(list);
     }
   }
-  best_experts<K, LPT, V>(a, key, l, mine, margin, near);
+  each_step<LPT>([&](auto s) {
+    if constexpr (V > 4 || s.value > 0) {  // V == 4: step 0 is done above
+      uint32_t joined[kList];
+#pragma unroll
+      for (int i = 0; i < kList; ++i) joined[i] = umax(list[i], other_lane<s.value>(list[7 - i]));
+#pragma unroll
+      for (int i = 0; i < kList; ++i) list[i] = joined[i];
+      sort_bitonic(list);
+    }
+  });
 }
 
-// Keys s + b of one lane's experts (key of a logit of -inf: -inf).
-template <typename K, int LPT, int V>
-__device__ __forceinline__ void score_keys(const RouteArgs &a, const float (&x)[V], int l,
-                                           float xmax, K (&key)[V], K *best_score) {
-  K sum = 0;
-  if (a.softmax) {
+// What a route kernel's keys are.
+constexpr int kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2;
+
+// Keys s + b of one lane's experts (key of a logit of -inf: -inf), and the
+// best score there can be: 1, or a softmax's.
+template <int LPT, int V, int kMode>
+__device__ __forceinline__ float score_keys(const float (&x)[V], float xmax, const float *bias,
+                                            int l, float (&key)[V]) {
+  float best = 1.0f;
+  if (kMode == kBySoftmax) {
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      key[i] = exp_of(K(x[i]) - K(xmax));
+      key[i] = exp_fast(x[i] - xmax);
       sum += key[i];
     }
-    sum = token_sum<LPT>(sum);
-    *best_score = K(1) / sum;
+    best = 1.0f / token_sum<LPT>(sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] *= best;
   } else {
-    *best_score = sigmoid_of(K(xmax));
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = sigmoid_fast(x[i]);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = expert_of<LPT, V>(l, i);
-    K s = a.softmax ? key[i] / sum : sigmoid_of(K(x[i]));
-    if (a.bias != nullptr && e < a.E) s += K(a.bias[e]);
-    key[i] = x[i] > -INFINITY ? s : K(-INFINITY);
+  for (int q = 0; q < V; q += kQuad) {
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(bias + expert_of<LPT, V>(l, q));
+#pragma unroll
+    for (int i = q; i < q + kQuad; ++i) key[i] = x[i] > -INFINITY ? key[i] + b[i % kQuad] : -INFINITY;
   }
+  return best;
 }
 
-// One token per LPT lanes.  Bound by the k rounds of the search, not by the
-// logits it reads.  Keys other than logits are computed in 32 bits first;
-// where neighbours in the order are within 2^-19 of the best score and key the
-// token's keys and order are computed again in 64.  (A score is off by at most
-// 2^-21.5 of the best, its sum with the bias by 2^-24 of the key; two sums of
-// two keys by four times that.)
-template <typename L, int LPT, int V>
+// The selection of one token with keys in 64 bits, by the whole wave: the path
+// of the few tokens whose groups (or more than 32 keys) are within the margin.
+// keys: LDS of E doubles, group_key of 64; expert j of the selection is given
+// to lane j as the result, -1 if there is none.  One token alone would leave
+// most of its wave idle for 20 us, which a short launch then waits for; by the
+// whole wave it is 3.
+template <typename L, int kMode>
+__device__ __forceinline__ int select_exactly(const RouteArgs &a, const L *row, float xmax,
+                                              double *keys, double *group_key) {
+  const double none = -INFINITY;
+  const int lane = threadIdx.x % 64;
+  double sum = 0.0;
+  if constexpr (kMode == kBySoftmax) {
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) sum += exp((double)logit_of(row[e]) - (double)xmax);
+    sum = token_sum<64>(sum);
+  }
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    double v = logit_of(row[e]);
+    if (v > none) {
+      v = kMode == kBySoftmax ? exp(v - (double)xmax) / sum : sigmoid_of(v);
+      if (a.bias != nullptr) v += (double)a.bias[e];
+    }
+    keys[e] = v;
+  }
+  wave_sync();
+  uint64_t kept = ~uint64_t{0};
+  if (a.G > 1) {
+    Best2<double> best = {none, none};
+    if (lane < a.G) {
+#pragma unroll 1
+      for (int i = 0; i < a.group_size; ++i) best.add(keys[lane * a.group_size + i]);
+    }
+    const double own = best.key(a.group_topn);
+    group_key[lane] = own;
+    wave_sync();
+    int before = 0;
+#pragma unroll 1
+    for (int h = 0; h < a.G; ++h)
+      before += group_key[h] > own || (group_key[h] == own && h < lane);
+    kept = __ballot(lane < a.G && own > none && before < a.topk_groups);
+  }
+  int mine = -1;
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    double best = none;
+    int at = 1 << 20;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {  // ascending: the first of equals stays
+      const int g = a.G > 1 ? (int)(((uint32_t)e * a.group_inv) >> 22) : 0;
+      const double v = (kept >> g) & 1 ? keys[e] : none;
+      at = v > best ? e : at;
+      best = v > best ? v : best;
+    }
+    each_step<64>([&](auto s) {
+      const double o = other_lane<s.value>(best);
+      const int oat = other_lane<s.value>(at);
+      const bool take = o > best || (o == best && oat < at);
+      best = take ? o : best;
+      at = take ? oat : at;
+    });
+    if (!(best > none)) break;
+    if (lane == j) mine = at;
+    if (lane == at % 64) keys[at] = none;
+    wave_sync();
+  }
+  wave_sync();
+  return mine;
+}
+
+// The order of the keys at or above `least`, in 64 bits: at most 32 of them,
+// a lane works out one or a few and ranks it among the others.  `own` is the
+// token's LDS: 32 doubles, then 2 x 32 integers.  False: there are more.
+// Written for few instructions (loops stay loops): a path that is taken now
+// and then waits for its own code to be fetched, which measured several times
+// what the code then takes.
+template <typename L, int LPT, int V, int kMode>
+__device__ __forceinline__ bool order_exactly(const RouteArgs &a, const L *row,
+                                              const float (&key)[V], int l, float xmax,
+                                              float least, double *own,
+                                              int (&mine)[32 / (LPT < 32 ? LPT : 32)]) {
+  constexpr int kMost = 32;
+  int *expert = reinterpret_cast<int *>(own + kMost), *slot = expert + kMost;
+  uint32_t in = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) in |= key[i] >= least ? 1u << i : 0u;
+  const int count = __popc(in);
+  int at = count;  // of this lane's among the token's: the lanes' counts before it
+#pragma unroll 1
+  for (int d = 1; d < LPT; d *= 2) {
+    const int before = __shfl_up(at, d, LPT);
+    at += l >= d ? before : 0;
+  }
+  const int n = __shfl(at, LPT - 1, LPT);
+  if (n > kMost) return false;
+  at -= count;
+#pragma unroll 1
+  for (; in != 0; in &= in - 1) expert[at++] = expert_of<LPT, V>(l, __ffs(in) - 1);
+  double sum = 0.0;
+  if constexpr (kMode == kBySoftmax) {
+#pragma unroll 1
+    for (int e = l; e < a.E; e += LPT) sum += exp((double)logit_of(row[e]) - (double)xmax);
+    sum = token_sum<LPT>(sum);
+  }
+  wave_sync();
+#pragma unroll 1
+  for (int c = l; c < kMost; c += LPT) {
+    slot[c] = -1;
+    if (c >= n) continue;
+    const int e = expert[c];
+    double v = logit_of(row[e]);
+    if constexpr (kMode == kBySoftmax) v = exp(v - (double)xmax) / sum;
+    if constexpr (kMode == kBySigmoid) v = sigmoid_of(v);
+    if (kMode != kByLogit && a.bias != nullptr) v += (double)a.bias[e];
+    own[c] = v;
+  }
+  wave_sync();
+#pragma unroll 1
+  for (int c = l; c < n; c += LPT) {
+    const double v = own[c];
+    const int e = expert[c];
+    int before = 0;
+#pragma unroll 1
+    for (int h = 0; h < n; ++h) before += own[h] > v || (own[h] == v && expert[h] < e);
+    slot[before] = e;
+  }
+  wave_sync();
+#pragma unroll
+  for (int s = 0; s < 32 / (LPT < 32 ? LPT : 32); ++s) {
+    const int c = s * LPT + l;
+    mine[s] = c < a.k && c < kMost ? slot[c] : -1;
+  }
+  wave_sync();
+  return true;
+}
+
+// One token per LPT lanes, several tokens in turn: the next row is loaded
+// before the present one is worked on.  Bound by the instructions of the
+// search, not by the logits it reads, so it goes in steps, each for what the
+// one before left open:
+//   kShort (k <= 8): sorted lists of eight keys cut to their front bits.
+//     Neighbours that the cut bits (or, for keys that are scores, the margin
+//     below) cannot tell apart leave the token open, about three in a hundred;
+//     the few keys in question are then ordered in 64 bits (order_exactly).
+//   k > 8 (and more than 32 keys in question): k rounds of a search over the
+//     32-bit keys.
+//   Groups, or neighbours of that search, within the margin: all of the token's
+//     keys and groups in 64 bits (select_exactly).
+// The margin is 2^-19 of the best score and key there can be: a score is off
+// by at most 2^-21 of the best, its sum with the bias by 2^-24 of the key, two
+// sums of two keys by four times that.  bf16 logits are whole within the front
+// bits: equal means equal.
+template <typename L, int LPT, int V, int kMode, bool kShort>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   constexpr int kTokens = kThreads / LPT;
-  __shared__ __align__(16) char lds[kTokens * (LPT * V + EP_MAX_GROUPS) * sizeof(double)];
-  const int l = threadIdx.x % LPT;
+  constexpr int kSlots = 32 / (LPT < 32 ? LPT : 32);
+  constexpr int kBits = LPT * V <= 32 ? 5 : LPT * V <= 64 ? 6 : LPT * V <= 128 ? 7
+                      : LPT * V <= 256 ? 8 : LPT * V <= 512 ? 9 : 10;
+  constexpr bool kScores = kMode != kByLogit;
+  __shared__ double group_keys[kTokens][EP_MAX_GROUPS];
+  __shared__ double rows[kScores ? kThreads / 64 : 1][kScores ? LPT * V : 1];
+  __shared__ float biases[kScores ? LPT * V : 1];
+  int l = threadIdx.x % LPT;
   const int slot = threadIdx.x / LPT;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
-  char *lds_row = lds + slot * (LPT * V + EP_MAX_GROUPS) * sizeof(double);
-  const bool live = t < a.T;
-  const bool on = live && (a.token_mask == nullptr || a.token_mask[t] != 0);
-  const L *row = static_cast<const L *>(a.logits) + (live ? t : 0) * a.E;
-  float x[V];
-  if (on) {
-    load_row<LPT, V>(row, a.E, l, a.vec, x);
-  } else {
+  double *group_key = group_keys[slot];
+  const int64_t stride = (int64_t)gridDim.x * kTokens;
+  float bias_size = 0.0f;
+  int bias_bad = 0;
+  if constexpr (kScores) {
+    for (int e = threadIdx.x; e < LPT * V; e += kThreads)
+      biases[e] = a.bias != nullptr && e < a.E ? a.bias[e] : 0.0f;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = -INFINITY;
+    for (int i = 0; i < V; ++i) {
+      const float b = biases[expert_of<LPT, V>(l, i)];
+      bias_bad |= !(b < INFINITY);
+      bias_size = fmaxf(bias_size, b > -INFINITY ? fabsf(b) : 0.0f);
+    }
+    bias_bad = token_or<LPT>(bias_bad);
+    bias_size = token_max<LPT>(bias_size);
   }
-  float xmax = -INFINITY;
-  int bad = 0;
+  const L *logits = static_cast<const L *>(a.logits);
+  // the first token of the wave, and this lane's: the whole wave stays in the
+  // loop until none of its tokens is left
+  int64_t first = (int64_t)blockIdx.x * kTokens + threadIdx.x / 64 * (64 / LPT);
+  const int in_wave = (int)(threadIdx.x % 64) / LPT;
+  float next[V];
+  bool next_on = false;
+  const auto load = [&](int64_t n) {
+    next_on = n < a.T && (a.token_mask == nullptr || a.token_mask[n] != 0);
+    load_row<LPT, V>(logits + (n < a.T ? n : a.T - 1) * a.E, a.E, l, a.vec, next);
+  };
+  load(first + in_wave);
+  for (; first < a.T; first += stride) {
+    const int64_t t = first + in_wave;
+    // the experts of a lane are a few additions: worked out before the loop,
+    // their numbers would fill the registers through it
+    asm volatile("" : "+v"(l));
+    const L *row = logits + (t < a.T ? t : a.T - 1) * a.E;
+    float x[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bad |= !(x[i] < INFINITY);
-    xmax = fmaxf(xmax, x[i]);
-  }
-  bad = token_or<LPT>(bad);
-  xmax = token_max<LPT>(xmax);
-  int mine[2] = {-1, -1};
-  if (!bad && xmax > -INFINITY) {
-    float key[V];
-    if (a.by_logit) {
+    for (int i = 0; i < V; ++i) x[i] = next_on ? next[i] : -INFINITY;
+    load(t + stride);
+    float xmax = -INFINITY;
+    int bad = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      bad |= !(x[i] < INFINITY);
+      xmax = fmaxf(xmax, x[i]);
+    }
+    xmax = token_max<LPT>(xmax);
+    float key[V], margin = 0.0f;
+    if constexpr (kScores) {
+      // a row of -inf has no scores: any finite value for its maximum
+      const float best =
+          score_keys<LPT, V, kMode>(x, xmax > -INFINITY ? xmax : 0.0f, biases, l, key);
+      margin = 0x1p-19f * (2.0f * best + bias_size);  // no key is larger than best + bias_size
+      if (bias_bad) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) bad |= !(key[i] < INFINITY);
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = x[i];
-      select<float, LPT, V>(a, key, l, lds_row, mine, 0.0f, nullptr);
-    } else {
-      float best_score;
-      score_keys<float, LPT, V>(a, x, l, xmax, key, &best_score);
-      float size = 0.0f;
+    }
+    bad = token_or<LPT>(bad);
+    if (bad) {  // no expert can be selected
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        bad |= !(key[i] < INFINITY);
-        if (key[i] > -INFINITY) size = fmaxf(size, fabsf(key[i]));
+      for (int i = 0; i < V; ++i) key[i] = -INFINITY;
+    }
+    // the weights' denominator where it is not that of the slots; the row's
+    // registers end here
+    float row_sum = 0.0f;
+    if (kMode != kBySigmoid && a.softmax && !a.normalize) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) row_sum += exp_fast(x[i] - xmax);
+      row_sum = token_sum<LPT>(row_sum);
+    }
+    bool open = false, near = false;
+    if (a.G > 1) {
+      float *gk = reinterpret_cast<float *>(group_key);
+      if (a.group_steps >= 0)
+        keep_even_groups<LPT, V>(a, key, l, gk, margin, kScores ? &near : nullptr);
+      else
+        keep_groups<LPT, V>(a, key, l, gk, margin, kScores ? &near : nullptr);
+    }
+    int mine[kSlots];
+    if constexpr (kShort) {
+      uint32_t packed[V], list[kList], after = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) packed[i] = pack_key<kBits>(key[i], expert_of<LPT, V>(l, i));
+      best_eight<LPT, V>(packed, list);
+      uint32_t own = 0;
+#pragma unroll
+      for (int j = 0; j < kList; ++j) {
+        own = l == j ? list[j] : own;
+        if (j + 1 < kList) after = l == j ? list[j + 1] : after;
       }
-      bad = token_or<LPT>(bad);
-      if (!bad) {
-        size = token_max<LPT>(size);
-        bool near = false;
-        const float margin = 0x1p-19f * (best_score + size);
-        select<float, LPT, V>(a, key, l, lds_row, mine, margin, &near);
-        if (near) {
-          double exact[V], best;
-          score_keys<double, LPT, V>(a, x, l, xmax, exact, &best);
-          select<double, LPT, V>(a, exact, l, lds_row, mine, 0.0, nullptr);
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        mine[s] = s == 0 && l < a.k ? expert_in<kBits>(own) : -1;
+      if constexpr (kScores || sizeof(L) == 4) {
+        // own against the next in the order; after the eighth, any other key that
+        // is not clearly below it
+        if (l < a.k && l + 1 < kList && own != 0 && after != 0)
+          open = !(key_in<kBits>(own, true) - key_in<kBits>(after, false) > margin);
+        uint32_t kth = list[0];
+#pragma unroll
+        for (int j = 1; j < kList; ++j) kth = j < a.k ? list[j] : kth;
+        const float least = kth != 0 ? key_in<kBits>(kth, true) - margin : -FLT_MAX;
+        if (a.k == kList) {
+          int above = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) above += key[i] >= least ? 1 : 0;
+          if (kth != 0 && token_sum<LPT>(above) > kList) open = true;
+        }
+        open = token_or<LPT>(open) != 0;
+        if (open)
+          open = !order_exactly<L, LPT, V, kMode>(a, row, key, l, xmax, least, group_key, mine);
+      }
+    }
+    if constexpr (kShort && kScores)
+      near = near || open;
+    else if (!kShort || open)
+      best_by_rounds<LPT, V, kScores>(a, key, l, mine, margin, &near);
+    if constexpr (kScores) {
+      for (uint64_t todo = __ballot(near && l == 0 && !bad); todo != 0; todo &= todo - 1) {
+        const int from = __ffsll((unsigned long long)todo) - 1;
+        const int64_t n = first + from / LPT;
+        const int e = select_exactly<L, kMode>(a, logits + n * a.E, __shfl(xmax, from),
+                                               rows[threadIdx.x / 64],
+                                               group_keys[threadIdx.x / 64 * (64 / LPT)]);
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+          const int got = __shfl(e, s * LPT + l);
+          if (in_wave == from / LPT) mine[s] = got;
         }
       }
     }
-  }
-  if (!live) return;
-  if (bad) {
-    mine[0] = mine[1] = -1;
-    if (l == 0) atomicOr(a.status, EP_STATUS_BIT_NONFINITE);
-  }
-  // Weights from the selected logits, relative to the largest in play.
-  float sx[2];
-  float smax = -INFINITY;
+    if (bad && l == 0) atomicOr(a.status, EP_STATUS_BIT_NONFINITE);
+    // Weights from the selected logits, relative to the largest in play.
+    float sx[kSlots], w[kSlots], smax = -INFINITY, total = 1.0f;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    sx[j] = mine[j] >= 0 ? logit_at(row, mine[j]) : -INFINITY;
-    smax = fmaxf(smax, sx[j]);
-  }
-  smax = token_max<LPT>(smax);
-  float w[2], total;
-  if (a.softmax) {
-    const float top = a.normalize ? smax : xmax;
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      w[j] = mine[j] >= 0 ? exp_of(sx[j] - top) : 0.0f;
-      sum += w[j];
+    for (int s = 0; s < kSlots; ++s) {
+      sx[s] = mine[s] >= 0 ? logit_of(row[mine[s] >= 0 ? mine[s] : 0]) : -INFINITY;
+      smax = fmaxf(smax, sx[s]);
     }
-    if (!a.normalize) {
-      sum = 0.0f;
+    if (a.softmax) {
+      const float top = a.normalize ? token_max<LPT>(smax) : xmax;
+      float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += xmax > -INFINITY ? exp_of(x[i] - xmax) : 0.0f;
+      for (int s = 0; s < kSlots; ++s) {
+        w[s] = mine[s] >= 0 ? exp_of(sx[s] - top) : 0.0f;
+        sum += w[s];
+      }
+      total = a.normalize ? token_sum<LPT>(sum) : row_sum;
+    } else {
+      const float m = a.normalize ? fminf(token_max<LPT>(smax), 0.0f) : 0.0f;
+      float sum = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s) {
+        w[s] = mine[s] >= 0 ? sigmoid_over(sx[s], m) : 0.0f;
+        sum += w[s];
+      }
+      if (a.normalize) total = token_sum<LPT>(sum);
     }
-    total = token_sum<LPT>(sum);
-  } else {
-    const float m = a.normalize ? fminf(smax, 0.0f) : 0.0f;
-    float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      w[j] = mine[j] >= 0 ? sigmoid_over(sx[j], m) : 0.0f;
-      sum += w[j];
-    }
-    total = a.normalize ? token_sum<LPT>(sum) : 1.0f;
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int at = j * LPT + l;
-    if (at < a.k) {
-      a.topk_idx[t * a.k + at] = mine[j];
-      a.topk_weights[t * a.k + at] = mine[j] >= 0 ? a.scale * (w[j] / total) : 0.0f;
+    for (int s = 0; s < kSlots; ++s) {
+      const int at = s * LPT + l;
+      if (at < a.k && t < a.T) {
+        a.topk_idx[t * a.k + at] = mine[s];
+        a.topk_weights[t * a.k + at] = mine[s] >= 0 ? a.scale * (w[s] / total) : 0.0f;
+      }
     }
   }
 }
@@ -650,10 +1116,11 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
   if (t >= a.T) return;
   float *own = lds + slot * LPT * V;
   const L *row = static_cast<const L *>(a.logits) + t * a.E;
-  float u[2], sx[2];
-  int mine[2], any = 0;
+  constexpr int kSlots = 32 / (LPT < 32 ? LPT : 32);
+  float u[kSlots], sx[kSlots];
+  int mine[kSlots], any = 0;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < kSlots; ++j) {
     const int at = j * LPT + l;
     int e = at < a.k ? a.topk_idx[t * a.k + at] : -1;
     if (e < -1 || e >= a.E) {
@@ -663,7 +1130,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
     mine[j] = e;
     any |= e >= 0;
     u[j] = e >= 0 && a.grad_weights != nullptr ? a.grad_weights[t * a.k + at] : 0.0f;
-    sx[j] = e >= 0 ? logit_at(row, e) : -INFINITY;
+    sx[j] = e >= 0 ? logit_of(row[e]) : -INFINITY;
   }
   any = token_or<LPT>(any);
   float x[V], d[V];
@@ -697,13 +1164,16 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
     }
     // the gates' part, per slot
     if (a.grad_weights != nullptr) {
-      float g[2];
+      float g[kSlots];
       if (a.normalize) {
-        float smax = token_max<LPT>(fmaxf(sx[0], sx[1]));
-        const float sm = fminf(smax, 0.0f);
-        float w[2], tot = 0.0f, dot = 0.0f;
+        float smax = sx[0];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 1; j < kSlots; ++j) smax = fmaxf(smax, sx[j]);
+        smax = token_max<LPT>(smax);
+        const float sm = fminf(smax, 0.0f);
+        float w[kSlots], tot = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
           w[j] = sx[j] > -INFINITY
                      ? (a.softmax ? exp_of(sx[j] - smax) : sigmoid_over(sx[j], sm))
                      : 0.0f;
@@ -712,35 +1182,35 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
         tot = token_sum<LPT>(tot);
         if (!(tot > 0.0f)) tot = 1.0f;  // slots of -inf logits only: no gradient
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kSlots; ++j) {
           w[j] /= tot;
           dot += w[j] * u[j];
         }
         dot = token_sum<LPT>(dot);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kSlots; ++j) {
           g[j] = a.scale * w[j] * (u[j] - dot);
           if (!a.softmax) g[j] *= sigmoid_of(-sx[j]);
         }
       } else if (a.softmax) {
-        float s[2], dot = 0.0f;
+        float s[kSlots], dot = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kSlots; ++j) {
           s[j] = sx[j] > -INFINITY ? exp_of(sx[j] - xmax) / sum : 0.0f;
           dot += s[j] * u[j];
         }
         dot = token_sum<LPT>(dot);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) g[j] = a.scale * s[j] * u[j];
+        for (int j = 0; j < kSlots; ++j) g[j] = a.scale * s[j] * u[j];
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = -p[i] * (a.scale * dot);
       } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kSlots; ++j)
           g[j] = mine[j] < 0 ? 0.0f : a.scale * sigmoid_of(sx[j]) * sigmoid_of(-sx[j]) * u[j];
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < kSlots; ++j)
         if (mine[j] >= 0) atomicAdd(&own[mine[j]], g[j]);
     }
     wave_sync();
@@ -780,10 +1250,12 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
 template <typename F>
 void with_row_shape(int32_t E, F f) {
   using std::integral_constant;
-  if (E <= 64)
-    f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if (E <= 32)
+    f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+  else if (E <= 64)
+    f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
   else if (E <= 128)
-    f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    f(integral_constant<int, 8>{}, integral_constant<int, 16>{});
   else if (E <= 256)
     f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
   else if (E <= 512)
@@ -792,7 +1264,10 @@ void with_row_shape(int32_t E, F f) {
     f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 
-int lanes_per_token(int32_t E) { return E <= 256 ? 16 : (E <= 512 ? 32 : 64); }
+int lanes_per_token(int32_t E) { return E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64; }
+
+// Workgroups of a route launch: eight per compute unit, tokens in turn.
+constexpr int64_t kRouteGrid = 2048;
 
 // Tokens of a balance tile.
 constexpr int kBalanceTile = 64;
@@ -905,17 +1380,38 @@ ep_status_t ep_route(const ep_router_t *router, ep_dtype_t logits_dtype, const v
   a.group_inv = ((1u << 22) + a.group_size - 1) / a.group_size;
   a.softmax = router->score == EP_SCORE_SOFTMAX;
   a.normalize = router->normalize != 0;
-  a.by_logit = bias == nullptr && (a.G == 1 || a.group_topn == 1);
+  const bool by_logit = bias == nullptr && (a.G == 1 || a.group_topn == 1);
   a.vec = vector_rows(router, logits_dtype, logits);
   a.scale = router->scale;
+  a.group_steps = -1;
+  const int lanes = lanes_per_token(a.E);
+  for (int s = 0; (1 << s) <= lanes && a.G > 1; ++s)
+    if (a.group_size == kQuad << s) a.group_steps = s;
   with_row_shape(a.E, [&](auto lpt, auto v) {
-    const dim3 grid((unsigned)((a.T + kThreads / lpt.value - 1) / (kThreads / lpt.value)));
+    const int64_t need = (a.T + kThreads / lpt.value - 1) / (kThreads / lpt.value);
+    const dim3 grid((unsigned)(need < kRouteGrid ? need : kRouteGrid));
+    const auto launch = [&](auto type, auto mode) {
+      if (a.k <= kList)
+        hipLaunchKernelGGL(
+            (route_kernel<decltype(type), lpt.value, v.value, mode.value, true>), grid,
+            dim3(kThreads), 0, stream, a);
+      else
+        hipLaunchKernelGGL(
+            (route_kernel<decltype(type), lpt.value, v.value, mode.value, false>), grid,
+            dim3(kThreads), 0, stream, a);
+    };
+    const auto by_mode = [&](auto type) {
+      if (by_logit)
+        launch(type, std::integral_constant<int, kByLogit>{});
+      else if (a.softmax)
+        launch(type, std::integral_constant<int, kBySoftmax>{});
+      else
+        launch(type, std::integral_constant<int, kBySigmoid>{});
+    };
     if (logits_dtype == EP_DTYPE_F32)
-      hipLaunchKernelGGL((route_kernel<float, lpt.value, v.value>), grid, dim3(kThreads), 0,
-                         stream, a);
+      by_mode(float{});
     else
-      hipLaunchKernelGGL((route_kernel<uint16_t, lpt.value, v.value>), grid, dim3(kThreads), 0,
-                         stream, a);
+      by_mode(uint16_t{});
   });
   return launched("route launch");
 }
