@@ -206,13 +206,6 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
   return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x));
 }
 
-// sigmoid_over for every score of a row.
-__device__ __forceinline__ float sigmoid_over_fast(float x, float m) {
-  const float t = exp_fast(-fabsf(x));
-  const float num = x > 0.0f ? 1.0f : exp_fast(x - m);
-  return num * __builtin_amdgcn_rcpf(1.0f + t);
-}
-
 template <typename K>
 __device__ __forceinline__ K sigmoid_of(K x) {
   const K t = exp_of(x > K(0) ? -x : x);
@@ -900,7 +893,8 @@ struct BalanceArgs {
   float *part_p;     // [tiles + S, E] probability sums of a tile's part of a sequence
   int32_t *part_c;   // [tiles + S, E] counts, likewise
   int32_t *part_n;   // [tiles + S] tokens that count
-  double *seq_loss;  // [S] sum_e f P
+  double *seq_loss;  // [S, seq_blocks] sum of f P over 64 experts
+  int32_t seq_blocks;
   int32_t *counts, *seq_tokens;
   float *mean_probs, *prob_grad, *loss;
   int32_t *status;
@@ -912,61 +906,83 @@ __device__ __forceinline__ int64_t seq_bound(const int32_t *offsets, int32_t s, 
   return o < 0 ? 0 : (o > T ? T : o);
 }
 
-// The last sequence that starts at or before token t.
+// The last sequence that starts at or before token t (the same for the whole
+// wave): 64 starts are looked at side by side, so that 64 sequences take one
+// load and 4096 two.
 __device__ __forceinline__ int seq_of(const int32_t *offsets, int S, int64_t t) {
   if (offsets == nullptr) return 0;
-  int lo = 0, hi = S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (offsets[mid] <= t)
-      lo = mid;
-    else
-      hi = mid - 1;
+  const int lane = threadIdx.x % 64;
+  int lo = 0, n = S;  // it is one of [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int at = lane * step;
+    const uint64_t in = __ballot(at < n && offsets[lo + (at < n ? at : 0)] <= t);
+    // starts ascend; if they do not (which is reported), any of them will do
+    const int last = in != 0 ? 63 - __clzll(in) : 0;
+    lo += last * step;
+    n = n - last * step < step ? n - last * step : step;
   }
   return lo;
 }
 
-// Probabilities of one token's row; false (p zero) if nothing has a score.
-template <int LPT, int V>
-__device__ __forceinline__ void probabilities(const float (&x)[V], bool softmax, float (&p)[V]) {
-  float xmax = -INFINITY;
+// Scores of one token's row over exp(m) and the inverse of their sum: p[i] *
+// the result are its probabilities (0 if nothing has a score).
+template <int LPT, int V, bool kSoftmax>
+__device__ __forceinline__ float row_scores(const float (&x)[V], float (&p)[V]) {
+  float xmax = x[0], sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) xmax = fmaxf(xmax, x[i]);
+  for (int i = 1; i < V; ++i) xmax = fmaxf(xmax, x[i]);
   xmax = token_max<LPT>(xmax);
-  if (xmax == -INFINITY) {
+  if (kSoftmax) {
+    xmax = xmax > -INFINITY ? xmax : 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = 0.0f;
-    return;
+    for (int i = 0; i < V; ++i) p[i] = exp_fast(x[i] - xmax);
+  } else if (xmax > -60.0f) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = sigmoid_fast(x[i]);
+  } else {  // the scores underflow or nearly: relative to the largest
+    const float m = xmax > -INFINITY ? xmax : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = exp_fast(x[i] - m);
   }
-  float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    p[i] = softmax ? exp_of(x[i] - xmax) : sigmoid_over(x[i], fminf(xmax, 0.0f));
-    sum += p[i];
-  }
-  const float inv = 1.0f / token_sum<LPT>(sum);
-#pragma unroll
-  for (int i = 0; i < V; ++i) p[i] *= inv;
+  for (int i = 0; i < V; ++i) sum += p[i];
+  sum = token_sum<LPT>(sum);
+  return sum > 0.0f ? 1.0f / sum : 0.0f;
 }
 
 // One workgroup per tile of tokens.  A tile's part of sequence s goes to row
 // tile + s of the partial sums: along the tokens one of the two grows, so
-// every part has a row of its own.
-template <typename L, int LPT, int V>
+// every part has a row of its own.  The next token's row and ids are loaded
+// before the present one's are worked on.
+template <typename L, int LPT, int V, bool kSoftmax>
 __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
   constexpr int kTokens = kThreads / LPT;
+  constexpr int kSlots = 32 / (LPT < 32 ? LPT : 32);
   __shared__ float sums[kTokens * LPT * V];
   __shared__ int32_t cnt[EP_MAX_EXPERTS];
   __shared__ int32_t ntok;
-  const int l = threadIdx.x % LPT;
+  int l = threadIdx.x % LPT;
   const int slot = threadIdx.x / LPT;
   const int64_t first = (int64_t)blockIdx.x * a.tile;
   const int64_t end = first + a.tile < a.T ? first + a.tile : a.T;
+  float next[V];
+  int ids[kSlots];
+  const auto load = [&](int64_t t) {
+    t = t < end ? t : end - 1;
+    load_row<LPT, V>(static_cast<const L *>(a.logits) + t * a.E, a.E, l, a.vec, next);
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      const int at = s * LPT + l;
+      ids[s] = at < a.k ? a.topk_idx[t * a.k + (at < a.k ? at : 0)] : -1;
+    }
+  };
   int s = seq_of(a.seq_offsets, a.S, first);
   for (int64_t lo = first; lo < end && s < a.S; ++s) {
     int64_t hi = seq_bound(a.seq_offsets, s + 1, a.T);
     hi = hi < end ? hi : end;
     if (hi <= lo) continue;
+    load(lo + slot);
     for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) ntok = 0;
     __syncthreads();
@@ -975,9 +991,14 @@ __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     int mine = 0;
     for (int64_t t = lo + slot; t < hi; t += kTokens) {
+      asm volatile("" : "+v"(l));  // the experts' numbers are not held through the loop
+      float x[V], p[V];
       int any = 0;
-      for (int j = l; j < a.k; j += LPT) {
-        const int e = a.topk_idx[t * a.k + j];
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = next[i];
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        const int e = ids[j];
         if (e >= 0 && e < a.E) {
           any = 1;
           atomicAdd(&cnt[e], 1);
@@ -985,13 +1006,14 @@ __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
           atomicOr(a.status, EP_STATUS_BIT_ROUTE);
         }
       }
-      if (!token_or<LPT>(any)) continue;
-      mine += 1;
-      float x[V], p[V];
-      load_row<LPT, V>(static_cast<const L *>(a.logits) + t * a.E, a.E, l, a.vec, x);
-      probabilities<LPT, V>(x, a.softmax, p);
+      any = token_or<LPT>(any);
+      load(t + kTokens);
+      const float inv = row_scores<LPT, V, kSoftmax>(x, p);
+      mine += any;
+      if (any) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += p[i];
+        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(p[i], inv, acc[i]);
+      }
     }
     if (l == 0 && mine > 0) atomicAdd(&ntok, mine);
 #pragma unroll
@@ -1000,6 +1022,7 @@ __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
     const int64_t out = (int64_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
       float v = 0.0f;
+#pragma unroll 8
       for (int g = 0; g < kTokens; ++g) v += sums[g * LPT * V + e];
       a.part_p[out * a.E + e] = v;
       a.part_c[out * a.E + e] = cnt[e];
@@ -1010,12 +1033,20 @@ __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
   }
 }
 
-// One workgroup per sequence: adds its parts in order, in 64 bits.
-__global__ __launch_bounds__(kThreads) void balance_seq_kernel(BalanceArgs a) {
-  __shared__ double red[kThreads];
+constexpr int kSeqThreads = 1024;
+constexpr int kSeqCols = 64;  // experts of a workgroup
+
+// One workgroup per sequence and 64 experts: adds the sequence's parts in 64
+// bits, 16 slices of them side by side and then those in order.
+__global__ __launch_bounds__(kSeqThreads) void balance_seq_kernel(BalanceArgs a) {
+  constexpr int kSlices = kSeqThreads / kSeqCols;
+  __shared__ double sum_p[kSlices][kSeqCols];
+  __shared__ int32_t sum_c[kSlices][kSeqCols];
+  __shared__ int32_t tokens;
   const int s = blockIdx.x;
   const int64_t lo = seq_bound(a.seq_offsets, s, a.T);
   const int64_t hi = seq_bound(a.seq_offsets, s + 1, a.T);
+  if (threadIdx.x == 0) tokens = 0;
   if (threadIdx.x == 0 && a.seq_offsets != nullptr) {
     const int64_t o0 = a.seq_offsets[s], o1 = a.seq_offsets[s + 1];
     if (o0 > o1 || o0 < 0 || o1 > a.T || (s == 0 && o0 != 0) || (s == a.S - 1 && o1 != a.T))
@@ -1023,31 +1054,41 @@ __global__ __launch_bounds__(kThreads) void balance_seq_kernel(BalanceArgs a) {
   }
   const int64_t first = lo / a.tile + s;
   const int64_t last = lo < hi ? (hi - 1) / a.tile + s : first - 1;
-  int n = 0;
-  for (int64_t r = first; r <= last; ++r) n += a.part_n[r];
-  double dot = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    double p = 0.0;
-    int c = 0;
-    for (int64_t r = first; r <= last; ++r) {
+  const int col = threadIdx.x % kSeqCols, slice = threadIdx.x / kSeqCols;
+  const int e = blockIdx.y * kSeqCols + col;
+  double p = 0.0;
+  int c = 0;
+  if (e < a.E) {
+#pragma unroll 4
+    for (int64_t r = first + slice; r <= last; r += kSlices) {
       p += (double)a.part_p[r * a.E + e];
       c += a.part_c[r * a.E + e];
     }
-    const double mean = n > 0 ? p / n : 0.0;
-    const double f = n > 0 ? (double)a.E * c / ((double)a.k * n) : 0.0;
+  }
+  sum_p[slice][col] = p;
+  sum_c[slice][col] = c;
+  __syncthreads();
+  int n = 0;
+  for (int64_t r = first + threadIdx.x; r <= last; r += kSeqThreads) n += a.part_n[r];
+  if (n > 0) atomicAdd(&tokens, n);
+  __syncthreads();
+  if (slice != 0) return;
+  n = tokens;
+#pragma unroll
+  for (int g = 1; g < kSlices; ++g) {
+    p += sum_p[g][col];
+    c += sum_c[g][col];
+  }
+  const double mean = n > 0 ? p / n : 0.0;
+  double dot = n > 0 ? (double)a.E * c / ((double)a.k * n) * mean : 0.0;
+  if (e < a.E) {
     a.counts[(int64_t)s * a.E + e] = c;
     a.mean_probs[(int64_t)s * a.E + e] = (float)mean;
-    dot += f * mean;
   }
-  red[threadIdx.x] = dot;
-  __syncthreads();
-  for (int m = kThreads / 2; m > 0; m /= 2) {
-    if ((int)threadIdx.x < m) red[threadIdx.x] += red[threadIdx.x + m];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    a.seq_loss[s] = red[0];
-    a.seq_tokens[s] = n;
+  dot = token_sum<kSeqCols>(dot);
+  if (col == 0) {
+    a.seq_loss[(int64_t)s * gridDim.y + blockIdx.y] = dot;
+    if (blockIdx.y == 0) a.seq_tokens[s] = n;
   }
 }
 
@@ -1061,7 +1102,7 @@ __global__ __launch_bounds__(kThreads) void balance_loss_kernel(BalanceArgs a) {
   int mine = 0;
   for (int s = threadIdx.x; s < a.S; s += kThreads) {
     mine += a.seq_tokens[s] > 0;
-    part += a.seq_loss[s];
+    for (int b = 0; b < a.seq_blocks; ++b) part += a.seq_loss[(int64_t)s * a.seq_blocks + b];
   }
   if (mine > 0) atomicAdd(&live, mine);
   red[threadIdx.x] = part;
@@ -1096,150 +1137,175 @@ struct GradArgs {
   void *grad_logits;
   int32_t *status;
   int64_t T;
-  int32_t E, k, S;
-  bool softmax, normalize, vec;
+  int32_t E, k, S, passes;
+  bool normalize, vec, vec_q;
   float scale;
 };
 
-// One token per LPT lanes.  With p the probabilities, q the loss's gradient
-// for them and g its own:  d x_e = g p_e (q_e - sum q p), times (1 - s_e) for
-// sigmoid scores; the gates' part concerns the selected experts only (and,
-// for a softmax that is not normalised over them, -s_e sum s u for all): it
-// is spread over the row through LDS.
-template <typename L, int LPT, int V>
+// Tokens of a workgroup, in passes of one per LPT lanes: it looks for its
+// sequence once.  Fewer workgroups than two per compute unit take one pass
+// (333 tokens of 60 experts: 5 us, with four passes 10).
+constexpr int kGradPasses = 4;
+constexpr int kGradFew = 512;
+
+// With p the probabilities, q the loss's gradient for them and g its own,
+// d x_e = g p_e (q_e - sum q p), times (1 - s_e) for sigmoid scores.  The gates'
+// part concerns the selected experts (and, for a softmax that is not
+// normalised over them, -s_e sum s u for all): it reaches its place in the row
+// through LDS, where only the places written are cleared again.  Bound by
+// reading the logits and writing the gradient: the next row is loaded before
+// the present one is worked on.  kLoss: prob_grad is given.
+template <typename L, int LPT, int V, bool kSoftmax, bool kLoss>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
   constexpr int kTokens = kThreads / LPT;
-  __shared__ float lds[kTokens * LPT * V];
-  const int l = threadIdx.x % LPT;
-  const int slot = threadIdx.x / LPT;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
-  if (t >= a.T) return;
-  float *own = lds + slot * LPT * V;
-  const L *row = static_cast<const L *>(a.logits) + t * a.E;
   constexpr int kSlots = 32 / (LPT < 32 ? LPT : 32);
-  float u[kSlots], sx[kSlots];
-  int mine[kSlots], any = 0;
+  __shared__ __align__(16) float lds[kTokens * LPT * V];
+  int l = threadIdx.x % LPT;
+  const int slot = threadIdx.x / LPT;
+  float *own = lds + slot * LPT * V;
+  const L *logits = static_cast<const L *>(a.logits);
+  const float g = kLoss ? (a.grad_loss != nullptr ? *a.grad_loss : 1.0f) : 0.0f;
+  const bool dense = kLoss || (kSoftmax && !a.normalize && a.grad_weights != nullptr);
 #pragma unroll
-  for (int j = 0; j < kSlots; ++j) {
-    const int at = j * LPT + l;
-    int e = at < a.k ? a.topk_idx[t * a.k + at] : -1;
-    if (e < -1 || e >= a.E) {
-      atomicOr(a.status, EP_STATUS_BIT_ROUTE);
-      e = -1;
+  for (int i = 0; i < V; ++i) own[l * V + i] = 0.0f;
+  const int64_t first = (int64_t)blockIdx.x * kTokens * a.passes;
+  int64_t t = first + slot;
+  int seq = kLoss ? seq_of(a.seq_offsets, a.S, first) : 0;
+  float next[V], next_u[kSlots];
+  int next_id[kSlots];
+  const auto load = [&](int64_t n) {
+    n = n < a.T ? n : a.T - 1;
+    load_row<LPT, V>(logits + n * a.E, a.E, l, a.vec, next);
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      const int at = s * LPT + l;
+      next_id[s] = at < a.k ? a.topk_idx[n * a.k + at] : -1;
+      next_u[s] = at < a.k && a.grad_weights != nullptr ? a.grad_weights[n * a.k + at] : 0.0f;
     }
-    mine[j] = e;
-    any |= e >= 0;
-    u[j] = e >= 0 && a.grad_weights != nullptr ? a.grad_weights[t * a.k + at] : 0.0f;
-    sx[j] = e >= 0 ? logit_of(row[e]) : -INFINITY;
-  }
-  any = token_or<LPT>(any);
-  float x[V], d[V];
+  };
+  if (t >= a.T) return;
+  load(t);
+  for (int pass = 0; pass < a.passes && t < a.T; ++pass, t += kTokens) {
+    asm volatile("" : "+v"(l));  // the experts' numbers are not held through the loop
+    const L *row = logits + t * a.E;
+    float x[V], d[V], q[V], u[kSlots], sx[kSlots];
+    int mine[kSlots], any = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    d[i] = 0.0f;
-    own[expert_of<LPT, V>(l, i)] = 0.0f;
-  }
-  wave_sync();
-  if (any) {
-    load_row<LPT, V>(row, a.E, l, a.vec, x);
-    float xmax = -INFINITY;
+    for (int i = 0; i < V; ++i) x[i] = next[i];
+    bool inside = false;
+    if constexpr (kLoss) {
+      while (seq + 1 < a.S && t >= seq_bound(a.seq_offsets, seq + 1, a.T)) ++seq;
+      inside = t >= seq_bound(a.seq_offsets, seq, a.T) &&
+               t < seq_bound(a.seq_offsets, seq + 1, a.T);
+      load_row<LPT, V>(a.prob_grad + (int64_t)seq * a.E, a.E, l, a.vec_q, q);
+    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) xmax = fmaxf(xmax, x[i]);
-    xmax = token_max<LPT>(xmax);
-    const float m = fminf(xmax, 0.0f);
-    const bool loss = a.prob_grad != nullptr;
-    float p[V], sum = 0.0f;
-    const bool dense = loss || (a.softmax && !a.normalize);
-    if (dense) {
-      if (xmax == -INFINITY) xmax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        p[i] = a.softmax ? exp_of(x[i] - xmax) : sigmoid_over(x[i], m);
-        sum += p[i];
+    for (int j = 0; j < kSlots; ++j) {
+      int e = next_id[j];
+      if (e < -1 || e >= a.E) {
+        atomicOr(a.status, EP_STATUS_BIT_ROUTE);
+        e = -1;
       }
-      sum = token_sum<LPT>(sum);
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      mine[j] = e;
+      any |= e >= 0;
+      u[j] = e >= 0 ? next_u[j] : 0.0f;
+      sx[j] = e >= 0 ? logit_of(row[e >= 0 ? e : 0]) : -INFINITY;
+    }
+    any = token_or<LPT>(any);
+    load(t + kTokens);
+    float inv = 0.0f;
+    if (dense) inv = row_scores<LPT, V, kSoftmax>(x, d);
+    float dot = 0.0f, share = 0.0f;  // sum q p;  scale sum s u of a plain softmax
+    if constexpr (kLoss) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) p[i] *= inv;
+      for (int i = 0; i < V; ++i)
+        dot = __builtin_fmaf(expert_of<LPT, V>(l, i) < a.E ? q[i] : 0.0f, d[i], dot);
+      dot = token_sum<LPT>(dot) * inv;
     }
     // the gates' part, per slot
     if (a.grad_weights != nullptr) {
-      float g[kSlots];
-      if (a.normalize) {
-        float smax = sx[0];
+      float w[kSlots], smax = sx[0], total = 0.0f, sum = 0.0f;
 #pragma unroll
-        for (int j = 1; j < kSlots; ++j) smax = fmaxf(smax, sx[j]);
-        smax = token_max<LPT>(smax);
+      for (int j = 1; j < kSlots; ++j) smax = fmaxf(smax, sx[j]);
+      smax = token_max<LPT>(smax);
+      if (a.normalize) {
         const float sm = fminf(smax, 0.0f);
-        float w[kSlots], tot = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
           w[j] = sx[j] > -INFINITY
-                     ? (a.softmax ? exp_of(sx[j] - smax) : sigmoid_over(sx[j], sm))
+                     ? (kSoftmax ? exp_of(sx[j] - smax) : sigmoid_over(sx[j], sm))
                      : 0.0f;
-          tot += w[j];
+          total += w[j];
         }
-        tot = token_sum<LPT>(tot);
-        if (!(tot > 0.0f)) tot = 1.0f;  // slots of -inf logits only: no gradient
+        total = token_sum<LPT>(total);
+        total = total > 0.0f ? total : 1.0f;  // slots of -inf logits only: no gradient
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
-          w[j] /= tot;
-          dot += w[j] * u[j];
+          w[j] /= total;
+          sum += w[j] * u[j];
         }
-        dot = token_sum<LPT>(dot);
+        sum = token_sum<LPT>(sum);
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
-          g[j] = a.scale * w[j] * (u[j] - dot);
-          if (!a.softmax) g[j] *= sigmoid_of(-sx[j]);
+          w[j] = a.scale * w[j] * (u[j] - sum);
+          if (!kSoftmax) w[j] *= sigmoid_of(-sx[j]);
         }
-      } else if (a.softmax) {
-        float s[kSlots], dot = 0.0f;
+      } else if (kSoftmax) {
+        // the scores' own maximum, as row_scores takes it
+        float xmax = x[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) xmax = fmaxf(xmax, x[i]);
+        xmax = token_max<LPT>(xmax);
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
-          s[j] = sx[j] > -INFINITY ? exp_of(sx[j] - xmax) / sum : 0.0f;
-          dot += s[j] * u[j];
+          w[j] = sx[j] > -INFINITY ? exp_of(sx[j] - xmax) * inv * u[j] : 0.0f;
+          sum += w[j];
+          w[j] *= a.scale;
         }
-        dot = token_sum<LPT>(dot);
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) g[j] = a.scale * s[j] * u[j];
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = -p[i] * (a.scale * dot);
+        share = a.scale * token_sum<LPT>(sum);
       } else {
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
-          g[j] = mine[j] < 0 ? 0.0f : a.scale * sigmoid_of(sx[j]) * sigmoid_of(-sx[j]) * u[j];
+          w[j] = mine[j] >= 0 ? a.scale * sigmoid_of(sx[j]) * sigmoid_of(-sx[j]) * u[j] : 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < kSlots; ++j)
-        if (mine[j] >= 0) atomicAdd(&own[mine[j]], g[j]);
+        if (mine[j] >= 0) atomicAdd(&own[mine[j]], w[j]);
+      wave_sync();
     }
-    wave_sync();
-    if (loss) {
-      const int s = seq_of(a.seq_offsets, a.S, t);
-      const bool inside = t >= seq_bound(a.seq_offsets, s, a.T) &&
-                          t < seq_bound(a.seq_offsets, s + 1, a.T);
-      if (inside) {
-        const float g = a.grad_loss != nullptr ? *a.grad_loss : 1.0f;
-        float q[V], dot = 0.0f;
-        load_row<LPT, V>(a.prob_grad + (int64_t)s * a.E, a.E, l,
-                         a.E % kQuad == 0 && ((uintptr_t)a.prob_grad & 15) == 0, q);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (expert_of<LPT, V>(l, i) < a.E) dot = __builtin_fmaf(q[i], p[i], dot);
-        dot = token_sum<LPT>(dot);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (expert_of<LPT, V>(l, i) >= a.E) continue;
-          float v = g * p[i] * (q[i] - dot);
-          if (!a.softmax) v *= sigmoid_of(-x[i]);
-          d[i] += v;
+    for (int i = 0; i < V; ++i) {
+      float v = 0.0f;
+      if (dense) {
+        const float p = d[i] * inv;
+        v = -p * share;
+        if (kLoss) {
+          float c = inside ? g * p * (q[i] - dot) : 0.0f;
+          if (!kSoftmax) c *= sigmoid_fast(-x[i]);
+          v += expert_of<LPT, V>(l, i) < a.E ? c : 0.0f;
         }
       }
+      d[i] = v;
     }
+    if (a.grad_weights != nullptr) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] += own[expert_of<LPT, V>(l, i)];
+      for (int i = 0; i < V; i += kQuad) {
+        const f32x4 at = *reinterpret_cast<const f32x4 *>(own + expert_of<LPT, V>(l, i));
+#pragma unroll
+        for (int n = 0; n < kQuad; ++n) d[i + n] += at[n];
+      }
+      wave_sync();
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (mine[j] >= 0) own[mine[j]] = 0.0f;
+      wave_sync();
+    }
+    if (!any) {  // padding, whatever its logits are
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = 0.0f;
+    }
+    store_row<LPT, V>(static_cast<L *>(a.grad_logits) + t * a.E, a.E, l, a.vec, d);
   }
-  store_row<LPT, V>(static_cast<L *>(a.grad_logits) + t * a.E, a.E, l, a.vec, d);
 }
 
 // --------------------------------------------------------------------------
@@ -1269,8 +1335,13 @@ int lanes_per_token(int32_t E) { return E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 
 // Workgroups of a route launch: eight per compute unit, tokens in turn.
 constexpr int64_t kRouteGrid = 2048;
 
-// Tokens of a balance tile.
-constexpr int kBalanceTile = 64;
+// Tokens of a balance tile: about 1024 tiles (four workgroups per compute
+// unit) of 32 to 256 tokens.
+int balance_tile(int64_t T) {
+  int tile = 32;
+  while (tile < 256 && T / tile > 1024) tile *= 2;
+  return tile;
+}
 
 ep_status_t check_router(const ep_router_t *r) {
   if (r == nullptr) return failf(EP_ERR_INVALID_ARG, "router is NULL");
@@ -1320,26 +1391,28 @@ bool vector_rows(const ep_router_t *r, ep_dtype_t dtype, const void *p) {
 }
 
 struct BalanceLayout {
-  int64_t tiles, rows;
+  int64_t tiles, rows, blocks;
   size_t part_p, part_c, part_n, seq_loss, total;
 };
 
 BalanceLayout balance_layout(int64_t T, int64_t E, int64_t S) {
   BalanceLayout w;
   const auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-  w.tiles = (T + kBalanceTile - 1) / kBalanceTile;
+  const int tile = balance_tile(T);
+  w.tiles = (T + tile - 1) / tile;
+  w.blocks = (E + kSeqCols - 1) / kSeqCols;
   w.rows = w.tiles + S;
   w.part_p = 0;
   w.part_c = up(w.part_p + sizeof(float) * w.rows * E);
   w.part_n = up(w.part_c + sizeof(int32_t) * w.rows * E);
   w.seq_loss = up(w.part_n + sizeof(int32_t) * w.rows);
-  w.total = up(w.seq_loss + sizeof(double) * S);
+  w.total = up(w.seq_loss + sizeof(double) * S * w.blocks);
   return w;
 }
 
 ep_status_t check_seqs(int32_t num_seqs) {
-  if (num_seqs < 1 || num_seqs >= (1 << 24))
-    return failf(EP_ERR_INVALID_ARG, "num_seqs %d outside [1, 2^24)", num_seqs);
+  if (num_seqs < 1 || num_seqs >= (1 << 21))
+    return failf(EP_ERR_INVALID_ARG, "num_seqs %d outside [1, 2^21)", num_seqs);
   return EP_OK;
 }
 
@@ -1458,7 +1531,8 @@ ep_status_t ep_balance_loss(const ep_router_t *router, ep_dtype_t logits_dtype,
   a.E = router->num_experts;
   a.k = router->num_topk;
   a.S = num_seqs;
-  a.tile = kBalanceTile;
+  a.tile = balance_tile(a.T);
+  a.seq_blocks = (int32_t)w.blocks;
   a.softmax = router->score == EP_SCORE_SOFTMAX;
   a.vec = vector_rows(router, logits_dtype, logits);
   a.coef = coef;
@@ -1475,14 +1549,22 @@ ep_status_t ep_balance_loss(const ep_router_t *router, ep_dtype_t logits_dtype,
   if (w.tiles > 0)
     with_row_shape(a.E, [&](auto lpt, auto v) {
       const dim3 grid((unsigned)w.tiles);
-      if (logits_dtype == EP_DTYPE_F32)
-        hipLaunchKernelGGL((balance_tile_kernel<float, lpt.value, v.value>), grid,
-                           dim3(kThreads), 0, stream, a);
+      const auto launch = [&](auto type, auto softmax) {
+        hipLaunchKernelGGL(
+            (balance_tile_kernel<decltype(type), lpt.value, v.value, softmax.value>), grid,
+            dim3(kThreads), 0, stream, a);
+      };
+      if (logits_dtype == EP_DTYPE_F32 && a.softmax)
+        launch(float{}, std::true_type{});
+      else if (logits_dtype == EP_DTYPE_F32)
+        launch(float{}, std::false_type{});
+      else if (a.softmax)
+        launch(uint16_t{}, std::true_type{});
       else
-        hipLaunchKernelGGL((balance_tile_kernel<uint16_t, lpt.value, v.value>), grid,
-                           dim3(kThreads), 0, stream, a);
+        launch(uint16_t{}, std::false_type{});
     });
-  hipLaunchKernelGGL(balance_seq_kernel, dim3((unsigned)num_seqs), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL(balance_seq_kernel, dim3((unsigned)num_seqs, (unsigned)w.blocks),
+                     dim3(kSeqThreads), 0, stream, a);
   hipLaunchKernelGGL(balance_loss_kernel, dim3((unsigned)num_seqs), dim3(kThreads), 0, stream, a);
   return launched("balance loss launch");
 }
@@ -1518,19 +1600,35 @@ ep_status_t ep_route_backward(const ep_router_t *router, ep_dtype_t logits_dtype
   a.E = router->num_experts;
   a.k = router->num_topk;
   a.S = num_seqs;
-  a.softmax = router->score == EP_SCORE_SOFTMAX;
   a.normalize = router->normalize != 0;
   a.vec = vector_rows(router, logits_dtype, logits) &&
           vector_rows(router, logits_dtype, grad_logits);
+  a.vec_q = vector_rows(router, EP_DTYPE_F32, prob_grad);
   a.scale = router->scale;
+  const bool softmax = router->score == EP_SCORE_SOFTMAX;
   with_row_shape(a.E, [&](auto lpt, auto v) {
-    const dim3 grid((unsigned)((a.T + kThreads / lpt.value - 1) / (kThreads / lpt.value)));
-    if (logits_dtype == EP_DTYPE_F32)
-      hipLaunchKernelGGL((route_backward_kernel<float, lpt.value, v.value>), grid,
-                         dim3(kThreads), 0, stream, a);
+    const int64_t once = kThreads / lpt.value;
+    a.passes = a.T > once * kGradPasses * kGradFew ? kGradPasses : 1;
+    const int64_t tokens = once * a.passes;
+    const dim3 grid((unsigned)((a.T + tokens - 1) / tokens));
+    const auto launch = [&](auto type, auto soft) {
+      if (prob_grad != nullptr)
+        hipLaunchKernelGGL(
+            (route_backward_kernel<decltype(type), lpt.value, v.value, soft.value, true>), grid,
+            dim3(kThreads), 0, stream, a);
+      else
+        hipLaunchKernelGGL(
+            (route_backward_kernel<decltype(type), lpt.value, v.value, soft.value, false>), grid,
+            dim3(kThreads), 0, stream, a);
+    };
+    if (logits_dtype == EP_DTYPE_F32 && softmax)
+      launch(float{}, std::true_type{});
+    else if (logits_dtype == EP_DTYPE_F32)
+      launch(float{}, std::false_type{});
+    else if (softmax)
+      launch(uint16_t{}, std::true_type{});
     else
-      hipLaunchKernelGGL((route_backward_kernel<uint16_t, lpt.value, v.value>), grid,
-                         dim3(kThreads), 0, stream, a);
+      launch(uint16_t{}, std::false_type{});
   });
   return launched("route backward launch");
 }

@@ -109,7 +109,8 @@ ep_status_t ep_balance_workspace_bytes(const ep_router_t *router, int32_t num_se
  *   router       num_tokens, num_experts, num_topk and score are used
  *   topk_idx     [T, k] int32; an id outside [-1, E) counts as -1 and sets
  *                EP_STATUS_BIT_ROUTE
- *   seq_offsets  [num_seqs + 1] int32 device, ascending from 0 to T, or NULL
+ *   seq_offsets  [num_seqs + 1] int32 device, ascending from 0 to T (num_seqs
+ *                below 2^21), or NULL
  *                (then num_seqs is 1: all tokens).  Offsets that are not
  *                that set EP_STATUS_BIT_SEQS, and the results are meaningless
  *   workspace    ep_balance_workspace_bytes() bytes, 256-byte aligned; used
