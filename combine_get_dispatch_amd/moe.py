@@ -49,13 +49,28 @@ def register(L):
         getattr(L, name).restype = ctypes.c_int
 
 
-def _here(t, name):
-    """The library launches on the current device: its tensors live there."""
+def _device(t, name):
+    """The current device, where the library launches: its tensors live there."""
     import torch
 
-    if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if d != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return t
+    return d
+
+
+def _at(t, dev, dtype, shape, name):
+    """Device pointer of a contiguous tensor of this type and shape (None: any)
+    on device dev; None passes NULL."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and (shape is None or t.shape == shape) and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _ptr(t, dtype, shape, name)  # says what is wrong
+    raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
 def _logits_dtype(t):
@@ -81,14 +96,15 @@ def ep_route(router: ep_router_t, logits, bias, token_mask, topk_idx, topk_weigh
     import torch
 
     T, E, k = router.num_tokens, router.num_experts, router.num_topk
+    d = _device(logits, "logits")
     st = lib().ep_route(
         ctypes.byref(router), _logits_dtype(logits),
-        _ptr(_here(logits, "logits"), None, (T, E), "logits"),
-        _ptr(_here(bias, "bias"), torch.float32, (E,), "bias"),
-        _ptr(_here(token_mask, "token_mask"), torch.uint8, (T,), "token_mask"),
-        _ptr(topk_idx, torch.int32, (T, k), "topk_idx"),
-        _ptr(topk_weights, torch.float32, (T, k), "topk_weights"),
-        _ptr(status, torch.int32, (1,), "status"), _stream(stream))
+        _at(logits, d, logits.dtype, (T, E), "logits"),
+        _at(bias, d, torch.float32, (E,), "bias"),
+        _at(token_mask, d, torch.uint8, (T,), "token_mask"),
+        _at(topk_idx, d, torch.int32, (T, k), "topk_idx"),
+        _at(topk_weights, d, torch.float32, (T, k), "topk_weights"),
+        _at(status, d, torch.int32, (1,), "status"), _stream(stream))
     _check(st, "ep_route")
 
 
@@ -104,18 +120,17 @@ def ep_balance_loss(router: ep_router_t, logits, topk_idx, seq_offsets, coef, wo
     import torch
 
     T, E, k, S = router.num_tokens, router.num_experts, router.num_topk, _num_seqs(seq_offsets)
+    i32, f32, d = torch.int32, torch.float32, _device(logits, "logits")
     st = lib().ep_balance_loss(
         ctypes.byref(router), _logits_dtype(logits),
-        _ptr(_here(logits, "logits"), None, (T, E), "logits"),
-        _ptr(_here(topk_idx, "topk_idx"), torch.int32, (T, k), "topk_idx"),
-        _ptr(_here(seq_offsets, "seq_offsets"), torch.int32, name="seq_offsets"), S, float(coef),
-        _ptr(workspace, torch.uint8, name="workspace"), workspace.numel(),
-        _ptr(counts, torch.int32, (S, E), "counts"),
-        _ptr(seq_tokens, torch.int32, (S,), "seq_tokens"),
-        _ptr(mean_probs, torch.float32, (S, E), "mean_probs"),
-        _ptr(prob_grad, torch.float32, (S, E), "prob_grad"),
-        _ptr(loss, torch.float32, (1,), "loss"), _ptr(status, torch.int32, (1,), "status"),
-        _stream(stream))
+        _at(logits, d, logits.dtype, (T, E), "logits"),
+        _at(topk_idx, d, i32, (T, k), "topk_idx"),
+        _at(seq_offsets, d, i32, None, "seq_offsets"), S, float(coef),
+        _at(workspace, d, torch.uint8, None, "workspace"), workspace.numel(),
+        _at(counts, d, i32, (S, E), "counts"), _at(seq_tokens, d, i32, (S,), "seq_tokens"),
+        _at(mean_probs, d, f32, (S, E), "mean_probs"),
+        _at(prob_grad, d, f32, (S, E), "prob_grad"), _at(loss, d, f32, (1,), "loss"),
+        _at(status, d, i32, (1,), "status"), _stream(stream))
     _check(st, "ep_balance_loss")
 
 
@@ -125,16 +140,17 @@ def ep_route_backward(router: ep_router_t, logits, topk_idx, grad_weights, prob_
 
     T, E, k = router.num_tokens, router.num_experts, router.num_topk
     S = _num_seqs(seq_offsets) if prob_grad is not None else 1
+    i32, f32, d = torch.int32, torch.float32, _device(logits, "logits")
     st = lib().ep_route_backward(
         ctypes.byref(router), _logits_dtype(logits),
-        _ptr(_here(logits, "logits"), None, (T, E), "logits"),
-        _ptr(_here(topk_idx, "topk_idx"), torch.int32, (T, k), "topk_idx"),
-        _ptr(_here(grad_weights, "grad_weights"), torch.float32, (T, k), "grad_weights"),
-        _ptr(_here(prob_grad, "prob_grad"), torch.float32, (S, E), "prob_grad"),
-        _ptr(_here(seq_offsets, "seq_offsets"), torch.int32, name="seq_offsets"), S,
-        _ptr(_here(grad_loss, "grad_loss"), torch.float32, (1,), "grad_loss"),
-        _ptr(grad_logits, logits.dtype, (T, E), "grad_logits"),
-        _ptr(status, torch.int32, (1,), "status"), _stream(stream))
+        _at(logits, d, logits.dtype, (T, E), "logits"),
+        _at(topk_idx, d, i32, (T, k), "topk_idx"),
+        _at(grad_weights, d, f32, (T, k), "grad_weights"),
+        _at(prob_grad, d, f32, (S, E), "prob_grad"),
+        _at(seq_offsets, d, i32, None, "seq_offsets"), S,
+        _at(grad_loss, d, f32, (1,), "grad_loss"),
+        _at(grad_logits, d, logits.dtype, (T, E), "grad_logits"),
+        _at(status, d, i32, (1,), "status"), _stream(stream))
     _check(st, "ep_route_backward")
 
 
@@ -155,15 +171,15 @@ def ep_w4_pack(w4: ep_w4_t, codes, scales, zeros, w_codes, w_scales, w_zeros, st
     _sized(w_codes, nb, "w_codes")
     _sized(w_scales, ns, "w_scales")
     _sized(w_zeros, ns, "w_zeros")
+    d = _device(codes, "codes")
     st = lib().ep_w4_pack(
         ctypes.byref(w4),
-        _ptr(_here(codes, "codes"), torch.uint8, (w4.num_experts, rows, w4.in_features // 2),
-             "codes"),
-        _ptr(_here(scales, "scales"), torch.bfloat16, groups, "scales"),
-        _ptr(_here(zeros, "zeros"), torch.uint8, groups, "zeros"),
-        _ptr(w_codes, torch.uint8, name="w_codes"),
-        _ptr(w_scales, torch.bfloat16, name="w_scales"),
-        _ptr(w_zeros, torch.uint8, name="w_zeros"), _stream(stream))
+        _at(codes, d, torch.uint8, (w4.num_experts, rows, w4.in_features // 2), "codes"),
+        _at(scales, d, torch.bfloat16, groups, "scales"),
+        _at(zeros, d, torch.uint8, groups, "zeros"),
+        _at(w_codes, d, torch.uint8, None, "w_codes"),
+        _at(w_scales, d, torch.bfloat16, None, "w_scales"),
+        _at(w_zeros, d, torch.uint8, None, "w_zeros"), _stream(stream))
     _check(st, "ep_w4_pack")
 
 
@@ -185,11 +201,13 @@ def ep_expert_product_w4(w4: ep_w4_t, x, x_scales, w_codes, w_scales, w_zeros, e
 
 
 def _weight_ptrs(w_codes, w_scales, w_zeros):
+    """Their device, and the pointers."""
     import torch
 
-    return (_ptr(_here(w_codes, "w_codes"), torch.uint8, name="w_codes"),
-            _ptr(_here(w_scales, "w_scales"), torch.bfloat16, name="w_scales"),
-            _ptr(_here(w_zeros, "w_zeros"), torch.uint8, name="w_zeros"))
+    d = _device(w_codes, "w_codes")
+    return d, (_at(w_codes, d, torch.uint8, None, "w_codes"),
+               _at(w_scales, d, torch.bfloat16, None, "w_scales"),
+               _at(w_zeros, d, torch.uint8, None, "w_zeros"))
 
 
 def _product(w4, ref, x, x_scales, weights, expert_offsets, num_tokens_per_expert, out, stream):
@@ -205,13 +223,16 @@ def _product(w4, ref, x, x_scales, weights, expert_offsets, num_tokens_per_exper
     if expert_offsets.dim() != 1 or expert_offsets.shape[0] not in (E, E + 1):
         raise ValueError(f"expert_offsets has shape {tuple(expert_offsets.shape)}, "
                          f"expected ({E},) or ({E + 1},)")
+    d = _device(x, "x")
+    if d != weights[0]:
+        raise ValueError("the weights are not on the current device")
     st = lib().ep_expert_product_w4(
         ref, EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16,
-        _ptr(_here(x, "x"), torch.uint8 if fp8 else torch.bfloat16, name="x"),
-        _ptr(x_scales, torch.float32, (cap, K // 128), "x_scales"), *weights,
-        _ptr(expert_offsets, torch.int32, name="expert_offsets"),
-        _ptr(num_tokens_per_expert, torch.int32, (E,), "num_tokens_per_expert"), cap,
-        _ptr(out, torch.bfloat16, name="out"), _stream(stream))
+        _at(x, d, torch.uint8 if fp8 else torch.bfloat16, None, "x"),
+        _at(x_scales, d, torch.float32, (cap, K // 128), "x_scales"), *weights[1],
+        _at(expert_offsets, d, torch.int32, None, "expert_offsets"),
+        _at(num_tokens_per_expert, d, torch.int32, (E,), "num_tokens_per_expert"), cap,
+        _at(out, d, torch.bfloat16, None, "out"), _stream(stream))
     _check(st, "ep_expert_product_w4")
 
 
