@@ -261,8 +261,9 @@ struct Best2<float> {
     second = fmaxf(fminf(first, a), fmaxf(second, b));
     first = fmaxf(first, a);
   }
+  // two keys near the type's lowest add to -inf, which would mean no key
   __device__ __forceinline__ float key(int topn) const {
-    return topn == 2 && second > -INFINITY ? first + second : first;
+    return topn == 2 && second > -INFINITY ? fmaxf(first + second, -FLT_MAX) : first;
   }
 };
 
@@ -689,10 +690,12 @@ __device__ __forceinline__ bool order_exactly(const RouteArgs &a, const L *row,
 //     32-bit keys.
 //   Groups, or neighbours of that search, within the margin: all of the token's
 //     keys and groups in 64 bits (select_exactly).
-// The margin is 2^-19 of the best score and key there can be: a score is off
-// by at most 2^-21 of the best, its sum with the bias by 2^-24 of the key, two
-// sums of two keys by four times that.  bf16 logits are whole within the front
-// bits: equal means equal.
+// The margin is 2^-19 of the best score and key there can be, together 2^-18
+// of the best score: a score is off by at most 2^-22 of the best by its
+// exponential and quotient, those of a softmax by 2^-19.6 of themselves, all
+// alike, by the sum of the row; a difference of two sums of two keys by four
+// times the one and twice the other, and by 2^-22 of a key.  bf16 logits are
+// whole within the front bits: equal means equal.
 template <typename L, int LPT, int V, int kMode, bool kShort>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   constexpr int kTokens = kThreads / LPT;
@@ -810,7 +813,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
         uint32_t kth = list[0];
 #pragma unroll
         for (int j = 1; j < kList; ++j) kth = j < a.k ? list[j] : kth;
-        const float least = kth != 0 ? key_in<kBits>(kth, true) - margin : -FLT_MAX;
+        const float least =  // never -inf: keys of -inf are not among them
+            kth != 0 ? fmaxf(key_in<kBits>(kth, true) - margin, -FLT_MAX) : -FLT_MAX;
         if (a.k == kList) {
           int above = 0;
 #pragma unroll
@@ -977,11 +981,11 @@ __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
       ids[s] = at < a.k ? a.topk_idx[t * a.k + (at < a.k ? at : 0)] : -1;
     }
   };
-  int s = seq_of(a.seq_offsets, a.S, first);
-  for (int64_t lo = first; lo < end && s < a.S; ++s) {
+  for (int64_t lo = first; lo < end;) {
+    const int s = seq_of(a.seq_offsets, a.S, lo);
     int64_t hi = seq_bound(a.seq_offsets, s + 1, a.T);
     hi = hi < end ? hi : end;
-    if (hi <= lo) continue;
+    if (hi <= lo) break;  // the offsets do not ascend to T: reported by the next kernel
     load(lo + slot);
     for (int e = threadIdx.x; e < a.E; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) ntok = 0;
@@ -1092,7 +1096,11 @@ __global__ __launch_bounds__(kSeqThreads) void balance_seq_kernel(BalanceArgs a)
   }
 }
 
-// Workgroup s: prob_grad of sequence s; workgroup 0 the loss too.
+// Workgroups of the last launch: sequences in turn.  Each counts those with
+// tokens, which would grow with the square of a workgroup per sequence.
+constexpr int kLossGrid = 512;
+
+// prob_grad, and by workgroup 0 the loss.
 __global__ __launch_bounds__(kThreads) void balance_loss_kernel(BalanceArgs a) {
   __shared__ double red[kThreads];
   __shared__ int32_t live;
@@ -1115,12 +1123,13 @@ __global__ __launch_bounds__(kThreads) void balance_loss_kernel(BalanceArgs a) {
     }
     if (threadIdx.x == 0) *a.loss = (float)(scale * red[0]);
   }
-  const int s = blockIdx.x;
-  const int n = a.seq_tokens[s];
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    const double c = a.counts[(int64_t)s * a.E + e];
-    a.prob_grad[(int64_t)s * a.E + e] =
-        n > 0 ? (float)(scale * ((double)a.E * c / ((double)a.k * n)) / n) : 0.0f;
+  for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+    const int n = a.seq_tokens[s];
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+      const double c = a.counts[(int64_t)s * a.E + e];
+      a.prob_grad[(int64_t)s * a.E + e] =
+          n > 0 ? (float)(scale * ((double)a.E * c / ((double)a.k * n)) / n) : 0.0f;
+    }
   }
 }
 
@@ -1194,7 +1203,16 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
     for (int i = 0; i < V; ++i) x[i] = next[i];
     bool inside = false;
     if constexpr (kLoss) {
-      while (seq + 1 < a.S && t >= seq_bound(a.seq_offsets, seq + 1, a.T)) ++seq;
+      if (t >= seq_bound(a.seq_offsets, seq + 1, a.T)) {
+        int high = a.S - 1;  // the last sequence that starts at or before t
+        while (seq < high) {
+          const int mid = seq + (high - seq + 1) / 2;
+          if (seq_bound(a.seq_offsets, mid, a.T) <= t)
+            seq = mid;
+          else
+            high = mid - 1;
+        }
+      }
       inside = t >= seq_bound(a.seq_offsets, seq, a.T) &&
                t < seq_bound(a.seq_offsets, seq + 1, a.T);
       load_row<LPT, V>(a.prob_grad + (int64_t)seq * a.E, a.E, l, a.vec_q, q);
@@ -1565,7 +1583,9 @@ ep_status_t ep_balance_loss(const ep_router_t *router, ep_dtype_t logits_dtype,
     });
   hipLaunchKernelGGL(balance_seq_kernel, dim3((unsigned)num_seqs, (unsigned)w.blocks),
                      dim3(kSeqThreads), 0, stream, a);
-  hipLaunchKernelGGL(balance_loss_kernel, dim3((unsigned)num_seqs), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL(balance_loss_kernel,
+                     dim3((unsigned)(num_seqs < kLossGrid ? num_seqs : kLossGrid)),
+                     dim3(kThreads), 0, stream, a);
   return launched("balance loss launch");
 }
 

@@ -108,6 +108,55 @@ def test_route_ties_go_to_the_lowest_index():
                 assert np.array_equal(idx.cpu().numpy(), ids)
 
 
+def test_route_close_keys():
+    """Scores that 32 bits round together, in and across groups: every token is
+    decided in 64 bits.  Logits a few units of the last place apart, at the
+    flat end of the sigmoid and in the middle of a softmax."""
+    rng = np.random.default_rng(17)
+    for E, G, tg, topn, k in ((64, 1, 1, 1, 8), (64, 8, 3, 2, 6), (256, 8, 4, 2, 8),
+                              (100, 5, 2, 1, 12), (512, 16, 4, 2, 7), (1024, 8, 3, 2, 32),
+                              (16, 4, 2, 2, 3)):
+        T = 23
+        base = np.float32(4.0) + rng.integers(-6, 7, size=(T, E)).astype(np.float32) * np.float32(
+            2.0 ** -20)
+        x = np.where(rng.random((T, E)) < 0.3, base, rng.normal(size=(T, E))).astype(np.float32)
+        bias = np.where(rng.random(E) < 0.5, 0, rng.integers(-2, 3, size=E) * 2.0 ** -23).astype(
+            np.float32)
+        for score in ("sigmoid", "softmax"):
+            for b in (None, bias, bias + np.float32(0.25)):
+                say(f"close keys E={E} G={G} {score} bias={b is not None}")
+                r = ep.EpRouter(T, E, k, score=score, groups=G, topk_groups=tg, group_topn=topn)
+                got = r.route(dev(x), bias=None if b is None else dev(b))
+                r.check_status()
+                check_route(got, x, k, score=score, bias=b, groups=G, topk_groups=tg,
+                            group_topn=topn)
+
+
+def test_route_bias_of_the_lowest_value():
+    """Experts and whole groups put last by a bias of the type's lowest value,
+    beside logits of -inf: the sums of two such keys pass the 32-bit range, and
+    those experts still come before those that cannot be selected."""
+    rng = np.random.default_rng(18)
+    low = np.finfo(np.float32).min
+    for E, G, tg, topn, k in ((16, 4, 2, 2, 6), (16, 1, 1, 1, 8), (64, 8, 3, 2, 8),
+                              (60, 5, 2, 2, 7), (256, 8, 4, 2, 8), (256, 8, 4, 1, 20),
+                              (512, 1, 1, 1, 8), (1024, 8, 2, 2, 8)):
+        T = 19
+        x = rng.normal(size=(T, E)).astype(np.float32)
+        x[rng.random((T, E)) < 0.2] = -np.inf
+        x[: T // 2, : E // 2] = -np.inf
+        for share in (0.5, 0.97, 1.0):
+            bias = np.where(rng.random(E) < share, low, 0).astype(np.float32)
+            bias[: E // max(G, 2)] = low
+            for score in ("sigmoid", "softmax"):
+                say(f"lowest bias E={E} G={G} topn={topn} share={share} {score}")
+                r = ep.EpRouter(T, E, k, score=score, groups=G, topk_groups=tg, group_topn=topn)
+                got = r.route(dev(x), bias=dev(bias))
+                r.check_status()
+                check_route(got, x, k, score=score, bias=bias, groups=G, topk_groups=tg,
+                            group_topn=topn)
+
+
 def test_route_masked_experts_tokens_and_bad_rows():
     """-inf logits and biases, fewer selectable experts than slots, whole rows
     of -inf, the type's lowest values, masked tokens that hold NaN, and rows
@@ -218,6 +267,75 @@ def test_balance(T, E, k, S, score, bf16):
     assert np.all(np.abs(r.mean_probs.cpu().numpy() - mean) <= rel * mean + 1e-30)
     assert np.all(np.abs(r.prob_grad.cpu().numpy() - q) <= 4 * U32 * q)
     assert abs(loss.item() - l) <= rel * l + 1e-30
+
+
+def test_many_empty_sequences():
+    """Thousands of sequences without a token among a few that have some."""
+    T, E, k, S = 150, 8, 2, 5000
+    rng = np.random.default_rng(15)
+    x, t = draw_logits(rng, T, E, False)
+    ids = draw_route(rng, T, E, k)
+    offsets = np.zeros(S + 1, np.int32)
+    offsets[1000:] = 37
+    offsets[1001:] = 90
+    offsets[4000:] = T
+    q = rng.normal(size=(S, E)).astype(np.float32)
+    say("many empty sequences")
+    r = ep.EpRouter(T, E, k, max_seqs=S)
+    loss = r.balance_loss(t.cuda(), dev(ids), 0.5, seq_offsets=dev(offsets))
+    r.check_status()
+    l, counts, n, mean, pg = ref.balance(x, ids, 0.5, "softmax", offsets)
+    assert np.array_equal(r.counts.cpu().numpy(), counts)
+    assert np.array_equal(r.seq_tokens.cpu().numpy(), n)
+    rel = (score_steps(x).max() + 128) * U32
+    assert abs(loss.item() - l) <= rel * l
+    assert np.all(np.abs(r.prob_grad.cpu().numpy() - pg) <= 4 * U32 * pg)
+    g = r.backward(t.cuda(), dev(ids), None, prob_grad=dev(q), seq_offsets=dev(offsets))
+    check_grad(g, x, ids, None, False, prob_grad=q, offsets=offsets)
+
+
+def test_large_batches_cross_passes_and_tiles():
+    """Enough tokens that a workgroup takes several passes, tiles grow past 32
+    tokens and the router's workgroups take tokens in turn: checked on a sample
+    of rows, and the counts and means on all of them."""
+    T, E, k, S = 70001, 64, 6, 9
+    rng = np.random.default_rng(16)
+    x, t = draw_logits(rng, T, E, True)
+    mask = (rng.random(T) >= 0.1).astype(np.uint8)
+    offsets = draw_offsets(rng, T, S)
+    u = rng.normal(size=(T, k)).astype(np.float32)
+    say("large batch")
+    r = ep.EpRouter(T, E, k, score="sigmoid", logits_dtype=torch.bfloat16, max_seqs=S)
+    xd = t.cuda()
+    bias = (rng.normal(size=E) * 0.05).astype(np.float32)
+    idx, w = r.route(xd, bias=dev(bias), token_mask=dev(mask))
+    r.balance_loss(xd, idx, 0.1, seq_offsets=dev(offsets))
+    g = r.backward(xd, idx, dev(u), prob_grad=r.prob_grad, seq_offsets=dev(offsets))
+    r.check_status()
+    ids = idx.cpu().numpy()
+    rows = np.unique(np.concatenate([np.arange(40), rng.integers(0, T, 400), np.arange(T - 40, T)]))
+    want, ww, _ = ref.route(x[rows], k, "sigmoid", bias, mask[rows])
+    assert np.array_equal(ids[rows], want)
+    tol = ww * (score_steps(x[rows]) * U32)[:, None]
+    assert np.all(np.abs(w.cpu().numpy()[rows] - ww) <= tol)
+    assert np.array_equal(ids[:, 0] < 0, mask == 0)
+    on = mask != 0
+    p = ref.probabilities(x, "sigmoid")
+    rel = (score_steps(x).max() + 128) * U32
+    for s in range(S):
+        lo, hi = offsets[s], offsets[s + 1]
+        have = ids[lo:hi][on[lo:hi]].reshape(-1)
+        assert np.array_equal(r.counts[s].cpu().numpy(), np.bincount(have, minlength=E))
+        n = int(on[lo:hi].sum())
+        if n:
+            mean = p[lo:hi][on[lo:hi]].mean(axis=0)
+            assert np.all(np.abs(r.mean_probs[s].cpu().numpy() - mean) <= rel * mean)
+    pg = r.prob_grad.cpu().numpy()
+    seq = np.searchsorted(offsets[1:], rows, side="right")
+    for s in np.unique(seq):
+        sel = rows[seq == s]
+        check_grad(g[torch.from_numpy(sel).cuda()], x[sel], ids[sel], u[sel], True,
+                   score="sigmoid", prob_grad=pg[s:s + 1])
 
 
 def test_balance_empty_and_all_masked():
