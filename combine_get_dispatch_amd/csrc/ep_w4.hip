@@ -685,7 +685,15 @@ ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const vo
     return failf(EP_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned_to(x, 16) || !aligned_to(w_codes, 16))
     return failf(EP_ERR_INVALID_ARG, "x and w_codes must be 16-byte aligned");
+  // the row blocks of all experts are numbered in 32 bits, each expert's at most the buffer's
+  if ((capacity / kBlockRows + 1) * w4->num_experts >= INT32_MAX)
+    return failf(EP_ERR_INVALID_ARG, "capacity %lld x %d experts has too many row blocks",
+                 (long long)capacity, w4->num_experts);
   if (capacity == 0) return EP_OK;
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), out0 = reinterpret_cast<uintptr_t>(out);
+  if (x0 < out0 + (uintptr_t)capacity * w4->out_features * 2 &&
+      out0 < x0 + (uintptr_t)capacity * w4->in_features * (fp8 ? 1 : 2))
+    return failf(EP_ERR_INVALID_ARG, "out overlaps x");
   ProductArgs a;
   a.x = x;
   a.x_scales = x_scales;

@@ -314,7 +314,8 @@ class EpRouter:
 
 class W4Experts:
     """Packed 4-bit weights of a set of experts (W4Experts.pack lays out
-    row-major ones) and their product."""
+    row-major ones) and their product.  Their values may be rewritten in place;
+    other tensors are another W4Experts."""
 
     def __init__(self, w_codes, w_scales, w_zeros, out_features, in_features, group):
         if w_codes.dim() < 2:
@@ -327,9 +328,21 @@ class W4Experts:
         _sized(w_codes, nb, "w_codes")
         _sized(w_scales, ns, "w_scales")
         _sized(w_zeros, ns, "w_zeros")
-        self.w_codes, self.w_scales, self.w_zeros = w_codes, w_scales, w_zeros
+        self._tensors = w_codes, w_scales, w_zeros  # held as long as their pointers
         self._ref = ctypes.byref(self.cfg)
         self._weights = _weight_ptrs(w_codes, w_scales, w_zeros)
+
+    @property
+    def w_codes(self):
+        return self._tensors[0]
+
+    @property
+    def w_scales(self):
+        return self._tensors[1]
+
+    @property
+    def w_zeros(self):
+        return self._tensors[2]
 
     @classmethod
     def pack(cls, codes, scales, zeros=None, swiglu=False, stream=None):

@@ -20,8 +20,9 @@
  * ep_expert_product_w4 (gate and up, SwiGLU), ep_expert_product_w4 (down),
  * ep_combine.
  *
- * Every result is deterministic: sums have a fixed order.  Nothing is allocated and nothing waits, so every call
- * can be captured in a graph; the counts and offsets stay on the device.
+ * Every result is deterministic: sums have a fixed order.  Nothing is
+ * allocated and nothing waits, so every call can be captured in a graph; the
+ * counts and offsets stay on the device.
  */
 #ifndef EP_MOE_H
 #define EP_MOE_H
@@ -41,7 +42,8 @@ typedef enum ep_score {
 #define EP_MAX_GROUPS 64
 
 typedef struct ep_router {
-  int32_t num_tokens;  /* T >= 0, T * E < 2^40 */
+  int32_t num_tokens;  /* T >= 0; T * L <= 2^32 - 512 with L lanes per token: 8 up to
+                          128 experts, 16 up to 256, 32 up to 512, else 64 */
   int32_t num_experts; /* 1 <= E <= EP_MAX_EXPERTS */
   int32_t num_topk;    /* 1 <= k <= min(E, EP_MAX_TOPK) */
   int32_t score;       /* ep_score_t */
@@ -110,9 +112,9 @@ ep_status_t ep_balance_workspace_bytes(const ep_router_t *router, int32_t num_se
  *   topk_idx     [T, k] int32; an id outside [-1, E) counts as -1 and sets
  *                EP_STATUS_BIT_ROUTE
  *   seq_offsets  [num_seqs + 1] int32 device, ascending from 0 to T (num_seqs
- *                below 2^21), or NULL
- *                (then num_seqs is 1: all tokens).  Offsets that are not
- *                that set EP_STATUS_BIT_SEQS, and the results are meaningless
+ *                below 2^21), or NULL (then num_seqs is 1: all tokens).
+ *                Offsets that are not that set EP_STATUS_BIT_SEQS, and the
+ *                results are meaningless
  *   workspace    ep_balance_workspace_bytes() bytes, 256-byte aligned; used
  *                within the call only, by one call at a time
  *   counts, seq_tokens int32; mean_probs, prob_grad fp32; loss fp32 [1]
@@ -200,7 +202,7 @@ ep_status_t ep_w4_pack(const ep_w4_t *w4, const uint8_t *codes, const uint16_t *
  * instructions exactly, scales are applied in fp32; the output's is the only
  * rounding below fp32.
  *
- *   x_dtype       EP_DTYPE_BF16: x bf16 [capacity, K], K % 8 == 0 by group
+ *   x_dtype       EP_DTYPE_BF16: x bf16 [capacity, K]
  *                 EP_DTYPE_FP8_E4M3: x uint8 [capacity, K] and x_scales fp32
  *                 [capacity, K / 128] (K % 128 == 0), as ep_dispatch writes
  *   w_codes, w_scales, w_zeros (or NULL)   from ep_w4_pack, codes 16-byte aligned
@@ -210,7 +212,10 @@ ep_status_t ep_w4_pack(const ep_w4_t *w4, const uint8_t *codes, const uint16_t *
  *                 a pointer to the rank's first).  Rows are cut off at
  *                 `capacity`, as dispatch's are; an expert whose offset or
  *                 count is negative has none.
- *   out           bf16 [capacity, N]; only the experts' rows are written
+ *   capacity      rows of x and out; (capacity / 64 + 1) * num_experts < 2^31 - 1
+ *   out           bf16 [capacity, N], apart from x; only the experts' rows are
+ *                 written.  A row of x that is not finite makes its own
+ *                 outputs NaN, no other's
  */
 ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const void *x,
                                  const float *x_scales, const uint8_t *w_codes,

@@ -445,3 +445,22 @@ def test_two_streams_and_repeats_are_bit_equal():
             assert torch.equal(o, first)
         assert torch.equal(r.topk_idx, r0.topk_idx) and torch.equal(r.loss, r0.loss)
         assert torch.equal(r.mean_probs, r0.mean_probs)
+
+
+def test_weights_are_those_of_the_object():
+    """Rewritten in place they are used, and no other tensor can take their place."""
+    rng = np.random.default_rng(21)
+    q = rng.integers(0, 256, size=(2, 48, 32), dtype=np.uint8)
+    s = torch.ones(2, 48, 1, dtype=torch.bfloat16)
+    w = ep.W4Experts.pack(dev(q), s.cuda())
+    x = torch.from_numpy(rng.integers(-4, 5, size=(5, 64)).astype(np.float32)).bfloat16().cuda()
+    off, cnt = dev(np.array([0, 3], np.int32)), dev(np.array([3, 2], np.int32))
+    first = w.product(x, None, off, cnt).float().cpu()
+    with pytest.raises(AttributeError):
+        w.w_codes = w.w_codes.clone()
+    w.w_scales.mul_(2)  # exact in bf16
+    assert torch.equal(w.product(x, None, off, cnt).float().cpu(), 2 * first)
+    with pytest.raises(ep.EpError):  # rows written over those that others still read
+        w2 = ep.W4Experts.pack(dev(q[:, :, :]), s.cuda())
+        buf = torch.zeros(5, 64, dtype=torch.bfloat16, device="cuda")
+        w2.product(buf, None, off, cnt, out=buf.view(-1)[:240].view(5, 48))

@@ -127,6 +127,9 @@ def test_product_rejections():
     for kw in (dict(dtype=2), dict(dtype=1), dict(x=None), dict(codes=None), dict(scales=None),
                dict(off=None), dict(cnt=None), dict(cap=-1), dict(cap=(1 << 31) - 1),
                dict(out=None), dict(x=ctypes.c_void_p(0x100008)),
+               dict(out=_fake(1)), dict(out=ctypes.c_void_p(0x100000 + 8 * 256 * 2 - 2)),
+               dict(x=ctypes.c_void_p(0x600000 + 8 * 32 * 2 - 16)),
+               dict(w=_w4(E=1024), cap=1 << 28),
                dict(codes=ctypes.c_void_p(0x100008)),
                dict(w=_w4(K=96, group=32), dtype=1, xs=_fake(7))):
         assert call(**kw) == ep.EP_ERR_INVALID_ARG, kw
