@@ -104,6 +104,7 @@ struct ProductArgs {
   uint16_t *out;
   int64_t capacity;
   int32_t N, K, N16, K128;
+  int32_t stream_rows;  // experts with more rows are tiled
 };
 
 // Rows of an expert inside the buffers.
@@ -188,7 +189,12 @@ struct Frag<true> {
 };
 
 // Experts with at most kStreamRows rows are streamed (product_stream_kernel),
-// the others tiled (product_tile_kernel).
+// the others tiled (product_tile_kernel).  Past 16 rows a streamed expert's
+// weights are read twice; where the blocks of the tiles fill the chip several
+// times over (kTileRounds), those experts are tiled too.  17 and 32 rows each,
+// streamed and tiled: 64 experts 2048 x 7168 (3584 blocks) 221 and 248 us, 146
+// and 151; 32 experts 7168 x 2 x 2048, FP8 (1024 blocks) 172 and 206, 219 and
+// 229; 8 experts 4096 x 2048 (128 blocks) 20 and 23, about 37.
 constexpr int kStreamRows = 32;
 constexpr int kStreamWaves = 8;
 constexpr int64_t kInfinityCache = int64_t{256} << 20;
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
   const int col = lane & 15, quad = lane >> 4;
   int64_t first, rows;
   expert_rows(a, e, &first, &rows);
-  if (rows == 0 || rows > kStreamRows) return;
+  if (rows == 0 || rows > a.stream_rows) return;
   const int G = a.K / GROUP;
   const int ot = blockIdx.x * kOut;
   int64_t tile_row[kTiles];
@@ -328,6 +334,7 @@ constexpr int kBlockRows = 64;   // rows of a block
 constexpr int kBlockTiles = 8;   // weight column tiles of a block
 constexpr int kTileWaves = 3;    // waves per SIMD that fit
 constexpr int kTileGrid = 256 * kTileWaves;  // persistent workgroups, all resident
+constexpr int kTileRounds = 4;
 
 // Many rows: blocks of 64 rows x 128 weight columns (with SwiGLU 64 gate and
 // the same 64 up), taken in turn by persistent workgroups; the blocks of an
@@ -370,7 +377,7 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
       const int e = tid * 4 + i;
       int64_t first = 0, rows = 0;
       if (e < E) rows_between(a.offsets[e], a.counts[e], a.capacity, &first, &rows);
-      mine[i] = rows > kStreamRows ? (int32_t)((rows + kBlockRows - 1) / kBlockRows) : 0;
+      mine[i] = rows > a.stream_rows ? (int32_t)((rows + kBlockRows - 1) / kBlockRows) : 0;
       total += mine[i];
     }
     int32_t at = total;  // of this lane and those before it
@@ -719,6 +726,9 @@ ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const vo
   a.K = w4->in_features;
   a.N16 = (a.N + kTileN - 1) / kTileN;
   a.K128 = (a.K + kTileK - 1) / kTileK;
+  const int64_t blocks = (a.N16 * (w4->swiglu ? 2 : 1) + kBlockTiles - 1) / kBlockTiles;
+  const int64_t experts = capacity / kRows < w4->num_experts ? capacity / kRows : w4->num_experts;
+  a.stream_rows = experts * blocks >= kTileRounds * kTileGrid ? kRows : kStreamRows;
   with_product(fp8, w4->group, w_zeros != nullptr, w4->swiglu != 0,
                [&](auto p, auto g, auto z, auto s) {
                  // groups of 32: half the tiles, as four scales each leave no room
@@ -736,7 +746,7 @@ ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const vo
                    hipLaunchKernelGGL(
                        (product_stream_kernel<p.value, g.value, z.value, s.value, kTiles, false>),
                        grid, dim3(kStreamWaves * 64), 0, stream, a);
-                 if (capacity > kStreamRows)
+                 if (capacity > a.stream_rows)
                    hipLaunchKernelGGL((product_tile_kernel<p.value, g.value, z.value, s.value>),
                                       dim3(kTileGrid), dim3(256), 0, stream, a,
                                       w4->num_experts);

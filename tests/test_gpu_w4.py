@@ -464,3 +464,27 @@ def test_weights_are_those_of_the_object():
         w2 = ep.W4Experts.pack(dev(q[:, :, :]), s.cuda())
         buf = torch.zeros(5, 64, dtype=torch.bfloat16, device="cuda")
         w2.product(buf, None, off, cnt, out=buf.view(-1)[:240].view(5, 48))
+
+
+def test_many_experts_of_few_rows():
+    """Enough experts and columns that 17 to 32 rows are tiled, beside experts
+    of fewer rows, of more and of none: exact sums."""
+    E, K, N, group = 96, 64, 4200, 64
+    rng = np.random.default_rng(22)
+    counts = rng.integers(15, 34, size=E)
+    counts[[3, 50]] = 0
+    counts[[4, 60, 95]] = [1, 16, 32]
+    counts[[5, 70]] = [70, 130]
+    off = offsets_of(counts)
+    cap = int(off[-1]) - 3  # the last expert's last rows are cut off
+    assert min(cap // 16, E) * -(-(-(-N // 16)) // 8) >= 4 * 768
+    q, s, _ = draw(rng, E, K, N, group, False, False, True)
+    x, _, xv = draw_rows(rng, cap, K, False, True)
+    say("many experts of few rows")
+    out = packed(q, s, None, False).product(x, None, dev(off), dev(counts.astype(np.int32)))
+    w = ref.weights(q, s.float().numpy(), None, group)
+    got = out.float().cpu().numpy()
+    for e in range(E):
+        lo, hi = off[e], min(off[e + 1], cap)
+        want = bf16(xv[lo:hi] @ w[e].T).float().numpy()
+        assert np.array_equal(got[lo:hi], want), e
