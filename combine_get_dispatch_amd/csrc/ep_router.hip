@@ -696,6 +696,9 @@ __device__ __forceinline__ bool order_exactly(const RouteArgs &a, const L *row,
 // alike, by the sum of the row; a difference of two sums of two keys by four
 // times the one and twice the other, and by 2^-22 of a key.  bf16 logits are
 // whole within the front bits: equal means equal.
+// 4096 x 256 fp32, groups: 7.5 us; 131072 x 64 bf16: 15 (1.5 TB/s); 65536 x 256
+// fp32, sigmoid, bias, groups: 51 (1.4 TB/s), of which scores and lists are 28,
+// groups 9 and the 64-bit orders 14.  All keys in 64 bits: 152; k rounds: 144.
 template <typename L, int LPT, int V, int kMode, bool kShort>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   constexpr int kTokens = kThreads / LPT;
@@ -958,7 +961,8 @@ __device__ __forceinline__ float row_scores(const float (&x)[V], float (&p)[V]) 
 // One workgroup per tile of tokens.  A tile's part of sequence s goes to row
 // tile + s of the partial sums: along the tokens one of the two grows, so
 // every part has a row of its own.  The next token's row and ids are loaded
-// before the present one's are worked on.
+// before the present one's are worked on.  Bound by the scores' exponentials
+// and the LDS counts: 65536 x 256 bf16, sigmoid: 16 us, 2.2 TB/s.
 template <typename L, int LPT, int V, bool kSoftmax>
 __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
   constexpr int kTokens = kThreads / LPT;
@@ -1041,7 +1045,8 @@ constexpr int kSeqThreads = 1024;
 constexpr int kSeqCols = 64;  // experts of a workgroup
 
 // One workgroup per sequence and 64 experts: adds the sequence's parts in 64
-// bits, 16 slices of them side by side and then those in order.
+// bits, 16 slices of them side by side and then those in order.  A chain of
+// loads and barriers: 6 us for 1 x 64 as for 37 x 256.
 __global__ __launch_bounds__(kSeqThreads) void balance_seq_kernel(BalanceArgs a) {
   constexpr int kSlices = kSeqThreads / kSeqCols;
   __shared__ double sum_p[kSlices][kSeqCols];
@@ -1163,7 +1168,8 @@ constexpr int kGradFew = 512;
 // normalised over them, -s_e sum s u for all): it reaches its place in the row
 // through LDS, where only the places written are cleared again.  Bound by
 // reading the logits and writing the gradient: the next row is loaded before
-// the present one is worked on.  kLoss: prob_grad is given.
+// the present one is worked on.  65536 x 256 fp32, both gradients: 37 us, 3.7
+// TB/s of the 5.1 that a copy reaches.  kLoss: prob_grad is given.
 template <typename L, int LPT, int V, bool kSoftmax, bool kLoss>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(GradArgs a) {
   constexpr int kTokens = kThreads / LPT;
