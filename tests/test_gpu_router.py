@@ -498,3 +498,36 @@ def test_backward_against_differences():
                 d[t, e] = h
                 up, down = value(x + d), value(x - d)
                 assert abs(g[t, e] - (up - down) / (2 * h)) < h * h + 16 * 2.0 ** -22 / h
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 logits: a block of rows again and again has the same
+    selection, gates and gradient in every place, and counts that add up."""
+    B, n, E, k = 4096, 4100, 256, 8
+    T = B * n
+    assert T * E > 1 << 32
+    rng = np.random.default_rng(19)
+    x, t = draw_logits(rng, B, E, True)
+    u = torch.from_numpy(rng.normal(size=(B, k)).astype(np.float32)).cuda()
+    say("offsets past 32 bits")
+    small = ep.EpRouter(B, E, k, logits_dtype=torch.bfloat16)
+    xb = t.cuda()
+    ids, w = small.route(xb)
+    check_route((ids, w), x, k)
+    gb = small.backward(xb, ids, u)
+    r = ep.EpRouter(T, E, k, logits_dtype=torch.bfloat16)
+    xd = xb.repeat(n, 1)
+    got_ids, got_w = r.route(xd)
+    assert bool((got_ids.view(n, B, k) == ids).all())
+    assert bool((got_w.view(n, B, k) == w).all())
+    g = r.backward(xd, got_ids, u.repeat(n, 1))
+    for i in range(0, n, 100):  # in parts: the comparison needs memory too
+        assert bool((g.view(n, B, E)[i:i + 100] == gb).all()), i
+    r.balance_loss(xd, got_ids, 1.0)
+    r.check_status()
+    counts = torch.bincount(ids.reshape(-1).long(), minlength=E).cpu().numpy()
+    assert np.array_equal(r.counts[0].cpu().numpy(), counts * n)
+    assert r.seq_tokens.item() == T
+    mean = ref.probabilities(x, "softmax").mean(axis=0)
+    rel = (score_steps(x).max() + 256) * U32
+    assert np.all(np.abs(r.mean_probs[0].cpu().numpy() - mean) <= rel * mean)

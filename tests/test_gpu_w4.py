@@ -488,3 +488,37 @@ def test_many_experts_of_few_rows():
         lo, hi = off[e], min(off[e + 1], cap)
         want = bf16(xv[lo:hi] @ w[e].T).float().numpy()
         assert np.array_equal(got[lo:hi], want), e
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_past_32_bits(fp8):
+    """Experts whose rows of x lie past 2^32 values, and one whose output does.
+    Sums are exact: whole steps of 2^-5, and 7168 terms of random signs of at
+    most 256 (their mean square 30^2) stay far below the 2^19 that fp32 holds of
+    such steps."""
+    K, N = 7168, 1024
+    cap = (1 << 32) // N + 200
+    off = np.array([0, cap - 150, cap - 90, cap - 20], np.int32)
+    cnt = np.array([3, 9, 50, 30], np.int32)  # the last is cut off
+    rng = np.random.default_rng(23)
+    q, s, _ = draw(rng, 4, K, N, 128, False, False, True)
+    rows = np.concatenate([np.arange(o, min(o + c, cap)) for o, c in zip(off, cnt)])
+    x, xs, xv = draw_rows(rng, len(rows), K, fp8, True)
+    at = torch.from_numpy(rows).cuda()
+    say(f"rows past 32 bits fp8={fp8}")
+    big = torch.zeros((cap, K), dtype=x.dtype, device="cuda")
+    big[at] = x
+    scales = None
+    if fp8:
+        scales = torch.ones((cap, K // 128), device="cuda")
+        scales[at] = xs
+    out = torch.zeros((cap, N), dtype=torch.bfloat16, device="cuda")
+    packed(q, s, None, False).product(big, scales, dev(off), dev(cnt), out)
+    got = out[at].float().cpu().numpy()
+    w = ref.weights(q, s.float().numpy(), None, 128)
+    e = np.searchsorted(off, rows, side="right") - 1
+    for i in range(len(rows)):
+        want = w[e[i]] @ xv[i]
+        assert np.array_equal(got[i], bf16(want).float().numpy()), rows[i]
+    out[at] = 0
+    assert not bool(out.any())
