@@ -2,14 +2,15 @@
 // product on expert-major rows.  Contracts and the packed layout in
 // include/ep_moe.h.
 //
-// How 4 bits enter the matrix instructions exactly, without a conversion:
-//   bf16 rows: a code q in mantissa bits 3..6 of 0x3F80 is the bf16 1 + q/16,
-//     so sum x (1 + q/16) = X + sum(x q)/16 with X = sum x, and
-//     sum x (q - z) = 16 (sum x (1 + q/16) - X (1 + z/16));
-//   FP8 rows: a code q in the low bits of a byte is the E4M3 number q 2^-9 (a
-//     subnormal below 8, the first binade from there), so
-//     sum x (q - z) = 2^9 (sum x (q 2^-9) - z 2^-9 X).
+// How 4 bits enter the matrix instructions exactly, without a conversion: a code
+// q in mantissa bits 3..6 of 0x3F80 is the bf16 1 + q/16, so
+//     sum x (1 + q/16) = X + sum(x q)/16  with X = sum x, and
+//     sum x (q - z) = 16 (sum x (1 + q/16) - X (1 + z/16)).
 // X comes from the same instruction with a matrix of ones, once per row tile.
+// FP8 rows are turned into bf16, which holds every E4M3 number: the FP8
+// instruction keeps, of eight products, only what is less than 2^14 below the
+// largest (measured: of two, the smaller is lost from there on), while the bf16
+// one, of the same rate, sums them in 32 bits.
 // Group scales are applied to the fp32 sums of a group.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -24,6 +25,7 @@ namespace ep {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -137,55 +139,48 @@ __device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// The codes of one word as E4M3 q 2^-9, in the byte order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ long codes_fp8(uint32_t w) {
-  const uint64_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-  return (long)(lo | hi << 32);
+__device__ __forceinline__ f32x4 mul(bf16x8 x, bf16x8 w, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
-// Eight bytes of x in that order.
-__device__ __forceinline__ long rows_fp8(uint2 v) {
-  const uint64_t lo = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u);
-  const uint64_t hi = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);
-  return (long)(lo | hi << 32);
+__device__ __forceinline__ bf16x8 ones() {
+  return __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
 }
 
-// A wave's part of one weight tile's work: eight columns of x per lane and
-// matrix instruction.
+// dot of codes = kUnit * (dot of what codes_bf16() makes - zero_of(z) * sum of x)
+constexpr float kUnit = 0x1p4f;
+__device__ __forceinline__ float zero_of(float z) { return 1.0f + z * 0x1p-4f; }
+
+// The rows of x: eight columns per lane and matrix instruction, as they are
+// loaded and as the instruction takes them.
 template <bool FP8>
-struct Frag {
-  typedef bf16x8 X;
-  static __device__ __forceinline__ f32x4 mul(X x, X w, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ X codes(uint32_t w) { return codes_bf16(w); }
-  static __device__ __forceinline__ X ones() {
-    return __builtin_bit_cast(X, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-  }
+struct Rows {
+  typedef u32x4 Raw;
   static constexpr int kBytes = 2;
-  static __device__ __forceinline__ X load(const uint8_t *x, uint32_t at) {
-    return __builtin_bit_cast(
-        X, *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(x) + at));
+  static __device__ __forceinline__ Raw load(const uint8_t *x, uint32_t at) {
+    return *reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(x) + at);
   }
-  // dot of codes = kUnit * (dot of what codes() makes - zero_of(z) * sum of x)
-  static constexpr float kUnit = 0x1p4f;
-  static __device__ __forceinline__ float zero_of(float z) { return 1.0f + z * 0x1p-4f; }
+  static __device__ __forceinline__ bf16x8 bf16(Raw v) { return __builtin_bit_cast(bf16x8, v); }
 };
 
 template <>
-struct Frag<true> {
-  typedef long X;
-  static __device__ __forceinline__ f32x4 mul(X x, X w, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(x, w, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ X codes(uint32_t w) { return codes_fp8(w); }
-  static __device__ __forceinline__ X ones() { return 0x3838383838383838l; }
+struct Rows<true> {
+  typedef u32x2 Raw;
   static constexpr int kBytes = 1;
-  static __device__ __forceinline__ X load(const uint8_t *x, uint32_t at) {
-    return rows_fp8(*reinterpret_cast<const uint2 *>(x + at));
+  static __device__ __forceinline__ Raw load(const uint8_t *x, uint32_t at) {
+    return *reinterpret_cast<const u32x2 *>(x + at);
   }
-  static constexpr float kUnit = 0x1p9f;
-  static __device__ __forceinline__ float zero_of(float z) { return z * 0x1p-9f; }
+  static __device__ __forceinline__ bf16x8 bf16(Raw v) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[2 * i] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, false));
+      w[2 * i + 1] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, true));
+    }
+    return __builtin_bit_cast(bf16x8, w);
+  }
 };
 
 // Experts with at most kStreamRows rows are streamed (product_stream_kernel),
@@ -210,11 +205,11 @@ constexpr int64_t kInfinityCache = int64_t{256} << 20;
 // ONCE (non-temporal loads): where a call's weights exceed the Infinity Cache
 // nothing of them is found there again.  480 MB per call: 80 us with, 87
 // without; 34 MB per call, 100 MB in turn: 14.0 with, 12.0 without.
-// 480 MB (32 experts, 7168 x 2 x 2048, 4 rows each, FP8): 75 us, 6.4 TB/s of
-// the 6.9 that reading alone reaches.
+// 480 MB (32 experts, 7168 x 2 x 2048, 4 rows each, FP8; bf16: 78 us): 82 us a
+// call with the tiled kernel's empty launch, 5.9 TB/s.
 template <bool FP8, int GROUP, bool ZEROS, bool SWIGLU, int kTiles, bool ONCE>
 __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(ProductArgs a) {
-  typedef Frag<FP8> F;
+  typedef Rows<FP8> F;
   constexpr int kHalves = SWIGLU ? 2 : 1;
   constexpr int kOut = kTiles / kHalves;   // column tiles of the output
   constexpr int kGroups = kTileK / GROUP;  // groups in a tile
@@ -239,7 +234,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
     u32x4 w[kTiles];
     uint16_t s[kTiles][kGroups];
     uint8_t z[kTiles][kGroups];
-    typename F::X x[4];
+    typename F::Raw x[4];
     f32x4 sx;
   };
   for (int64_t r0 = 0; r0 < rows; r0 += kRows) {
@@ -271,7 +266,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = kt * kTileK + j * 32;
-        p.x[j] = typename F::X{};
+        p.x[j] = typename F::Raw{};
         if (GROUP == kTileK || c < a.K) p.x[j] = F::load(x0 + c * F::kBytes, xat);
       }
       if (FP8) {
@@ -282,23 +277,28 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
         }
       }
     };
+    // One step of all tiles after the other, so that a step's rows are turned
+    // into bf16 only then.
     const auto work = [&](const Piece &p) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        f32x4 sum = {0, 0, 0, 0};
+        f32x4 sum = {0, 0, 0, 0}, dot[kTiles];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum = F::mul(p.x[g * kPer + j], F::ones(), sum);
+        for (int i = 0; i < kTiles; ++i) dot[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const bf16x8 x = F::bf16(p.x[g * kPer + j]);
+          sum = mul(x, ones(), sum);
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) dot[i] = mul(x, codes_bf16(p.w[i][g * kPer + j]), dot[i]);
+        }
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-          f32x4 dot = {0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < kPer; ++j)
-            dot = F::mul(p.x[g * kPer + j], F::codes(p.w[i][g * kPer + j]), dot);
-          const float s = bf16_to_f32(p.s[i][g]) * F::kUnit;
-          const float z = F::zero_of(ZEROS ? (float)p.z[i][g] : 8.0f);
+          const float s = bf16_to_f32(p.s[i][g]) * kUnit;
+          const float z = zero_of(ZEROS ? (float)p.z[i][g] : 8.0f);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const float d = __builtin_fmaf(-z, sum[v], dot[v]);
+            const float d = __builtin_fmaf(-z, sum[v], dot[i][v]);
             acc[i][v] = __builtin_fmaf(FP8 ? s * p.sx[v] : s, d, acc[i][v]);
           }
         }
@@ -307,6 +307,9 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
     for (int kt = wave; kt < a.K128; kt += kStreamWaves) {
       Piece p;
       load(kt, p);
+      // all loads before the first wait: the compiler would put those of the
+      // scales behind it, a second trip to memory (FP8, 480 MB: 90 us)
+      __builtin_amdgcn_sched_barrier(0);
       work(p);
     }
 #pragma unroll
@@ -352,7 +355,7 @@ constexpr int kTileRounds = 4;
 // waiting for the loads of x in the same piece: 217.
 template <bool FP8, int GROUP, bool ZEROS, bool SWIGLU>
 __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductArgs a, int E) {
-  typedef Frag<FP8> F;
+  typedef Rows<FP8> F;
   constexpr int kHalves = SWIGLU ? 2 : 1;
   constexpr int kTiles = kBlockTiles / 4;       // of a wave
   constexpr int kOut = kTiles / kHalves;        // output tiles of a wave
@@ -360,7 +363,7 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
   constexpr int kPer = GROUP / 32;
   constexpr int kMT = kBlockRows / kRows;       // row tiles of a block
   static_assert(kMT == 4, "one row tile per wave is staged");
-  __shared__ __align__(16) typename F::X xs[2][kMT][4][64];
+  __shared__ __align__(16) bf16x8 xs[2][kMT][4][64];
   __shared__ float sums[2][kMT][kGroups][kRows];  // of x over a group
   __shared__ float sxs[2][kMT][kRows];            // FP8: scales of the rows
   __shared__ int32_t starts[EP_MAX_EXPERTS + 1];  // first block of each expert
@@ -442,26 +445,26 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
     const uint32_t xat = (uint32_t)(mine < left ? mine : left - 1) * a.K + quad * 8;
     const float *sx0 = FP8 ? a.x_scales + (first + r0) * a.K128 : nullptr;
     const uint32_t sxat = (uint32_t)(mine < left ? mine : left - 1) * a.K128;
-    typename F::X stage[4];
+    typename F::Raw stage[4];
     float row_scale = 0.0f;
     const auto load_x = [&](int kt) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = kt * kTileK + j * 32;
-        stage[j] = typename F::X{};
+        stage[j] = typename F::Raw{};
         if (GROUP == kTileK || c < a.K) stage[j] = F::load(x0 + (int64_t)c * F::kBytes, xat);
       }
       if (FP8) row_scale = (sx0 + kt)[sxat];
     };
     const auto stage_x = [&](int buf) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xs[buf][wave][j][lane] = stage[j];
+      for (int j = 0; j < 4; ++j) xs[buf][wave][j][lane] = F::bf16(stage[j]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum = F::mul(stage[g * kPer + j], F::ones(), sum);
-        if (!ZEROS) sum *= -F::zero_of(8.0f);
+        for (int j = 0; j < kPer; ++j) sum = mul(F::bf16(stage[g * kPer + j]), ones(), sum);
+        if (!ZEROS) sum *= -zero_of(8.0f);
         if (col == 0) *reinterpret_cast<f32x4 *>(&sums[buf][wave][g][quad * 4]) = sum;
       }
       if (FP8 && quad == 0) sxs[buf][wave][col] = row_scale;
@@ -513,8 +516,8 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
           raw[i] = codes[i];
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
-            s[i][g] = bf16_to_f32(scale[i][g]) * F::kUnit;
-            z[i][g] = -F::zero_of(ZEROS ? (float)zero[i][g] : 8.0f);
+            s[i][g] = bf16_to_f32(scale[i][g]) * kUnit;
+            z[i][g] = -zero_of(ZEROS ? (float)zero[i][g] : 8.0f);
           }
         }
         load_w(kt + 1 < last ? kt + 1 : last);
@@ -524,18 +527,18 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
           f32x4 dot[kM][kTiles];
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
-            typename F::X w[kTiles];
+            bf16x8 w[kTiles];
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) w[i] = F::codes(raw[i][g * kPer + j]);
+            for (int i = 0; i < kTiles; ++i) w[i] = codes_bf16(raw[i][g * kPer + j]);
 #pragma unroll
             for (int m = 0; m < kM; ++m) {
-              const typename F::X x = xs[buf][m][g * kPer + j][lane];
+              const bf16x8 x = xs[buf][m][g * kPer + j][lane];
               f32x4 sum;
               if (j == 0) sum = *reinterpret_cast<const f32x4 *>(&sums[buf][m][g][quad * 4]);
 #pragma unroll
               for (int i = 0; i < kTiles; ++i) {
                 if (j == 0) dot[m][i] = ZEROS ? sum * z[i][g] : sum;
-                dot[m][i] = F::mul(x, w[i], dot[m][i]);
+                dot[m][i] = mul(x, w[i], dot[m][i]);
               }
             }
           }

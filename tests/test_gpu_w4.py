@@ -522,3 +522,33 @@ def test_rows_past_32_bits(fp8):
         assert np.array_equal(got[i], bf16(want).float().numpy()), rows[i]
     out[at] = 0
     assert not bool(out.any())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("rows", [7, 130])
+def test_fp8_sums_keep_small_terms(group, zeros, rows):
+    """In every 128 columns one code of 448, whose weights are zero (code and
+    zero point equal), beside codes of n 2^-9, |n| <= 15: the result is made of
+    terms 2^15 and more below the largest that is summed.  It is exact: the sums
+    are of x (16 + q) / 16, whole steps of 2^-13, the large one at most
+    448 x 31 / 16 = 868 and the others together 127 x 15 x 31 steps, below 2^23
+    steps in all."""
+    rng = np.random.default_rng(31)
+    K, N = 384, 48
+    v = rng.integers(-15, 16, size=(rows, K)) * 2.0 ** -9
+    at = 128 * np.arange(K // 128) + rng.integers(0, 128, size=K // 128)
+    v[:, at] = 448.0 * rng.choice([-1.0, 1.0], size=(rows, len(at)))
+    q = rng.integers(0, 16, size=(1, N, K)).astype(np.uint8)
+    z = rng.integers(0, 16, size=(1, N, K // group)).astype(np.uint8) if zeros else None
+    q[:, :, at] = 8 if z is None else z[:, :, at // group]
+    s = bf16(np.ones((1, N, K // group)))
+    x = torch.from_numpy(v.astype(np.float32)).to(torch.float8_e4m3fn)
+    assert np.array_equal(x.double().numpy(), v)
+    say(f"fp8 sums group={group} zeros={zeros} rows={rows}")
+    out = packed(q, s, z, False).product(x.view(torch.uint8).cuda(),
+                                         torch.ones(rows, K // 128, device="cuda"),
+                                         dev(np.array([0], np.int32)),
+                                         dev(np.array([rows], np.int32)))
+    want = v @ ref.weights(q, s.float().numpy(), z, group)[0].T
+    assert np.array_equal(out.float().cpu().numpy(), bf16(want).float().numpy())
