@@ -3,10 +3,14 @@
 // include/ep_moe.h.
 //
 // How 4 bits enter the matrix instructions exactly, without a conversion: a code
-// q in mantissa bits 3..6 of 0x3F80 is the bf16 1 + q/16, so
-//     sum x (1 + q/16) = X + sum(x q)/16  with X = sum x, and
-//     sum x (q - z) = 16 (sum x (1 + q/16) - X (1 + z/16)).
-// X comes from the same instruction with a matrix of ones, once per row tile.
+// q in mantissa bits 3..6 of 0x3B80 is the bf16 u (1 + q/16) with u = 2^-8, so
+//     sum x u (1 + q/16) = X + u sum(x q)/16  with X = sum x u, and
+//     sum x (q - z) = 2^12 (sum x u (1 + q/16) - X (1 + z/16)).
+// X comes from the same instruction with a matrix of u, once per row tile.  With
+// u the sums over a group stay finite for every finite row (128 terms of at
+// most 31/16 u), and no bit is lost at the other end (x is a whole number of
+// 2^-133, a term of 2^-145).  The 2^12 comes last, so that only a result that
+// is itself out of range leaves it.
 // FP8 rows are turned into bf16, which holds every E4M3 number: the FP8
 // instruction keeps, of eight products, only what is less than 2^14 below the
 // largest (measured: of two, the smaller is lost from there on), while the bf16
@@ -124,18 +128,18 @@ __device__ __forceinline__ void expert_rows(const ProductArgs &a, int e, int64_t
   rows_between(uniform(a.offsets[e]), uniform(a.counts[e]), a.capacity, first, rows);
 }
 
-// The pairs of codes of one word as bf16 pairs 1 + q/16: a shift and one
+// The pairs of codes of one word as bf16 pairs u (1 + q/16): a shift and one
 // and-or each.  The instruction takes one constant from a scalar register and
 // none from its own encoding, so the other is kept in a vector register.
 __device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
-  uint32_t mask = 0x00780078u, one = 0x3F803F80u;
+  uint32_t mask = 0x00780078u, u = 0x3B803B80u;
   asm("" : "+s"(mask));
-  asm("" : "+v"(one));
+  asm("" : "+v"(u));
   u32x4 v;
-  v[0] = ((w << 3) & mask) | one;
-  v[1] = ((w >> 1) & mask) | one;
-  v[2] = ((w >> 5) & mask) | one;
-  v[3] = ((w >> 9) & mask) | one;
+  v[0] = ((w << 3) & mask) | u;
+  v[1] = ((w >> 1) & mask) | u;
+  v[2] = ((w >> 5) & mask) | u;
+  v[3] = ((w >> 9) & mask) | u;
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -143,12 +147,12 @@ __device__ __forceinline__ f32x4 mul(bf16x8 x, bf16x8 w, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ bf16x8 ones() {
-  return __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+__device__ __forceinline__ bf16x8 units() {
+  return __builtin_bit_cast(bf16x8, u32x4{0x3B803B80u, 0x3B803B80u, 0x3B803B80u, 0x3B803B80u});
 }
 
-// dot of codes = kUnit * (dot of what codes_bf16() makes - zero_of(z) * sum of x)
-constexpr float kUnit = 0x1p4f;
+// dot of codes = kUnit * (dot of what codes_bf16() makes - zero_of(z) * dot of units())
+constexpr float kUnit = 0x1p12f;
 __device__ __forceinline__ float zero_of(float z) { return 1.0f + z * 0x1p-4f; }
 
 // The rows of x: eight columns per lane and matrix instruction, as they are
@@ -288,18 +292,18 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const bf16x8 x = F::bf16(p.x[g * kPer + j]);
-          sum = mul(x, ones(), sum);
+          sum = mul(x, units(), sum);
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) dot[i] = mul(x, codes_bf16(p.w[i][g * kPer + j]), dot[i]);
         }
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-          const float s = bf16_to_f32(p.s[i][g]) * kUnit;
+          const float s = bf16_to_f32(p.s[i][g]);
           const float z = zero_of(ZEROS ? (float)p.z[i][g] : 8.0f);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             const float d = __builtin_fmaf(-z, sum[v], dot[i][v]);
-            acc[i][v] = __builtin_fmaf(FP8 ? s * p.sx[v] : s, d, acc[i][v]);
+            acc[i][v] = __builtin_fmaf(s, FP8 ? d * p.sx[v] : d, acc[i][v]);
           }
         }
       }
@@ -326,7 +330,8 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
         y += part[s][i][at];
         if (SWIGLU) up += part[s][kOut + i][at];
       }
-      if (SWIGLU) y = silu(y) * up;
+      y *= kUnit;
+      if (SWIGLU) y = silu(y) * (up * kUnit);
       if (m < left && n < a.N) a.out[(first + r0 + m) * a.N + n] = f32_to_bf16(y);
     }
     __syncthreads();
@@ -463,7 +468,7 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
       for (int g = 0; g < kGroups; ++g) {
         f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum = mul(F::bf16(stage[g * kPer + j]), ones(), sum);
+        for (int j = 0; j < kPer; ++j) sum = mul(F::bf16(stage[g * kPer + j]), units(), sum);
         if (!ZEROS) sum *= -zero_of(8.0f);
         if (col == 0) *reinterpret_cast<f32x4 *>(&sums[buf][wave][g][quad * 4]) = sum;
       }
@@ -516,7 +521,7 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
           raw[i] = codes[i];
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
-            s[i][g] = bf16_to_f32(scale[i][g]) * kUnit;
+            s[i][g] = bf16_to_f32(scale[i][g]);
             z[i][g] = -zero_of(ZEROS ? (float)zero[i][g] : 8.0f);
           }
         }
@@ -550,7 +555,7 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
             for (int i = 0; i < kTiles; ++i)
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                acc[m][i][v] = __builtin_fmaf(FP8 ? s[i][g] * sx[v] : s[i][g], dot[m][i][v],
+                acc[m][i][v] = __builtin_fmaf(s[i][g], FP8 ? dot[m][i][v] * sx[v] : dot[m][i][v],
                                               acc[m][i][v]);
           }
         }
@@ -570,8 +575,8 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
           uint16_t *row = out0 + (int64_t)(m * kRows + v) * a.N;
 #pragma unroll
           for (int i = 0; i < kOut; ++i) {
-            float y = acc[m][i][v];
-            if (SWIGLU) y = silu(y) * acc[m][kOut + i][v];
+            float y = acc[m][i][v] * kUnit;
+            if (SWIGLU) y = silu(y) * (acc[m][kOut + i][v] * kUnit);
             if ((ot + i) * kTileN + col < a.N) row[at + i * kTileN] = f32_to_bf16(y);
           }
         }

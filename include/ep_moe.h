@@ -200,7 +200,9 @@ ep_status_t ep_w4_pack(const ep_w4_t *w4, const uint8_t *codes, const uint16_t *
  * summed in fp32, and out[r, n] = bf16(y[r, n]), or with swiglu
  * bf16(silu(y_gate[r, n]) * y_up[r, n]).  Codes and rows enter the matrix
  * instructions exactly, scales are applied in fp32; the output's is the only
- * rounding below fp32.
+ * rounding below fp32.  Rows and scales may be any finite values: y is finite
+ * where the sums of groups and of the experts' row are in fp32's range, and
+ * each group adds an error of at most (1 + |scale|) 2^-138 at its lower end.
  *
  *   x_dtype       EP_DTYPE_BF16: x bf16 [capacity, K]
  *                 EP_DTYPE_FP8_E4M3: x uint8 [capacity, K] and x_scales fp32

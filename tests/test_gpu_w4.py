@@ -552,3 +552,40 @@ def test_fp8_sums_keep_small_terms(group, zeros, rows):
                                          dev(np.array([rows], np.int32)))
     want = v @ ref.weights(q, s.float().numpy(), z, group)[0].T
     assert np.array_equal(out.float().cpu().numpy(), bf16(want).float().numpy())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [5, 70])
+def test_product_over_the_whole_range(group, zeros, fp8, rows):
+    """Rows at the top and the bottom of their types and scales that bring the
+    result back: finite wherever the result is.  Exact: rows are one power of
+    two with any signs and each matrix has one scale, so a sum is at most
+    256 x 31 steps of a power of two."""
+    rng = np.random.default_rng(41)
+    K, N = 256, 40
+    if fp8:  # power of the codes, of the rows' scales, of the weights' scales
+        cases = [(8, 119, -30), (-9, 115, 12), (8, -110, 120), (-9, -60, 100), (8, -126, 20)]
+    else:
+        cases = [(127, 0, -30), (127, 0, -120), (-100, 0, 120), (-126, 0, 126), (-133, 0, 100),
+                 (0, 0, 110), (0, 0, -110)]
+    q = rng.integers(0, 16, size=(1, N, K)).astype(np.uint8)
+    z = rng.integers(0, 16, size=(1, N, K // group)).astype(np.uint8) if zeros else None
+    sign = rng.choice([-1.0, 1.0], size=(rows, K))
+    off, cnt = dev(np.array([0], np.int32)), dev(np.array([rows], np.int32))
+    for px, ps, pw in cases:
+        say(f"range group={group} zeros={zeros} fp8={fp8} rows={rows} powers={px, ps, pw}")
+        v = torch.from_numpy(sign * 2.0 ** px)
+        x, xs = v.to(torch.bfloat16), None
+        if fp8:
+            x = v.to(torch.float8_e4m3fn)
+            xs = torch.full((rows, K // 128), 2.0 ** ps, device="cuda")
+        assert torch.equal(x.double(), v)
+        s = torch.full((1, N, K // group), 2.0 ** pw).to(torch.bfloat16)
+        out = packed(q, s, z, False).product((x.view(torch.uint8) if fp8 else x).cuda(), xs, off,
+                                             cnt)
+        w = ref.weights(q, s.double().numpy(), z, group)[0]
+        want = torch.from_numpy((sign @ w.T) * 2.0 ** (px + ps)).to(torch.bfloat16)
+        assert bool(torch.isfinite(want).all())
+        assert torch.equal(out.cpu(), want)
