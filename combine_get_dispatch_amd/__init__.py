@@ -164,6 +164,18 @@ def _stream(stream):
     return ctypes.c_void_p(_current_stream())
 
 
+def _empty(stream, *size, **kw):
+    """torch.empty for a call on `stream` (a raw handle, None: the current
+    one), from that stream's memory: a block of another stream's may still be
+    in use by work queued there, which this call would not wait for."""
+    import torch
+
+    if stream is None:
+        return torch.empty(*size, **kw)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=kw["device"])):
+        return torch.empty(*size, **kw)
+
+
 def _ptr(t, dtype=None, shape=None, name="tensor"):
     """Device pointer of a contiguous CUDA tensor (None passes NULL)."""
     if t is None:
@@ -530,7 +542,9 @@ def ep_time_next_kernel(start, stop):
 class EpBuffers:
     """Device tensors for one (T, H, k, E, R, A, dtype) configuration, and
     the three calls on them.  Tensors are allocated once with torch and
-    reused; outputs are views into them."""
+    reused; outputs are views into them.  They are made on the current stream:
+    another stream waits for it before its first call.  A result that a call
+    allocates belongs to the stream the call runs on."""
 
     def __init__(self, num_tokens, hidden, num_topk, num_experts, num_ranks,
                  expert_alignment=1, fp8=False, capacity=None, device="cuda", zero_padding=True):
@@ -707,10 +721,8 @@ class EpBuffers:
         return self.out
 
     def dispatch_backward(self, grad_recv_x, grad_x=None, stream=None):
-        import torch
-
         if grad_x is None:
-            grad_x = torch.empty_like(self.out)
+            grad_x = _empty(stream, self.out.shape, dtype=self.out.dtype, device=self.out.device)
         ep_dispatch_backward(self.handle, grad_recv_x, grad_x, stream=stream)
         return grad_x
 
@@ -719,15 +731,15 @@ class EpBuffers:
         import torch
 
         if grad_expert_out is None:
-            grad_expert_out = torch.empty((self.capacity, self.cfg.hidden), dtype=torch.bfloat16,
-                                          device=grad_out.device)
+            grad_expert_out = _empty(stream, (self.capacity, self.cfg.hidden),
+                                     dtype=torch.bfloat16, device=grad_out.device)
         ep_combine_backward(self.handle, grad_out, topk_weights, expert_out, grad_expert_out,
                             grad_weights, stream=stream)
         return grad_expert_out
 
     # --- non-expanded (rank-deduplicated) path; its buffers are made on first use
 
-    def _ranked_buffers(self):
+    def _ranked_buffers(self, stream):
         import torch
 
         if getattr(self, "ne_x", None) is not None:
@@ -737,19 +749,19 @@ class EpBuffers:
         qc = ep_ranked_capacity_rows(c)
         self.ranked_capacity = qc
         i32 = dict(dtype=torch.int32, device=dev)
-        self.ne_x = torch.empty((qc, H), dtype=torch.uint8 if self.fp8 else torch.bfloat16,
-                                device=dev)
-        self.ne_scales = (torch.empty((qc, H // 128), dtype=torch.float32, device=dev)
+        self.ne_x = _empty(stream, (qc, H), dtype=torch.uint8 if self.fp8 else torch.bfloat16,
+                           device=dev)
+        self.ne_scales = (_empty(stream, (qc, H // 128), dtype=torch.float32, device=dev)
                           if self.fp8 else None)
-        self.ne_topk_idx = torch.empty((qc, k), **i32)
-        self.ne_topk_weights = torch.empty((qc, k), dtype=torch.float32, device=dev)
-        self.ne_src = torch.empty(qc, **i32)
-        self.rank_token_offsets = torch.empty(R + 1, **i32)
-        self.tok_rank_row = torch.empty((T, R), **i32)
+        self.ne_topk_idx = _empty(stream, (qc, k), **i32)
+        self.ne_topk_weights = _empty(stream, (qc, k), dtype=torch.float32, device=dev)
+        self.ne_src = _empty(stream, qc, **i32)
+        self.rank_token_offsets = _empty(stream, R + 1, **i32)
+        self.tok_rank_row = _empty(stream, (T, R), **i32)
         self.partials = None
 
     def dispatch_ranked(self, x, topk_idx, topk_weights, stream=None):
-        self._ranked_buffers()
+        self._ranked_buffers(stream)
         self.ranked = ep_dispatch_ranked(
             self.cfg, EP_DTYPE_FP8_E4M3 if self.fp8 else EP_DTYPE_BF16, x, topk_idx, topk_weights,
             self.expert_offsets, self.workspace, self.capacity, self.ranked_capacity, self.ne_x,
@@ -770,8 +782,8 @@ class EpBuffers:
         import torch
 
         if self.partials is None:
-            self.partials = torch.empty((self.ranked_capacity, self.cfg.hidden),
-                                        dtype=torch.float32, device=self.out.device)
+            self.partials = _empty(stream, (self.ranked_capacity, self.cfg.hidden),
+                                   dtype=torch.float32, device=self.out.device)
         out = self.out if out is None else out
         ep_combine_ranked(self.ranked, expert_out, weighted, self.partials, out, stream=stream)
         return out

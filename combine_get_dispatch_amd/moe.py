@@ -10,7 +10,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import EP_DTYPE_BF16, EP_DTYPE_F32, EP_DTYPE_FP8_E4M3, _check, _ptr, _stream, lib
+from . import (EP_DTYPE_BF16, EP_DTYPE_F32, EP_DTYPE_FP8_E4M3, _check, _empty, _ptr, _stream,
+               lib)
 
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 _SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
@@ -240,7 +241,9 @@ class EpRouter:
     """The router of one configuration: selection, balance loss and their
     gradient, with the outputs and the workspace allocated once.  Results are
     views of these buffers: the next call of the same method overwrites them.
-    One call at a time may use them (as the workspace of EpBuffers)."""
+    One call at a time may use them (as the workspace of EpBuffers).  They are
+    made on the current stream: another stream waits for it before its first
+    call."""
 
     def __init__(self, num_tokens, num_experts, num_topk, score="softmax", groups=1,
                  topk_groups=1, group_topn=1, normalize=True, scale=1.0, logits_dtype=None,
@@ -362,20 +365,23 @@ class W4Experts:
         cfg = ep_w4_t(E, K, N, group, 1 if swiglu else 0)
         ep_w4_packed_sizes(cfg)
         n16, k128, dev = -(-N // 16), -(-K // 128), codes.device
-        w_codes = torch.empty((E, halves, n16, k128, 1024), dtype=torch.uint8, device=dev)
-        w_scales = torch.empty((E, halves, n16, K // group, 16), dtype=torch.bfloat16, device=dev)
-        w_zeros = torch.empty_like(w_scales, dtype=torch.uint8) if zeros is not None else None
+        w_codes = _empty(stream, (E, halves, n16, k128, 1024), dtype=torch.uint8, device=dev)
+        groups = (E, halves, n16, K // group, 16)
+        w_scales = _empty(stream, groups, dtype=torch.bfloat16, device=dev)
+        w_zeros = (_empty(stream, groups, dtype=torch.uint8, device=dev)
+                   if zeros is not None else None)
         ep_w4_pack(cfg, codes, scales, zeros, w_codes, w_scales, w_zeros, stream=stream)
         return cls(w_codes, w_scales, w_zeros, N, K, group)
 
     def product(self, x, x_scales, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, out_features]: each expert's rows times its weights.
-        Rows that are no expert's are left as they are."""
+        Rows that are no expert's are left as they are.  Without ``out`` the
+        result belongs to the stream the call runs on."""
         import torch
 
         if out is None:
-            out = torch.empty((x.shape[0], self.cfg.out_features), dtype=torch.bfloat16,
-                              device=x.device)
+            out = _empty(stream, (x.shape[0], self.cfg.out_features), dtype=torch.bfloat16,
+                         device=x.device)
         _product(self.cfg, self._ref, x, x_scales, self._weights, expert_offsets,
                  num_tokens_per_expert, out, stream)
         return out
