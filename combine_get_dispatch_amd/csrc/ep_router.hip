@@ -265,35 +265,48 @@ struct Best2<float> {
   __device__ __forceinline__ float key(int topn) const {
     return topn == 2 && second > -INFINITY ? fmaxf(first + second, -FLT_MAX) : first;
   }
+  // what its rounding goes by: the two may cancel
+  __device__ __forceinline__ float size(int topn) const {
+    return topn == 2 && second > -INFINITY ? fmaxf(fabsf(first), fabsf(second)) : fabsf(first);
+  }
 };
 
+// How far a key in 32 bits may be off by the rounding of its own bias and sum:
+// of one key 2^-24 of itself, of a group's sum of two 2^-22 of the larger.  Two
+// neighbours are compared by the lower one: a higher one of more than twice its
+// size is far enough away.
+constexpr float kKeyStep = 0x1p-20f;
+constexpr float kGroupStep = 0x1p-21f;
+
 // The groups kept, as 64 bits, from the group keys in LDS (written by lanes of
-// this token, and read here after the wave has met).  Lane l ranks groups
-// l, l + LPT, ...; near: a kept and a dropped group are within `margin`.
-template <typename K, int LPT>
-__device__ __forceinline__ uint64_t kept_of(const RouteArgs &a, int l, K *group_key,
-                                            K margin, bool *near) {
-  const K none = -INFINITY;
+// this token, and read here after the wave has met; behind them, if near is
+// given, their sizes).  Lane l ranks groups l, l + LPT, ...; near: a kept and a
+// dropped group are within `margin` and what their own roundings add.
+template <int LPT>
+__device__ __forceinline__ uint64_t kept_of(const RouteArgs &a, int l, float *group_key,
+                                            float margin, bool *near) {
+  const float none = -INFINITY;
   if (l < (-a.G & 3)) group_key[a.G + l] = none;
   wave_sync();
   uint32_t kept[2] = {0, 0};
-  K low = INFINITY, high = none;  // worst kept, best dropped
+  float low = INFINITY, high = none;  // the lowest a kept one can be, the highest a dropped one
   for (int g = l; g < a.G; g += LPT) {
-    const K v = group_key[g];
+    const float v = group_key[g];
     if (!(v > none)) continue;
+    const float off = near != nullptr ? kGroupStep * group_key[EP_MAX_GROUPS + g] : 0.0f;
     int before = 0;
     for (int h = 0; h < a.G; h += 4) {  // the keys are filled up to fours
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const K o = group_key[h + i];
+        const float o = group_key[h + i];
         before += o > v || (o == v && h + i < g);
       }
     }
     if (before < a.topk_groups) {
       kept[g / 32] |= 1u << (g % 32);
-      low = v < low ? v : low;
+      low = fminf(low, v - off);
     } else {
-      high = v > high ? v : high;
+      high = fmaxf(high, v + off);
     }
   }
   if (near != nullptr) {
@@ -321,8 +334,9 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &a, float (&key)[V],
     }
     each_step<LPT>([&](auto s) { best.template join<s.value>(); });
     if (l == 0) group_key[g] = best.key(a.group_topn);
+    if (l == 0 && near != nullptr) group_key[EP_MAX_GROUPS + g] = best.size(a.group_topn);
   }
-  const uint64_t kept = kept_of<float, LPT>(a, l, group_key, margin, near);
+  const uint64_t kept = kept_of<LPT>(a, l, group_key, margin, near);
   wave_sync();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -355,9 +369,12 @@ __device__ __forceinline__ void keep_even_groups(const RouteArgs &a, float (&key
 #pragma unroll
   for (int q = 0; q < V / kQuad; ++q) {
     const int g = (q * LPT + l) >> a.group_steps;
-    if (leader && g < a.G) group_key[g] = best[q].key(a.group_topn);
+    if (leader && g < a.G) {
+      group_key[g] = best[q].key(a.group_topn);
+      if (near != nullptr) group_key[EP_MAX_GROUPS + g] = best[q].size(a.group_topn);
+    }
   }
-  const uint64_t kept = kept_of<float, LPT>(a, l, group_key, margin, near);
+  const uint64_t kept = kept_of<LPT>(a, l, group_key, margin, near);
   wave_sync();
 #pragma unroll
   for (int q = 0; q < V / kQuad; ++q) {
@@ -372,7 +389,7 @@ __device__ __forceinline__ void keep_even_groups(const RouteArgs &a, float (&key
 // The k best of one token's keys, in order, by k rounds of a search; slot j is
 // given to lane j % LPT as its mine[j / LPT].  A key of -inf is never selected.
 // near (kCheck): two neighbours in the order, the first one not selected
-// among them, are within `margin`.
+// among them, are within `margin` and what their own roundings add.
 template <int LPT, int V, bool kCheck>
 __device__ __forceinline__ void best_by_rounds(const RouteArgs &a, float (&key)[V], int l,
                                                int (&mine)[32 / (LPT < 32 ? LPT : 32)],
@@ -398,7 +415,7 @@ __device__ __forceinline__ void best_by_rounds(const RouteArgs &a, float (&key)[
       at = take ? oat : at;
     });
     if (!(best > none)) break;
-    if (kCheck && !(last - best > margin)) *near = true;
+    if (kCheck && !(last - best > margin + kKeyStep * fabsf(best))) *near = true;
     last = best;
 #pragma unroll
     for (int s = 0; s < 32 / (LPT < 32 ? LPT : 32); ++s)
@@ -690,12 +707,13 @@ __device__ __forceinline__ bool order_exactly(const RouteArgs &a, const L *row,
 //     32-bit keys.
 //   Groups, or neighbours of that search, within the margin: all of the token's
 //     keys and groups in 64 bits (select_exactly).
-// The margin is 2^-19 of the best score and key there can be, together 2^-18
-// of the best score: a score is off by at most 2^-22 of the best by its
-// exponential and quotient, those of a softmax by 2^-19.6 of themselves, all
-// alike, by the sum of the row; a difference of two sums of two keys by four
-// times the one and twice the other, and by 2^-22 of a key.  bf16 logits are
-// whole within the front bits: equal means equal.
+// The margin is 2^-18 of the best score there can be: a score is off by at most
+// 2^-22 of the best by its exponential and quotient, those of a softmax by
+// 2^-19.6 of themselves, all alike, by the sum of the row; a difference of two
+// sums of two keys by four times the one and twice the other.  What the biases
+// add goes by the keys compared (kKeyStep, kGroupStep), not by the largest bias,
+// so that experts put last by a large finite one leave the others' order to 32
+// bits.  bf16 logits are whole within the front bits: equal means equal.
 // 4096 x 256 fp32, groups: 7.5 us; 131072 x 64 bf16: 15 (1.5 TB/s); 65536 x 256
 // fp32, sigmoid, bias, groups: 51 (1.4 TB/s), of which scores and lists are 28,
 // groups 9 and the 64-bit orders 14.  All keys in 64 bits: 152; k rounds: 144.
@@ -713,7 +731,6 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   const int slot = threadIdx.x / LPT;
   double *group_key = group_keys[slot];
   const int64_t stride = (int64_t)gridDim.x * kTokens;
-  float bias_size = 0.0f;
   int bias_bad = 0;
   if constexpr (kScores) {
     for (int e = threadIdx.x; e < LPT * V; e += kThreads)
@@ -723,10 +740,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     for (int i = 0; i < V; ++i) {
       const float b = biases[expert_of<LPT, V>(l, i)];
       bias_bad |= !(b < INFINITY);
-      bias_size = fmaxf(bias_size, b > -INFINITY ? fabsf(b) : 0.0f);
     }
     bias_bad = token_or<LPT>(bias_bad);
-    bias_size = token_max<LPT>(bias_size);
   }
   const L *logits = static_cast<const L *>(a.logits);
   // the first token of the wave, and this lane's: the whole wave stays in the
@@ -763,7 +778,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
       // a row of -inf has no scores: any finite value for its maximum
       const float best =
           score_keys<LPT, V, kMode>(x, xmax > -INFINITY ? xmax : 0.0f, biases, l, key);
-      margin = 0x1p-19f * (2.0f * best + bias_size);  // no key is larger than best + bias_size
+      margin = 0x1p-18f * best;
       if (bias_bad) {
 #pragma unroll
         for (int i = 0; i < V; ++i) bad |= !(key[i] < INFINITY);
@@ -811,13 +826,18 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
       if constexpr (kScores || sizeof(L) == 4) {
         // own against the next in the order; after the eighth, any other key that
         // is not clearly below it
-        if (l < a.k && l + 1 < kList && own != 0 && after != 0)
-          open = !(key_in<kBits>(own, true) - key_in<kBits>(after, false) > margin);
+        if (l < a.k && l + 1 < kList && own != 0 && after != 0) {
+          const float next_key = key_in<kBits>(after, false);
+          open = !(key_in<kBits>(own, true) - next_key >
+                   (kScores ? margin + kKeyStep * fabsf(next_key) : 0.0f));
+        }
         uint32_t kth = list[0];
 #pragma unroll
         for (int j = 1; j < kList; ++j) kth = j < a.k ? list[j] : kth;
+        const float kth_key = key_in<kBits>(kth, true);
+        const float below = kScores ? margin + kKeyStep * fabsf(kth_key) : 0.0f;
         const float least =  // never -inf: keys of -inf are not among them
-            kth != 0 ? fmaxf(key_in<kBits>(kth, true) - margin, -FLT_MAX) : -FLT_MAX;
+            kth != 0 ? fmaxf(kth_key - below, -FLT_MAX) : -FLT_MAX;
         if (a.k == kList) {
           int above = 0;
 #pragma unroll

@@ -531,3 +531,66 @@ def test_offsets_past_32_bits():
     mean = ref.probabilities(x, "softmax").mean(axis=0)
     rel = (score_steps(x).max() + 256) * U32
     assert np.all(np.abs(r.mean_probs[0].cpu().numpy() - mean) <= rel * mean)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_large_finite_biases(score):
+    """Experts put last or first by large finite biases of either sign: the
+    others' order is that of their own keys, sums of two keys that cancel
+    included."""
+    rng = np.random.default_rng(61)
+    for E, G, tg, topn, k in ((64, 1, 1, 1, 8), (64, 1, 1, 1, 3), (64, 8, 3, 2, 6), (60, 5, 2, 2, 6),
+                              (256, 8, 4, 2, 8), (256, 8, 4, 1, 8), (100, 1, 1, 1, 20),
+                              (512, 16, 4, 2, 12), (1024, 8, 2, 2, 8)):
+        T = 31
+        x = rng.normal(size=(T, E)).astype(np.float32)
+        x[::3] = np.round(x[::3] * 4) / 4  # equal keys among them
+        for big in (1e4, 1e9, 3e38):
+            for signs in ([-1], [1], [-1, 1]):
+                bias = (rng.normal(size=E) * 0.05).astype(np.float32)
+                at = rng.permutation(E)[: max(2, E // 8)]
+                bias[at] = np.float32(big) * rng.choice(signs, size=len(at)).astype(np.float32)
+                # neighbours in size that round apart, and pairs that add up to nearly nothing
+                bias[at[: len(at) // 2]] *= np.float32(1 - 2.0 ** -20)
+                say(f"large biases E={E} G={G} topn={topn} k={k} {score} big={big} signs={signs}")
+                r = ep.EpRouter(T, E, k, score=score, groups=G, topk_groups=tg, group_topn=topn)
+                got = r.route(dev(x), bias=dev(bias))
+                r.check_status()
+                check_route(got, x, k, score=score, bias=bias, groups=G, topk_groups=tg,
+                            group_topn=topn)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,tg,topn", [(256, 8, 4, 2), (64, 1, 1, 1)])
+def test_route_with_experts_put_last_costs_no_more(score, E, G, tg, topn):
+    """A large finite bias on some experts leaves the other tokens' selection to
+    32 bits: at most twice the time of the call without it (64-bit keys for all
+    tokens take ten times as long)."""
+    T, k = 65536, 8
+    rng = np.random.default_rng(62)
+    x = dev(rng.normal(size=(T, E)).astype(np.float32))
+    bias = (rng.normal(size=E) * 0.05).astype(np.float32)
+    r = ep.EpRouter(T, E, k, score=score, groups=G, topk_groups=tg, group_topn=topn)
+
+    def best_time(b):
+        b = dev(b)
+        times = []
+        for _ in range(5):
+            start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(5):
+                r.route(x, bias=b)
+            stop.record()
+            stop.synchronize()
+            times.append(start.elapsed_time(stop) / 5)
+        return min(times)
+
+    say(f"time with experts put last E={E} G={G} {score}")
+    plain = best_time(bias)
+    for big in (-1e4, -1e9, float(np.finfo(np.float32).min)):
+        last = bias.copy()
+        last[::17] = big
+        took = best_time(last)
+        say(f"  plain {1e3 * plain:.1f} us, bias {big:g}: {1e3 * took:.1f} us")
+        assert took <= 2 * plain
+    r.check_status()
