@@ -186,7 +186,10 @@ __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
 // exp of every score of a row: the hardware's exp2 of x log2(e), off by
-// (|x| + 3) 2^-24 of it.
+// (1.23 |x| + 3) 2^-24 of it: the product's rounding 1 |x|, its fp32 constant
+// 0.22 |x|, the exp2 2.  (A second fma for the constant's rest would be two
+// instructions more on a path that instructions bound, for scores whose own
+// steps are far larger.)
 __device__ __forceinline__ float exp_fast(float v) {
   return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f);
 }
@@ -707,10 +710,13 @@ __device__ __forceinline__ bool order_exactly(const RouteArgs &a, const L *row,
 //     32-bit keys.
 //   Groups, or neighbours of that search, within the margin: all of the token's
 //     keys and groups in 64 bits (select_exactly).
-// The margin is 2^-18 of the best score there can be: a score is off by at most
-// 2^-22 of the best by its exponential and quotient, those of a softmax by
-// 2^-19.6 of themselves, all alike, by the sum of the row; a difference of two
-// sums of two keys by four times the one and twice the other.  What the biases
+// The margin is 2^-18 of the best score there can be, 2^-17 for a softmax.  In
+// steps of 2^-24 of the best: a score is off by 4 by its exponential and quotient
+// (s (1 - s) (1.23 |x| + 3) + 3 s of a sigmoid, e^-t (1.23 t + 3) + 1 of a
+// softmax), the scores of a softmax, all alike, by 31 of themselves by the sum of
+// the row (15 additions in a lane, 6 between lanes, 3 + 1.23 t w / (w + 1) <= 8.5
+// for the terms with w = 1023 e^-t, a quotient).  A difference of two sums of two
+// keys is off by 4 x 4 + 2 x 31 = 78 at most.  What the biases
 // add goes by the keys compared (kKeyStep, kGroupStep), not by the largest bias,
 // so that experts put last by a large finite one leave the others' order to 32
 // bits.  bf16 logits are whole within the front bits: equal means equal.
@@ -778,7 +784,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
       // a row of -inf has no scores: any finite value for its maximum
       const float best =
           score_keys<LPT, V, kMode>(x, xmax > -INFINITY ? xmax : 0.0f, biases, l, key);
-      margin = 0x1p-18f * best;
+      margin = (kMode == kBySoftmax ? 0x1p-17f : 0x1p-18f) * best;
       if (bias_bad) {
 #pragma unroll
         for (int i = 0; i < V; ++i) bad |= !(key[i] < INFINITY);

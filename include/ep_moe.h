@@ -106,7 +106,11 @@ ep_status_t ep_balance_workspace_bytes(const ep_router_t *router, int32_t num_se
  *   loss             coef / S' * sum_s sum_e f[s, e] P[s, e],  S' sequences with N_s > 0
  *   prob_grad[s, e]  coef * f[s, e] / (S' * N_s) = d loss / d p[t, e]  (0 if N_s = 0)
  *
- * The counts are constants to the gradient, as a count has none.
+ * The counts are constants to the gradient, as a count has none.  A score here
+ * and in ep_route_backward is exp2(x log2 e) of fp32, off by
+ * (1.23 |x| + 3) 2^-24 of itself (x the logit, of a softmax less the row's
+ * largest), and 0 below 2^-126; sums over a tile of at most 256 tokens are fp32,
+ * those over tiles fp64.
  *
  *   router       num_tokens, num_experts, num_topk and score are used
  *   topk_idx     [T, k] int32; an id outside [-1, E) counts as -1 and sets

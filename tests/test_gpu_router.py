@@ -594,3 +594,24 @@ def test_route_with_experts_put_last_costs_no_more(score, E, G, tg, topn):
         say(f"  plain {1e3 * plain:.1f} us, bias {big:g}: {1e3 * took:.1f} us")
         assert took <= 2 * plain
     r.check_status()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_fast_exponential_on_the_device(bf16):
+    """Softmax rows of two experts, each a sequence of its own, so that
+    mean_probs is exp(x) / (1 + exp(x)): the exponential's bound of
+    (1.23 |x| + 3) 2^-24, a sum, a quotient and a product, and the mean."""
+    T = 4000
+    v = np.linspace(0, 87, T).astype(np.float32)
+    x = np.stack([np.zeros(T, np.float32), -v], axis=1)
+    t = torch.from_numpy(x)
+    t = t.bfloat16() if bf16 else t
+    x = t.double().numpy()
+    ids = dev(np.zeros((T, 1), np.int32))
+    say(f"fast exponential bf16={bf16}")
+    r = ep.EpRouter(T, 2, 1, logits_dtype=t.dtype, max_seqs=T)
+    r.balance_loss(t.cuda(), ids, 1.0, seq_offsets=dev(np.arange(T + 1, dtype=np.int32)))
+    r.check_status()
+    got = r.mean_probs[:, 1].double().cpu().numpy()
+    want = np.exp(x[:, 1]) / (1 + np.exp(x[:, 1]))
+    assert np.all(np.abs(got / want - 1) <= (1.23 * -x[:, 1] + 3 + 6) * U32)

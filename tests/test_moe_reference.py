@@ -94,3 +94,22 @@ def test_tiles_hold_every_code_once():
     assert np.array_equal(np.bincount(nib, minlength=16)[1:],
                           np.bincount(q.reshape(-1), minlength=16)[1:])
     assert ref.pack_codes(q).shape == (2, 38, 80)
+
+
+def test_bound_of_the_fast_exponential():
+    """exp(x) as the router's kernels take it, exp2 of the fp32 product with the
+    fp32 constant: even an exact exp2 stays within the stated bound less the 2
+    that are left for the hardware's."""
+    import os
+    import re
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "combine_get_dispatch_amd", "csrc", "ep_router.hip")
+    text = open(path).read()
+    const = np.float32(float.fromhex(re.search(r"exp2f\(v \* (0x1\.[0-9a-f]+p\+0)f\)", text).group(1)))
+    per, plus = re.search(r"exp2 of x log2\(e\), off by\s*//\s*\(([\d.]*) ?\|x\| \+ (\d)\) 2\^-24",
+                          text).groups()
+    x = -np.random.default_rng(5).uniform(0, 87, 4_000_000).astype(np.float32)
+    got = np.exp2((x * const).astype(np.longdouble))
+    off = np.abs(got / np.exp(x.astype(np.longdouble)) - 1).astype(np.float64) * 2.0 ** 24
+    assert np.all(off <= float(per or 1) * np.abs(x) + int(plus) - 2 + 1e-3)
