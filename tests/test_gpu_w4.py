@@ -589,3 +589,46 @@ def test_product_over_the_whole_range(group, zeros, fp8, rows):
         want = torch.from_numpy((sign @ w.T) * 2.0 ** (px + ps)).to(torch.bfloat16)
         assert bool(torch.isfinite(want).all())
         assert torch.equal(out.cpu(), want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_weights_past_the_cache(fp8, group, zeros, swiglu):
+    """Weights of more than 256 MiB, which are read past the caches: experts of
+    no row, of one, of a full row tile and of two, and one that is tiled.  The
+    matrices repeat after 64 rows, so that the reference stays small: exact, as
+    every repetition of the columns has to be."""
+    rng = np.random.default_rng(71)
+    E, K, N = 12, 8192, 3200 if swiglu else 6400
+    halves = 2 if swiglu else 1
+    counts = [1, 0, 3, 16, 1, 0, 17, 33, 0, 2, 32, 1]
+    off = offsets_of(counts)
+    cap = int(off[-1])
+    assert min(cap, E) * halves * -(-N // 16) * (K // 128) * 1024 > 1 << 28
+    base = rng.integers(0, 16, size=(E, halves, 64, K)).astype(np.uint8)
+    s = 2.0 ** rng.integers(-3, 2, size=(E, halves, 64, K // group))
+    z = rng.integers(0, 16, size=(E, halves, 64, K // group)).astype(np.uint8) if zeros else None
+
+    def whole(v, dtype):
+        t = torch.from_numpy(v).cuda().to(dtype)
+        return t.repeat(1, 1, N // 64, 1).reshape(E, halves * N, -1)
+
+    codes = whole(ref.pack_codes(base), torch.uint8)
+    say(f"weights past the cache fp8={fp8} group={group} zeros={zeros} swiglu={swiglu}")
+    w = ep.W4Experts.pack(codes, whole(s, torch.bfloat16),
+                          None if z is None else whole(z, torch.uint8), swiglu=swiglu)
+    del codes
+    x, xs, xv = draw_rows(rng, cap, K, fp8, True)
+    out = w.product(x, xs, dev(off), dev(np.array(counts, np.int32)))
+    got = out.float().cpu().numpy().reshape(cap, N // 64, 64)
+    assert (got == got[:, :1]).all()
+    small = ref.weights(base.reshape(E, halves * 64, K), s.reshape(E, halves * 64, -1),
+                        None if z is None else z.reshape(E, halves * 64, -1), group)
+    rows, _ = ref.product(xv, small, off, counts, swiglu)
+    want = np.stack([rows[r] for r in range(cap)])
+    if swiglu:  # silu and two products: 12 half steps, then the output's rounding
+        assert np.all(np.abs(got[:, 0] - want) <= np.abs(want) * (UBF16 + 13 * U32) + 1e-37)
+    else:
+        assert np.array_equal(got[:, 0], bf16(want).float().numpy())
