@@ -140,6 +140,9 @@ ep_status_t ep_balance_loss(const ep_router_t *router, ep_dtype_t logits_dtype,
  * experts has no gradient, nor has the bias.  Slots of -1 take no part (their
  * grad_weights are not read into any result); a token with no slot gets a row
  * of zeros whatever its logits are.
+ * An expert that a token's slots repeat (ep_route makes none; a layout rejects
+ * them) counts as often, here as in ep_balance_loss; of three slots and more with
+ * the same expert the order of the sum is not fixed.
  *
  *   router        the forward's (score, normalize and scale are used)
  *   topk_idx      [T, k] int32, the forward's; an id outside [-1, E) counts

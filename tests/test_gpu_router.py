@@ -615,3 +615,29 @@ def test_fast_exponential_on_the_device(bf16):
     got = r.mean_probs[:, 1].double().cpu().numpy()
     want = np.exp(x[:, 1]) / (1 + np.exp(x[:, 1]))
     assert np.all(np.abs(got / want - 1) <= (1.23 * -x[:, 1] + 3 + 6) * U32)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_repeated_ids_count_as_often(score, normalize):
+    """The same expert in two and more slots of a token: each slot counts, and
+    its gradient adds up."""
+    rng = np.random.default_rng(81)
+    for T, E, k in ((21, 8, 2), (40, 64, 6), (17, 256, 8), (9, 300, 32)):
+        x, t = draw_logits(rng, T, E, False)
+        ids = draw_route(rng, T, E, k)
+        ids[::2, 1] = ids[::2, 0]
+        ids[::4] = ids[::4, :1]
+        u = rng.normal(size=(T, k)).astype(np.float32)
+        q = rng.normal(size=(1, E)).astype(np.float32)
+        say(f"repeated ids T={T} E={E} k={k} {score} normalize={normalize}")
+        r = ep.EpRouter(T, E, k, score=score, normalize=normalize)
+        g = r.backward(t.cuda(), dev(ids), dev(u), prob_grad=dev(q))
+        check_grad(g, x, ids, u, False, score=score, normalize=normalize, prob_grad=q)
+        loss = r.balance_loss(t.cuda(), dev(ids), 0.3)
+        r.check_status()
+        l, counts, n, _, pg = ref.balance(x, ids, 0.3, score)
+        assert np.array_equal(r.counts.cpu().numpy(), counts)
+        assert np.array_equal(r.seq_tokens.cpu().numpy(), n)
+        assert abs(loss.item() - l) <= (score_steps(x).max() + 128) * U32 * l
+        assert np.all(np.abs(r.prob_grad.cpu().numpy() - pg) <= 4 * U32 * pg)
