@@ -189,17 +189,11 @@ struct Rows<true> {
 
 // Experts with at most kStreamRows rows are streamed (product_stream_kernel),
 // the others tiled (product_tile_kernel).  Past 16 rows a streamed expert's
-// weights are read twice; where the tiles have kTileFrom blocks or more, two per
-// compute unit, those experts are tiled too.  Streamed and tiled with 17 rows
-// each, and with 32, in us (FP8 rows: the same to 8 %):
-//     blocks   224 (4 experts, 2048 x 7168)        16, 20   18, 21
-//     448      (8)                                 27, 23   30, 25
-//     512      (16 experts, 7168 x 2 x 2048)       83, 85   93, 87
-//     640      (20)                               106, 99  129, 100
-//     784      (14 experts, 2048 x 7168)           43, 47   49, 51
-//     896      (16)                                45, 40   50, 42
-//     1024     (32 experts, 7168 x 2 x 2048)      169, 165  202, 167
-//     3584     (64 experts, 2048 x 7168)          184, 142  206, 155
+// weights are read twice; where the blocks of the tiles fill the chip several
+// times over (kTileRounds), those experts are tiled too.  17 and 32 rows each,
+// streamed and tiled: 64 experts 2048 x 7168 (3584 blocks) 221 and 248 us, 146
+// and 151; 32 experts 7168 x 2 x 2048, FP8 (1024 blocks) 172 and 206, 219 and
+// 229; 8 experts 4096 x 2048 (128 blocks) 20 and 23, about 37.
 constexpr int kStreamRows = 32;
 constexpr int kStreamWaves = 8;
 constexpr int64_t kInfinityCache = int64_t{256} << 20;
@@ -213,11 +207,10 @@ constexpr int64_t kInfinityCache = int64_t{256} << 20;
 // piece in flight per wave measured slower: its registers halve the waves.)
 //
 // ONCE (non-temporal loads): where a call's weights exceed the Infinity Cache
-// nothing of them is found there again.  480 MB per call: 77 us with, 86
-// without; below it the two differ by 5 % either way, and where 17 to 32 rows
-// read the weights twice (16 experts, 4096 x 2 x 2048) 59 with, 58 without.
-// 480 MB (32 experts, 7168 x 2 x 2048, 4 rows each): bf16 77 us, FP8 79 with the
-// tiled kernel's empty launch, 6.1 TB/s of the 6.9 that reading alone reaches.
+// nothing of them is found there again.  480 MB per call: 80 us with, 87
+// without; 34 MB per call, 100 MB in turn: 14.0 with, 12.0 without.
+// 480 MB (32 experts, 7168 x 2 x 2048, 4 rows each, FP8; bf16: 78 us): 82 us a
+// call with the tiled kernel's empty launch, 5.9 TB/s.
 template <bool FP8, int GROUP, bool ZEROS, bool SWIGLU, int kTiles, bool ONCE>
 __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(ProductArgs a) {
   typedef Rows<FP8> F;
@@ -345,13 +338,11 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
   }
 }
 
-constexpr int kBlockRows = 64;  // rows of a block
-constexpr int kBlockTiles = 8;  // weight column tiles of a block
-// Waves per SIMD: 168 registers each, which hold all but 7 or 8 of the FP8
-// kernels of groups of 32 with zero points (those keep them in scratch).
-constexpr int kTileWaves = 3;
+constexpr int kBlockRows = 64;   // rows of a block
+constexpr int kBlockTiles = 8;   // weight column tiles of a block
+constexpr int kTileWaves = 3;    // waves per SIMD that fit
 constexpr int kTileGrid = 256 * kTileWaves;  // persistent workgroups, all resident
-constexpr int64_t kTileFrom = 512;
+constexpr int kTileRounds = 4;
 
 // Many rows: blocks of 64 rows x 128 weight columns (with SwiGLU 64 gate and
 // the same 64 up), taken in turn by persistent workgroups; the blocks of an
@@ -745,7 +736,7 @@ ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const vo
   a.K128 = (a.K + kTileK - 1) / kTileK;
   const int64_t blocks = (a.N16 * (w4->swiglu ? 2 : 1) + kBlockTiles - 1) / kBlockTiles;
   const int64_t experts = capacity / kRows < w4->num_experts ? capacity / kRows : w4->num_experts;
-  a.stream_rows = experts * blocks >= kTileFrom ? kRows : kStreamRows;
+  a.stream_rows = experts * blocks >= kTileRounds * kTileGrid ? kRows : kStreamRows;
   with_product(fp8, w4->group, w_zeros != nullptr, w4->swiglu != 0,
                [&](auto p, auto g, auto z, auto s) {
                  // groups of 32: half the tiles, as four scales each leave no room
