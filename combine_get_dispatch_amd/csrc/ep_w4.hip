@@ -190,10 +190,22 @@ struct Rows<true> {
 // Experts with at most kStreamRows rows are streamed (product_stream_kernel),
 // the others tiled (product_tile_kernel).  Past 16 rows a streamed expert's
 // weights are read twice; where the blocks of the tiles fill the chip several
-// times over (kTileRounds), those experts are tiled too.  17 and 32 rows each,
-// streamed and tiled: 64 experts 2048 x 7168 (3584 blocks) 221 and 248 us, 146
-// and 151; 32 experts 7168 x 2 x 2048, FP8 (1024 blocks) 172 and 206, 219 and
-// 229; 8 experts 4096 x 2048 (128 blocks) 20 and 23, about 37.
+// times over (kTileRounds), those experts are tiled too.  Streamed and tiled, us
+// (FP8 rows: the same to 8 %), with every expert at 17 rows, at 32, and with an
+// average of 12, 16, 20 and 24 rows of random experts:
+//   64 experts, 2048 x 7168 (3584 blocks)
+//       184, 142   206, 155   102, 109   143, 134   187, 147   200, 157
+//   64, 7168 x 2 x 2048 (2048)
+//       332, 271   399, 278   189, 218   261, 257   370, 261   400, 295
+//   32, 7168 x 2 x 2048 (1024)
+//       169, 165   202, 167    99, 143   135, 137   167, 183   224, 182
+//   16, 7168 x 2 x 2048 (512)
+//        83,  85    93,  87    56, 117    76, 101    84, 103   163, 100
+//   8, 4096 x 2048 (128)
+//        18,  32    19,  32
+// How many experts have more than 16 rows only the device knows: few of them,
+// tiled, wait for the longest, so the tiles are left to calls where that costs
+// little.
 constexpr int kStreamRows = 32;
 constexpr int kStreamWaves = 8;
 constexpr int64_t kInfinityCache = int64_t{256} << 20;
@@ -207,10 +219,11 @@ constexpr int64_t kInfinityCache = int64_t{256} << 20;
 // piece in flight per wave measured slower: its registers halve the waves.)
 //
 // ONCE (non-temporal loads): where a call's weights exceed the Infinity Cache
-// nothing of them is found there again.  480 MB per call: 80 us with, 87
-// without; 34 MB per call, 100 MB in turn: 14.0 with, 12.0 without.
-// 480 MB (32 experts, 7168 x 2 x 2048, 4 rows each, FP8; bf16: 78 us): 82 us a
-// call with the tiled kernel's empty launch, 5.9 TB/s.
+// nothing of them is found there again.  480 MB per call: 77 us with, 86
+// without; below it the two differ by 5 % either way, and where 17 to 32 rows
+// read the weights twice (16 experts, 4096 x 2 x 2048) 59 with, 58 without.
+// 480 MB (32 experts, 7168 x 2 x 2048, 4 rows each): bf16 77 us, FP8 79 with the
+// tiled kernel's empty launch, 6.1 TB/s of the 6.9 that reading alone reaches.
 template <bool FP8, int GROUP, bool ZEROS, bool SWIGLU, int kTiles, bool ONCE>
 __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(ProductArgs a) {
   typedef Rows<FP8> F;
@@ -338,9 +351,11 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
   }
 }
 
-constexpr int kBlockRows = 64;   // rows of a block
-constexpr int kBlockTiles = 8;   // weight column tiles of a block
-constexpr int kTileWaves = 3;    // waves per SIMD that fit
+constexpr int kBlockRows = 64;  // rows of a block
+constexpr int kBlockTiles = 8;  // weight column tiles of a block
+// Waves per SIMD: 168 registers each, which hold all but 7 or 8 of the FP8
+// kernels of groups of 32 with zero points (those keep them in scratch).
+constexpr int kTileWaves = 3;
 constexpr int kTileGrid = 256 * kTileWaves;  // persistent workgroups, all resident
 constexpr int kTileRounds = 4;
 

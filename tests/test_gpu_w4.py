@@ -632,3 +632,46 @@ def test_weights_past_the_cache(fp8, group, zeros, swiglu):
         assert np.all(np.abs(got[:, 0] - want) <= np.abs(want) * (UBF16 + 13 * U32) + 1e-37)
     else:
         assert np.array_equal(got[:, 0], bf16(want).float().numpy())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_few_rows_tiled(fp8, group, zeros, swiglu):
+    """48 experts wide enough that 17 to 32 rows are tiled, beside experts that
+    are streamed: exact sums, the matrices repeating after 40 rows."""
+    rng = np.random.default_rng(91)
+    E, K, N = 48, 256, 4200 if swiglu else 8400
+    halves = 2 if swiglu else 1
+    counts = [17, 32, 16, 1, 0, 24, 31, 33, 18, 15, 64, 2, 20, 0, 65, 17] * 3
+    off = offsets_of(counts, gap=1)
+    cap = int(off[-1]) - 1
+    assert min(cap // 16, E) * -(-(halves * -(-N // 16)) // 8) >= 4 * 768
+    base = rng.integers(0, 16, size=(E, halves, 40, K)).astype(np.uint8)
+    s = 2.0 ** rng.integers(-3, 2, size=(E, halves, 40, K // group))
+    z = rng.integers(0, 16, size=(E, halves, 40, K // group)).astype(np.uint8) if zeros else None
+
+    def whole(v, dtype):
+        t = torch.from_numpy(v).cuda().to(dtype)
+        return t.repeat(1, 1, N // 40, 1).reshape(E, halves * N, -1)
+
+    say(f"few rows tiled fp8={fp8} group={group} zeros={zeros} swiglu={swiglu}")
+    w = ep.W4Experts.pack(whole(ref.pack_codes(base), torch.uint8), whole(s, torch.bfloat16),
+                          None if z is None else whole(z, torch.uint8), swiglu=swiglu)
+    x, xs, xv = draw_rows(rng, cap, K, fp8, True)
+    out = torch.full((cap, N), 99.0, dtype=torch.bfloat16, device="cuda")
+    w.product(x, xs, dev(off), dev(np.array(counts, np.int32)), out)
+    got = out.float().cpu().numpy().reshape(cap, N // 40, 40)
+    assert (got == got[:, :1]).all()
+    small = ref.weights(base.reshape(E, halves * 40, K), s.reshape(E, halves * 40, -1),
+                        None if z is None else z.reshape(E, halves * 40, -1), group)
+    rows, _ = ref.product(xv, small, off, counts, swiglu)
+    for r in range(cap):
+        if r not in rows:
+            assert (got[r] == 99.0).all(), r
+        elif swiglu:
+            tol = np.abs(rows[r]) * (UBF16 + 13 * U32) + 1e-37
+            assert np.all(np.abs(got[r, 0] - rows[r]) <= tol), r
+        else:
+            assert np.array_equal(got[r, 0], bf16(rows[r]).float().numpy()), r
