@@ -720,9 +720,12 @@ __device__ __forceinline__ bool order_exactly(const RouteArgs &a, const L *row,
 // add goes by the keys compared (kKeyStep, kGroupStep), not by the largest bias,
 // so that experts put last by a large finite one leave the others' order to 32
 // bits.  bf16 logits are whole within the front bits: equal means equal.
-// 4096 x 256 fp32, groups: 7.5 us; 131072 x 64 bf16: 15 (1.5 TB/s); 65536 x 256
-// fp32, sigmoid, bias, groups: 51 (1.4 TB/s), of which scores and lists are 28,
-// groups 9 and the 64-bit orders 14.  All keys in 64 bits: 152; k rounds: 144.
+// 4096 x 256 fp32, groups: 8 us; 131072 x 64 bf16: 15 (1.5 TB/s); 65536 x 256
+// fp32, sigmoid, bias, groups: 50 (1.4 TB/s), of which scores and lists are 28,
+// groups 9 and the 64-bit orders 14; a softmax there 53; 16384 x 256, k = 20: 24
+// by logit, 61 by sigmoid and bias.  All keys in 64 bits: 152; k rounds of a
+// search for k = 8: 128.  A batch whose keys are all equal is ordered in 64 bits
+// token by token: 260.
 template <typename L, int LPT, int V, int kMode, bool kShort>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   constexpr int kTokens = kThreads / LPT;
@@ -987,8 +990,11 @@ __device__ __forceinline__ float row_scores(const float (&x)[V], float (&p)[V]) 
 // One workgroup per tile of tokens.  A tile's part of sequence s goes to row
 // tile + s of the partial sums: along the tokens one of the two grows, so
 // every part has a row of its own.  The next token's row and ids are loaded
-// before the present one's are worked on.  Bound by the scores' exponentials
-// and the LDS counts: 65536 x 256 bf16, sigmoid: 16 us, 2.2 TB/s.
+// before the present one's are worked on.  65536 x 256 bf16, sigmoid: 16 us, 2.2
+// TB/s.  Of these the exponentials are 3 and the LDS counts none (timing copies
+// without them 13.4 and 16.3); what is left is a workgroup's chain of a few
+// loads, its sums in LDS and its partial row.  Longer tiles: 128 tokens 17, 256
+// tokens (one workgroup per compute unit) 23.
 template <typename L, int LPT, int V, bool kSoftmax>
 __global__ __launch_bounds__(kThreads) void balance_tile_kernel(BalanceArgs a) {
   constexpr int kTokens = kThreads / LPT;
@@ -1072,7 +1078,9 @@ constexpr int kSeqCols = 64;  // experts of a workgroup
 
 // One workgroup per sequence and 64 experts: adds the sequence's parts in 64
 // bits, 16 slices of them side by side and then those in order.  A chain of
-// loads and barriers: 6 us for 1 x 64 as for 37 x 256.
+// loads and barriers: 6 us for 1 x 64 of 256 parts as for 37 x 256 of 1061, 12
+// for 1 x 64 of 1024 parts (131072 tokens in one sequence), which one workgroup
+// adds.
 __global__ __launch_bounds__(kSeqThreads) void balance_seq_kernel(BalanceArgs a) {
   constexpr int kSlices = kSeqThreads / kSeqCols;
   __shared__ double sum_p[kSlices][kSeqCols];

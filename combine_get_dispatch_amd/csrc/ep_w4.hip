@@ -366,8 +366,8 @@ constexpr int kTileRounds = 4;
 // registers to LDS, in the order the matrix instructions take them, one
 // piece ahead of its use and one behind its load; on the way a wave sums
 // its 16 rows over the groups.  So a piece needs one barrier.
-// 4096 rows of 32 experts, 2048 x 7168: 215 us, 560 TFLOP/s; 8 experts of 512
-// rows each: 160 us, 750.  Bound by neither memory (with the weights of one
+// 4096 rows of 32 experts, 2048 x 7168: 207 us, 580 TFLOP/s; 8 experts of 512
+// rows each: 160 us, 750; FP8 rows, 7168 x 2 x 2048 with SwiGLU: 430 us, 560.  Bound by neither memory (with the weights of one
 // piece read again and again 192 us) nor one kind of instruction (matrix
 // instructions 29 % of the time, others 38 %): by each wave's waits in its
 // chain of LDS reads, products and group scales.  128 rows per block, two waves
