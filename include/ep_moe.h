@@ -223,8 +223,8 @@ ep_status_t ep_w4_pack(const ep_w4_t *w4, const uint8_t *codes, const uint16_t *
  *                 count is negative has none.
  *   capacity      rows of x and out; (capacity / 64 + 1) * num_experts < 2^31 - 1
  *   out           bf16 [capacity, N], apart from x; only the experts' rows are
- *                 written.  A row of x that is not finite makes its own
- *                 outputs NaN, no other's
+ *                 written.  A row of x (or a scale of it) that is not
+ *                 finite makes its own outputs infinite or NaN, no other's
  */
 ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const void *x,
                                  const float *x_scales, const uint8_t *w_codes,

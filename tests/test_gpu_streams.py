@@ -147,3 +147,30 @@ def test_host_threads():
         for i, (a, b) in enumerate(zip(g, w)):
             rows = slice(0, c.T * c.k) if i in (4, 5, 7) else slice(None)
             assert torch.equal(a[rows], b[rows]), i
+
+
+def test_default_stream_by_its_handle():
+    """The default stream's handle, 0, and the current stream's inside a capture."""
+    c = Case(55)
+    want = [t.clone() for t in c.run()]
+    say("default stream's handle")
+    got = c.run(stream=torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    c.check()
+    for i, (a, b) in enumerate(zip(got, want)):
+        rows = slice(0, c.T * c.k) if i in (4, 5, 7) else slice(None)
+        assert torch.equal(a[rows], b[rows]), i
+    say("capturing stream's handle")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = c.run(stream=torch.cuda.current_stream().cuda_stream)
+    for n in range(3):
+        for t in got:
+            t.view(torch.uint8).fill_(n)
+        g.replay()
+        torch.cuda.synchronize()
+        c.check()
+        for i, (a, b) in enumerate(zip(got, want)):
+            rows = slice(0, c.T * c.k) if i in (4, 5, 7) else slice(None)
+            assert torch.equal(a[rows], b[rows]), (n, i)
+        c.run()

@@ -675,3 +675,34 @@ def test_few_rows_tiled(fp8, group, zeros, swiglu):
             assert np.all(np.abs(got[r, 0] - rows[r]) <= tol), r
         else:
             assert np.array_equal(got[r, 0], bf16(rows[r]).float().numpy()), r
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_rows_that_are_not_finite_keep_to_themselves(fp8, swiglu):
+    """NaN and infinities in some rows, the last of an expert's among them: their
+    outputs are not finite, all others are as they were."""
+    rng = np.random.default_rng(101)
+    E, K, N = 3, 256, 40
+    q, s, z = draw(rng, E, K, N, 128, True, swiglu, False)
+    counts = [5, 17, 70]
+    off = offsets_of(counts)
+    x, xs, _ = draw_rows(rng, 92, K, fp8, False)
+    w = packed(q, s, z, swiglu)
+    o, c = dev(off), dev(np.array(counts, np.int32))
+    say(f"rows that are not finite fp8={fp8} swiglu={swiglu}")
+    want = w.product(x, xs, o, c)
+    rows = [0, 4, 6, 20, 21, 50, 91]
+    for i, r in enumerate(rows):
+        if not fp8:
+            x[r, 37 * i % K] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+        elif i % 2:
+            x[r, 37 * i % K] = 0x7F | (0x80 if i % 4 == 1 else 0)
+        else:
+            xs[r, i % 2] = (float("nan"), float("inf"))[i % 4 // 2]
+    got = w.product(x, xs, o, c)
+    bad = torch.zeros(92, dtype=torch.bool)
+    bad[rows] = True
+    bad = bad.cuda()
+    assert not bool(torch.isfinite(got[bad]).any())
+    assert torch.equal(got[~bad], want[~bad])
