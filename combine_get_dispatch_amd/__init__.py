@@ -687,20 +687,49 @@ class EpBuffers:
             self.row_src, self.status, stream=stream, zero_padding=self.zero_padding)
         return self.handle
 
-    def expert_product(self, experts, x=None, out=None, rank=None, stream=None):
-        """The experts' product (W4Experts) on the receive rows, or on bf16
-        rows x in their places: bf16 [capacity, out_features].  The weights
-        are all experts', or with ``rank`` that rank's (its rows alone are
-        written)."""
+    def _experts_at(self, rank):
+        """Offsets and counts of all experts, or of one rank's."""
         offs, counts = self.expert_offsets, self.num_tokens_per_expert
         if rank is not None:
             if not 0 <= rank < self.cfg.num_ranks:
                 raise ValueError(f"rank {rank} outside [0, {self.cfg.num_ranks})")
             n = self.cfg.num_experts // self.cfg.num_ranks
             offs, counts = offs[rank * n:(rank + 1) * n + 1], counts[rank * n:(rank + 1) * n]
+        return offs, counts
+
+    def expert_product(self, experts, x=None, out=None, rank=None, stream=None):
+        """The experts' product (W4Experts or Bf16Experts) on the receive rows,
+        or on bf16 rows x in their places: bf16 [capacity, out_features].  The
+        weights are all experts', or with ``rank`` that rank's (its rows alone
+        are written)."""
+        offs, counts = self._experts_at(rank)
         scales = self.recv_scales if x is None else None
         return experts.product(self.recv_x if x is None else x, scales, offs, counts, out=out,
                                stream=stream)
+
+    def expert_backward_rows(self, experts, grad_out, out=None, rank=None, stream=None):
+        """Gradient of the product with Bf16Experts for its rows: bf16
+        [capacity, in_features]."""
+        return experts.backward_rows(grad_out, *self._experts_at(rank), out=out, stream=stream)
+
+    def expert_backward_weights(self, experts, grad_out, x=None, out=None, add=None, dtype=None,
+                                rank=None, stream=None):
+        """Gradient of the product with Bf16Experts for the weights, from the
+        receive rows or from bf16 rows x in their places."""
+        scales = self.recv_scales if x is None else None
+        return experts.backward_weights(self.recv_x if x is None else x, scales, grad_out,
+                                        *self._experts_at(rank), out=out, add=add, dtype=dtype,
+                                        stream=stream)
+
+    def swiglu_checkpoint(self, checkpoint, gate_up, out=None, rank=None, stream=None):
+        """silu(gate) * up of the experts' rows [capacity, 2 features], kept in
+        8 bits by a SwigluCheckpoint."""
+        return checkpoint.save(gate_up, *self._experts_at(rank), out=out, stream=stream)
+
+    def swiglu_backward(self, checkpoint, grad_h, out=None, h=None, rank=None, stream=None):
+        """Gradient for gate and up from a SwigluCheckpoint, and its
+        silu(gate) * up again."""
+        return checkpoint.backward(grad_h, *self._experts_at(rank), out=out, h=h, stream=stream)
 
     def combine(self, expert_out, topk_weights, out=None, stream=None):
         import torch
@@ -793,6 +822,9 @@ class EpBuffers:
 
 
 from . import moe  # noqa: E402  (needs the names above)
-from .moe import (EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, EpRouter, W4Experts,  # noqa: E402,F401
-                  ep_balance_loss, ep_balance_workspace_bytes, ep_expert_product_w4, ep_route,
-                  ep_route_backward, ep_router_t, ep_w4_pack, ep_w4_packed_sizes, ep_w4_t)
+from .moe import (EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, Bf16Experts, EpRouter,  # noqa: E402,F401
+                  SwigluCheckpoint, W4Experts, ep_balance_loss, ep_balance_workspace_bytes,
+                  ep_expert_product, ep_expert_product_backward_rows,
+                  ep_expert_product_backward_weights, ep_expert_product_w4, ep_experts_t, ep_route,
+                  ep_route_backward, ep_router_t, ep_swiglu_checkpoint,
+                  ep_swiglu_checkpoint_backward, ep_w4_pack, ep_w4_packed_sizes, ep_w4_t)

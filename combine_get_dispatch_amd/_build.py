@@ -17,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f)
            for f in ("ep_kernels.hip", "ep_api.hip", "hbm_probe.hip", "ep_router.hip",
-                     "ep_w4.hip")]
+                     "ep_w4.hip", "ep_experts.hip", "ep_checkpoint.hip")]
 LIB = os.path.join(PKG, "libep.so")
 
 HIPCC_FLAGS = [

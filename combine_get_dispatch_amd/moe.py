@@ -1,10 +1,11 @@
 """Python binding of include/ep_moe.h: the router in front of the dispatch /
-combine path and the experts' 4-bit products behind it.
+combine path, and behind it the experts' products with 4-bit or bf16 weights,
+the latter's gradients, and the 8-bit checkpoint of the SwiGLU between them.
 
 The functions carry the C names and take preallocated torch tensors on the
-current device; ``EpRouter`` and ``W4Experts`` keep the buffers, the
-workspace and the packed weights of one configuration.  The package exports
-all of them.
+current device; ``EpRouter``, ``W4Experts``, ``Bf16Experts`` and
+``SwigluCheckpoint`` keep the buffers, the workspace and the weights of one
+configuration.  The package exports all of them.
 """
 from __future__ import annotations
 
@@ -31,11 +32,17 @@ class ep_w4_t(ctypes.Structure):
                 ("swiglu", ctypes.c_int32)]
 
 
+class ep_experts_t(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("out_features", ctypes.c_int32)]
+
+
 def register(L):
     """Argument types of this header's functions (called once, by lib())."""
     P, S, i32, i64, f32 = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64,
                            ctypes.c_float)
     router, w4 = ctypes.POINTER(ep_router_t), ctypes.POINTER(ep_w4_t)
+    experts = ctypes.POINTER(ep_experts_t)
     types = {
         "ep_route": [router, ctypes.c_int, P, P, P, P, P, P, P],
         "ep_balance_workspace_bytes": [router, i32, ctypes.POINTER(S)],
@@ -44,6 +51,12 @@ def register(L):
         "ep_w4_packed_sizes": [w4, ctypes.POINTER(i64), ctypes.POINTER(i64)],
         "ep_w4_pack": [w4, P, P, P, P, P, P, P],
         "ep_expert_product_w4": [w4, ctypes.c_int, P, P, P, P, P, P, P, i64, P, P],
+        "ep_expert_product": [experts, ctypes.c_int, P, P, P, i32, P, P, i64, P, P],
+        "ep_expert_product_backward_rows": [experts, P, P, P, P, i64, P, P],
+        "ep_expert_product_backward_weights": [experts, ctypes.c_int, P, P, P, P, P, i64,
+                                               ctypes.c_int, P, P, P],
+        "ep_swiglu_checkpoint": [i32, i32, P, P, P, i64, P, P, P, P],
+        "ep_swiglu_checkpoint_backward": [i32, i32, P, P, P, P, P, i64, P, P, P],
     }
     for name, args in types.items():
         getattr(L, name).argtypes = args
@@ -237,6 +250,141 @@ def _product(w4, ref, x, x_scales, weights, expert_offsets, num_tokens_per_exper
     _check(st, "ep_expert_product_w4")
 
 
+def _expert_rows(t, cols, name):
+    """Rows of a tensor [capacity, cols]."""
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {cols})")
+    return t.shape[0]
+
+
+def _at_least(t, rows, cols, name):
+    if t is not None and (t.dim() != 2 or t.shape[1] != cols or t.shape[0] < rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (>= {rows}, {cols})")
+
+
+def _expert_at(expert_offsets, num_tokens_per_expert, E, d):
+    """Pointers of the layout's arrays; expert_offsets may have one entry more
+    than there are experts, as the layout's has."""
+    import torch
+
+    if expert_offsets.dim() != 1 or expert_offsets.shape[0] not in (E, E + 1):
+        raise ValueError(f"expert_offsets has shape {tuple(expert_offsets.shape)}, "
+                         f"expected ({E},) or ({E + 1},)")
+    return (_at(expert_offsets, d, torch.int32, None, "expert_offsets"),
+            _at(num_tokens_per_expert, d, torch.int32, (E,), "num_tokens_per_expert"))
+
+
+def _x_at(x, x_scales, K, d):
+    """Type and pointers of bf16 rows, or of E4M3 codes and their scales."""
+    import torch
+
+    fp8 = x_scales is not None
+    return (EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16,
+            _at(x, d, torch.uint8 if fp8 else torch.bfloat16, None, "x"),
+            _at(x_scales, d, torch.float32, (x.shape[0], K // 128), "x_scales"))
+
+
+def _weight_shape(experts):
+    return experts.num_experts, experts.out_features, experts.in_features
+
+
+def ep_expert_product(experts: ep_experts_t, x, x_scales, w, swiglu, expert_offsets,
+                      num_tokens_per_expert, out, stream=None):
+    """x: bf16 [capacity, K], or uint8 E4M3 codes with x_scales."""
+    import torch
+
+    K, N = experts.in_features, experts.out_features
+    cap = _expert_rows(x, K, "x")
+    _at_least(out, cap, N // 2 if swiglu else N, "out")
+    d = _device(x, "x")
+    st = lib().ep_expert_product(
+        ctypes.byref(experts), *_x_at(x, x_scales, K, d),
+        _at(w, d, torch.bfloat16, _weight_shape(experts), "w"), 1 if swiglu else 0,
+        *_expert_at(expert_offsets, num_tokens_per_expert, experts.num_experts, d), cap,
+        _at(out, d, torch.bfloat16, None, "out"), _stream(stream))
+    _check(st, "ep_expert_product")
+
+
+def ep_expert_product_backward_rows(experts: ep_experts_t, grad_out, w, expert_offsets,
+                                    num_tokens_per_expert, grad_x, stream=None):
+    import torch
+
+    cap = _expert_rows(grad_out, experts.out_features, "grad_out")
+    _at_least(grad_x, cap, experts.in_features, "grad_x")
+    d = _device(grad_out, "grad_out")
+    st = lib().ep_expert_product_backward_rows(
+        ctypes.byref(experts), _at(grad_out, d, torch.bfloat16, None, "grad_out"),
+        _at(w, d, torch.bfloat16, _weight_shape(experts), "w"),
+        *_expert_at(expert_offsets, num_tokens_per_expert, experts.num_experts, d), cap,
+        _at(grad_x, d, torch.bfloat16, None, "grad_x"), _stream(stream))
+    _check(st, "ep_expert_product_backward_rows")
+
+
+def ep_expert_product_backward_weights(experts: ep_experts_t, x, x_scales, grad_out,
+                                       expert_offsets, num_tokens_per_expert, add, grad_w,
+                                       stream=None):
+    """grad_w: bf16 or fp32 [experts, N, K], written whole; add: the same type
+    and shape (grad_w itself to add to it), or None."""
+    import torch
+
+    K, N = experts.in_features, experts.out_features
+    cap = _expert_rows(grad_out, N, "grad_out")
+    if _expert_rows(x, K, "x") != cap:
+        raise ValueError(f"x has {x.shape[0]} rows, grad_out {cap}")
+    if grad_w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"grad_w must be float32 or bfloat16, not {grad_w.dtype}")
+    d, shape = _device(grad_out, "grad_out"), _weight_shape(experts)
+    st = lib().ep_expert_product_backward_weights(
+        ctypes.byref(experts), *_x_at(x, x_scales, K, d),
+        _at(grad_out, d, torch.bfloat16, None, "grad_out"),
+        *_expert_at(expert_offsets, num_tokens_per_expert, experts.num_experts, d), cap,
+        EP_DTYPE_F32 if grad_w.dtype == torch.float32 else EP_DTYPE_BF16,
+        _at(add, d, grad_w.dtype, shape, "add"), _at(grad_w, d, grad_w.dtype, shape, "grad_w"),
+        _stream(stream))
+    _check(st, "ep_expert_product_backward_weights")
+
+
+def _checkpoint_shape(cap, features):
+    return cap, 2 * -(-features // 128)
+
+
+def ep_swiglu_checkpoint(num_experts, features, gate_up, expert_offsets, num_tokens_per_expert, h,
+                         codes, scales, stream=None):
+    import torch
+
+    cap = _expert_rows(gate_up, 2 * features, "gate_up")
+    for t, cols, name in ((h, features, "h"), (codes, 2 * features, "codes"),
+                          (scales, _checkpoint_shape(cap, features)[1], "scales")):
+        _at_least(t, cap, cols, name)
+    d = _device(gate_up, "gate_up")
+    st = lib().ep_swiglu_checkpoint(
+        int(num_experts), int(features), _at(gate_up, d, torch.bfloat16, None, "gate_up"),
+        *_expert_at(expert_offsets, num_tokens_per_expert, num_experts, d), cap,
+        _at(h, d, torch.bfloat16, None, "h"), _at(codes, d, torch.uint8, None, "codes"),
+        _at(scales, d, torch.float32, None, "scales"), _stream(stream))
+    _check(st, "ep_swiglu_checkpoint")
+
+
+def ep_swiglu_checkpoint_backward(num_experts, features, codes, scales, grad_h, expert_offsets,
+                                  num_tokens_per_expert, grad_gate_up, h, stream=None):
+    import torch
+
+    cap = _expert_rows(grad_h, features, "grad_h")
+    for t, cols, name in ((h, features, "h"), (grad_gate_up, 2 * features, "grad_gate_up"),
+                          (codes, 2 * features, "codes"),
+                          (scales, _checkpoint_shape(cap, features)[1], "scales")):
+        _at_least(t, cap, cols, name)
+    d = _device(grad_h, "grad_h")
+    st = lib().ep_swiglu_checkpoint_backward(
+        int(num_experts), int(features), _at(codes, d, torch.uint8, None, "codes"),
+        _at(scales, d, torch.float32, None, "scales"),
+        _at(grad_h, d, torch.bfloat16, None, "grad_h"),
+        *_expert_at(expert_offsets, num_tokens_per_expert, num_experts, d), cap,
+        _at(grad_gate_up, d, torch.bfloat16, None, "grad_gate_up"),
+        _at(h, d, torch.bfloat16, None, "h"), _stream(stream))
+    _check(st, "ep_swiglu_checkpoint_backward")
+
+
 class EpRouter:
     """The router of one configuration: selection, balance loss and their
     gradient, with the outputs and the workspace allocated once.  Results are
@@ -385,3 +533,106 @@ class W4Experts:
         _product(self.cfg, self._ref, x, x_scales, self._weights, expert_offsets,
                  num_tokens_per_expert, out, stream)
         return out
+
+
+class Bf16Experts:
+    """bf16 weights [experts, out_features, in_features] of a set of experts,
+    their product and its gradients.  With swiglu the rows of a weight matrix
+    are the gate's, then the up projection's, and ``product`` gives
+    silu(gate) * up; the gradients are those of the plain product (gate and
+    up), which an object without swiglu on the same weights gives.  The
+    weights are read in place at each call."""
+
+    def __init__(self, weights, swiglu=False):
+        import torch
+
+        if weights.dim() != 3 or weights.dtype != torch.bfloat16:
+            raise ValueError("weights must be bf16 [experts, out_features, in_features]")
+        self.weights, self.swiglu = weights, bool(swiglu)
+        E, N, K = weights.shape
+        self.cfg = ep_experts_t(E, K, N)
+
+    def product(self, x, x_scales, expert_offsets, num_tokens_per_expert, out=None, stream=None):
+        """bf16 [rows, out_features] (half of them with swiglu): each expert's
+        rows times its weights.  Rows that are no expert's are left as they
+        are.  Without ``out`` the result belongs to the stream the call runs on
+        (so for the other methods)."""
+        import torch
+
+        if out is None:
+            N = self.cfg.out_features // (2 if self.swiglu else 1)
+            out = _empty(stream, (x.shape[0], N), dtype=torch.bfloat16, device=x.device)
+        ep_expert_product(self.cfg, x, x_scales, self.weights, self.swiglu, expert_offsets,
+                          num_tokens_per_expert, out, stream=stream)
+        return out
+
+    def backward_rows(self, grad_out, expert_offsets, num_tokens_per_expert, out=None,
+                      stream=None):
+        """bf16 [rows, in_features]: the plain product's gradient for its rows."""
+        import torch
+
+        if out is None:
+            out = _empty(stream, (grad_out.shape[0], self.cfg.in_features), dtype=torch.bfloat16,
+                         device=grad_out.device)
+        ep_expert_product_backward_rows(self.cfg, grad_out, self.weights, expert_offsets,
+                                        num_tokens_per_expert, out, stream=stream)
+        return out
+
+    def backward_weights(self, x, x_scales, grad_out, expert_offsets, num_tokens_per_expert,
+                         out=None, add=None, dtype=None, stream=None):
+        """The plain product's gradient for the weights, in their shape: bf16,
+        or fp32 by ``dtype`` or ``out``, plus ``add`` (which may be ``out``)."""
+        import torch
+
+        if out is None:
+            dtype = dtype or (torch.bfloat16 if add is None else add.dtype)
+            out = _empty(stream, tuple(self.weights.shape), dtype=dtype,
+                         device=grad_out.device)
+        ep_expert_product_backward_weights(self.cfg, x, x_scales, grad_out, expert_offsets,
+                                           num_tokens_per_expert, add, out, stream=stream)
+        return out
+
+
+class SwigluCheckpoint:
+    """The 8-bit checkpoint of a layer's gate and up rows: codes
+    [capacity, 2 features], scales [capacity, 2 ceil(features / 128)].  They
+    are allocated once, on the current stream (another stream waits for it
+    before its first call), and the next ``save`` overwrites them."""
+
+    def __init__(self, capacity, features, num_experts, device="cuda"):
+        import torch
+
+        dev = torch.device(device)
+        self.capacity, self.features = int(capacity), int(features)
+        self.num_experts = int(num_experts)
+        self.codes = torch.empty((self.capacity, 2 * self.features), dtype=torch.uint8,
+                                 device=dev)
+        self.scales = torch.empty(_checkpoint_shape(self.capacity, self.features),
+                                  dtype=torch.float32, device=dev)
+
+    def save(self, gate_up, expert_offsets, num_tokens_per_expert, out=None, stream=None):
+        """bf16 [rows, features]: silu(gate) * up; keeps gate and up."""
+        import torch
+
+        if out is None:
+            out = _empty(stream, (gate_up.shape[0], self.features), dtype=torch.bfloat16,
+                         device=gate_up.device)
+        ep_swiglu_checkpoint(self.num_experts, self.features, gate_up, expert_offsets,
+                             num_tokens_per_expert, out, self.codes, self.scales, stream=stream)
+        return out
+
+    def backward(self, grad_h, expert_offsets, num_tokens_per_expert, out=None, h=None,
+                 stream=None):
+        """(bf16 [rows, 2 features], bf16 [rows, features]): the gradient for
+        gate and up, and silu(gate) * up of the kept values."""
+        import torch
+
+        rows, kw = grad_h.shape[0], dict(dtype=torch.bfloat16, device=grad_h.device)
+        if out is None:
+            out = _empty(stream, (rows, 2 * self.features), **kw)
+        if h is None:
+            h = _empty(stream, (rows, self.features), **kw)
+        ep_swiglu_checkpoint_backward(self.num_experts, self.features, self.codes, self.scales,
+                                      grad_h, expert_offsets, num_tokens_per_expert, out, h,
+                                      stream=stream)
+        return out, h

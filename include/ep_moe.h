@@ -15,10 +15,23 @@
  *                         recv_scales) times their experts' 4-bit weights,
  *                         plain or with a SwiGLU epilogue; its rows are what
  *                         ep_combine takes
+ *   ep_expert_product     the same with bf16 weights
+ *   ep_expert_product_backward_rows, ep_expert_product_backward_weights
+ *                         its gradients for the rows and for the weights
+ *   ep_swiglu_checkpoint, ep_swiglu_checkpoint_backward
+ *                         SwiGLU of gate and up rows that keeps them in 8
+ *                         bits, and its gradient from what was kept
  *
- * A layer's step: ep_route, ep_get_dispatch_layout, ep_dispatch,
- * ep_expert_product_w4 (gate and up, SwiGLU), ep_expert_product_w4 (down),
- * ep_combine.
+ * A layer's step: ep_route, ep_get_dispatch_layout, ep_dispatch, the product
+ * (gate and up, SwiGLU), the product (down), ep_combine.
+ *
+ * A training step keeps no activation in bf16: ep_dispatch (FP8),
+ * ep_expert_product (gate and up), ep_swiglu_checkpoint, ep_expert_product
+ * (down), ep_combine; then ep_combine_backward,
+ * ep_expert_product_backward_rows (down), ep_swiglu_checkpoint_backward,
+ * ep_expert_product_backward_weights (down, from the h that the checkpoint
+ * gives again; gate and up, from dispatch's FP8 rows),
+ * ep_expert_product_backward_rows (gate and up), ep_dispatch_backward.
  *
  * Every result is deterministic: sums have a fixed order.  Nothing is
  * allocated and nothing waits, so every call can be captured in a graph; the
@@ -232,6 +245,119 @@ ep_status_t ep_expert_product_w4(const ep_w4_t *w4, ep_dtype_t x_dtype, const vo
                                  const int32_t *expert_offsets,
                                  const int32_t *num_tokens_per_expert, int64_t capacity,
                                  uint16_t *out, hipStream_t stream);
+
+/* bf16 weights of a set of experts: [num_experts, out_features, in_features]. */
+typedef struct ep_experts {
+  int32_t num_experts;  /* >= 1, at most EP_MAX_EXPERTS (a rank's experts, or all) */
+  int32_t in_features;  /* K: 1 <= K < 2^20 */
+  int32_t out_features; /* N: 1 <= N < 2^20; gate and up of a SwiGLU are its halves */
+} ep_experts_t;
+
+/*
+ * The experts' product on expert-major rows: for row r of expert e,
+ *     y[r, n] = sum_c x[r, c] * w_e[n, c]
+ * summed in fp32, and out[r, n] = bf16(y[r, n]), or with swiglu
+ * bf16(silu(y[r, n]) * y[r, N / 2 + n]), the gate's rows of w before the up
+ * projection's.  FP8 rows enter as bf16(code * scale): one rounding, off by at
+ * most 2^-8 of a value whose code is itself off by up to 2^-4; a scale that is
+ * a power of two loses nothing.  (The gradient for the weights sums over the
+ * rows, where the scales cannot be left to the sum; both see the same values.)
+ *
+ *   x_dtype       EP_DTYPE_BF16: x bf16 [capacity, K]
+ *                 EP_DTYPE_FP8_E4M3: x uint8 [capacity, K] and x_scales fp32
+ *                 [capacity, K / 128] (K % 128 == 0), as ep_dispatch writes
+ *   w             bf16 [experts, N, K]
+ *   swiglu        non-zero: N is even and out has N / 2 columns
+ *   expert_offsets, num_tokens_per_expert, capacity   as in
+ *                 ep_expert_product_w4; (capacity / 64 + 1) * num_experts < 2^31 - 1
+ *   out           bf16 [capacity, N or N / 2], apart from x and w; only the
+ *                 experts' rows are written.  A row that is not finite makes
+ *                 its own outputs infinite or NaN, no other's
+ * x and w are 16-byte aligned.  Any K and N will do; where they are multiples
+ * of 8 rows begin at 16-byte boundaries, which the fast kernels need.
+ */
+ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, const void *x,
+                              const float *x_scales, const uint16_t *w, int32_t swiglu,
+                              const int32_t *expert_offsets, const int32_t *num_tokens_per_expert,
+                              int64_t capacity, uint16_t *out, hipStream_t stream);
+
+/*
+ * Gradient of ep_expert_product (without swiglu) for the rows:
+ *     grad_x[r, c] = bf16(sum_n grad_out[r, n] * w_e[n, c]),  summed in fp32.
+ *
+ *   grad_out  bf16 [capacity, N]
+ *   grad_x    bf16 [capacity, K], apart from grad_out and w; only the experts'
+ *             rows are written
+ */
+ep_status_t ep_expert_product_backward_rows(const ep_experts_t *experts, const uint16_t *grad_out,
+                                            const uint16_t *w, const int32_t *expert_offsets,
+                                            const int32_t *num_tokens_per_expert,
+                                            int64_t capacity, uint16_t *grad_x,
+                                            hipStream_t stream);
+
+/*
+ * Gradient of ep_expert_product (without swiglu) for the weights, over the
+ * rows r of each expert:
+ *     grad_w[e, n, c] = add[e, n, c] + sum_r grad_out[r, n] * x[r, c]
+ * summed in fp32 and rounded once to grad_dtype.  An expert without rows gets
+ * add, or zeros.
+ *
+ *   x_dtype, x, x_scales   as in ep_expert_product (FP8 rows rounded as there)
+ *   grad_out   bf16 [capacity, N]
+ *   grad_dtype EP_DTYPE_BF16 or EP_DTYPE_F32: the type of add and grad_w
+ *   add        [experts, N, K] or NULL; may be grad_w itself (gradients of
+ *              several batches added up in place), else apart from it
+ *   grad_w     [experts, N, K], written whole
+ */
+ep_status_t ep_expert_product_backward_weights(
+    const ep_experts_t *experts, ep_dtype_t x_dtype, const void *x, const float *x_scales,
+    const uint16_t *grad_out, const int32_t *expert_offsets, const int32_t *num_tokens_per_expert,
+    int64_t capacity, ep_dtype_t grad_dtype, const void *add, void *grad_w, hipStream_t stream);
+
+/*
+ * SwiGLU of the experts' gate and up rows, and a checkpoint of them in 8 bits:
+ *     h[r, n] = bf16(silu(g) * u),  g = gate_up[r, n], u = gate_up[r, F + n]
+ * and per row, half and block of 128 consecutive columns (the last one of a
+ * half may be shorter)
+ *     scale = 2^e, e the smallest integer from -100 on with max |v| <= 448 * 2^e
+ *     code  = E4M3(v / scale), rounded to nearest even.
+ * A power of two costs E4M3 no precision, and what a code stands for, code *
+ * scale, is a bf16 number: products that take the checkpoint as FP8 rows round
+ * nothing.  A value that is not finite is kept as NaN and has no part in the
+ * scale; one within 2^-5 of bf16's largest may come back infinite.
+ *
+ *   num_experts  1 .. EP_MAX_EXPERTS;  features  F: 1 <= F < 2^20
+ *   gate_up  bf16 [capacity, 2 F], as ep_expert_product writes it; 16-byte aligned
+ *   expert_offsets, num_tokens_per_expert, capacity   as in ep_expert_product;
+ *            only the experts' rows are read and written
+ *   h        bf16 [capacity, F];  codes uint8 [capacity, 2 F];
+ *   scales   fp32 [capacity, 2 * ceil(F / 128)]; all apart from gate_up,
+ *            h and codes 16-byte aligned
+ */
+ep_status_t ep_swiglu_checkpoint(int32_t num_experts, int32_t features, const uint16_t *gate_up,
+                                 const int32_t *expert_offsets,
+                                 const int32_t *num_tokens_per_expert, int64_t capacity,
+                                 uint16_t *h, uint8_t *codes, float *scales, hipStream_t stream);
+
+/*
+ * Gradient of ep_swiglu_checkpoint's h for gate and up, from the checkpoint:
+ * with g, u = code * scale and s = 1 / (1 + exp(-g)),
+ *     grad_gate_up[r, n]     = bf16(grad_h * u * s * (1 + g * (1 - s)))
+ *     grad_gate_up[r, F + n] = bf16(grad_h * g * s)
+ *     h[r, n]                = bf16(g * s * u), the forward's h of the kept values
+ * in fp32.
+ *
+ *   grad_h        bf16 [capacity, F]
+ *   grad_gate_up  bf16 [capacity, 2 F];  h bf16 [capacity, F] or NULL: not
+ *                 wanted.  Both apart from the inputs; all of these 16-byte
+ *                 aligned
+ */
+ep_status_t ep_swiglu_checkpoint_backward(int32_t num_experts, int32_t features,
+                                          const uint8_t *codes, const float *scales,
+                                          const uint16_t *grad_h, const int32_t *expert_offsets,
+                                          const int32_t *num_tokens_per_expert, int64_t capacity,
+                                          uint16_t *grad_gate_up, uint16_t *h,
+                                          hipStream_t stream);
 
 #ifdef __cplusplus
 }

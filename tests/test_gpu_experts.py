@@ -1,0 +1,309 @@
+"""The experts' products with bf16 weights and their gradients on the GPU.
+
+Where inputs are small integers (and scales powers of two) every sum is exact
+in fp32, and the result has to be the rounding of the exact one, bit for bit.
+Elsewhere a sum of L terms of fp32 is off by at most L + 8 half steps of the
+sum of magnitudes, the output by a half step of its type.  FP8 rows enter as
+bf16(code * scale), so that is what the reference multiplies.
+
+Rows that are no expert's, and weights of experts without rows, are NaN: they
+may enter no result."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import combine_get_dispatch_amd as ep  # noqa: E402
+from tests import experts_reference as ref  # noqa: E402
+from tests.gpu_backend import dev, say  # noqa: E402
+
+U32, UBF16 = ref.U32, ref.UBF16
+
+
+def layout_of(counts, gap):
+    """Offsets with `gap` rows behind each expert, and the rows in all."""
+    off = np.concatenate([[0], np.cumsum(np.asarray(counts) + gap)]).astype(np.int32)
+    return off, int(off[-1])
+
+
+def only_experts(v, off, counts):
+    """NaN in the rows that are no expert's."""
+    out = np.full_like(v, np.nan)
+    for _, lo, hi in ref.expert_rows(off, counts, v.shape[0]):
+        out[lo:hi] = v[lo:hi]
+    return out
+
+
+def draw_rows(rng, cap, K, exact):
+    return rng.integers(-4, 5, size=(cap, K)).astype(np.float64) if exact else ref.rounded(
+        rng.normal(size=(cap, K)))
+
+
+def draw_fp8(rng, cap, K, exact):
+    """(codes, scales on the device, the bf16 values that enter the product)"""
+    v = draw_rows(rng, cap, K, exact)
+    t = torch.from_numpy(v.astype(np.float32)).to(torch.float8_e4m3fn)
+    if exact:
+        s = 2.0 ** rng.integers(-2, 3, size=(cap, K // 128))
+    else:
+        s = (rng.random((cap, K // 128)) + 0.1).astype(np.float32).astype(np.float64)
+    # a product of 4 and 24 bits, rounded to 24, then to 8
+    val = (t.float().numpy() * np.repeat(s, 128, axis=1).astype(np.float32)).astype(np.float32)
+    return t.view(torch.uint8).cuda(), dev(s.astype(np.float32)), ref.rounded(val)
+
+
+def draw_x(rng, cap, K, fp8, exact, off, counts):
+    if fp8:
+        x, xs, xv = draw_fp8(rng, cap, K, exact)
+        dead = torch.from_numpy(np.isnan(only_experts(xv, off, counts)[:, 0])).cuda()
+        x[dead] = 0x7F
+        xs[dead] = float("nan")
+        return x, xs, xv
+    xv = draw_rows(rng, cap, K, exact)
+    return ref.to_bf16(only_experts(xv, off, counts)).cuda(), None, xv
+
+
+def draw_w(rng, counts, N, K, exact):
+    E = len(counts)
+    w = rng.integers(-4, 5, size=(E, N, K)).astype(np.float64) if exact else ref.rounded(
+        rng.normal(size=(E, N, K)) / np.sqrt(K))
+    t = w.copy()
+    t[np.asarray(counts) == 0] = np.nan
+    return ref.to_bf16(t).cuda(), w
+
+
+def check_rows(got, want, size, terms, exact):
+    """bf16 rows; NaN in `want`: not an expert's, still 99."""
+    got = got.double().cpu().numpy()
+    dead = np.isnan(want)
+    assert (got[dead] == 99.0).all(), "a row that is no expert's was written"
+    if exact:
+        w = ref.rounded(np.where(dead, 99.0, want))
+        bad = got != w
+        assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], w[bad][:4])
+        return
+    err = ref.sum_error(terms, size)
+    tol = err + (np.abs(want) + err) * UBF16 + 1e-37
+    d = np.abs(got - want)
+    assert np.all(d[~dead] <= tol[~dead]), np.max((d / tol)[~dead])
+
+
+SHAPES = [  # K, N, counts
+    (1, 1, [1]), (8, 8, [1]), (33, 18, [3, 0]), (128, 40, [0, 1, 17]), (256, 130, [65, 1, 0, 64]),
+    (1024, 100, [0, 7]), (640, 264, [33, 1, 0, 129, 2]), (384, 96, [9, 8, 7, 6, 5, 4, 3, 200]),
+    (512, 520, [300]), (136, 1002, [257, 31]), (384, 512, [130, 256, 0, 511]), (72, 64, [16] * 9),
+    (1920, 256, [2, 4, 1, 15, 16, 17]), (2048, 24, [100, 31, 32, 33]), (904, 776, [64, 128, 192]),
+]
+
+
+@pytest.mark.parametrize("K,N,counts", SHAPES)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product(K, N, counts, fp8, swiglu):
+    if fp8 and K % 128:
+        pytest.skip("FP8 rows come in blocks of 128")
+    if swiglu and N % 2:
+        pytest.skip("gate and up are halves")
+    rng = np.random.default_rng(K + N)
+    off, cap = layout_of(counts, 2)
+    for exact in (True, False):
+        say(f"product K={K} N={N} counts={counts} fp8={fp8} swiglu={swiglu} exact={exact}")
+        x, xs, xv = draw_x(rng, cap, K, fp8, exact, off, counts)
+        wt, w = draw_w(rng, counts, N, K, exact)
+        out = torch.full((cap, N // 2 if swiglu else N), 99.0, dtype=torch.bfloat16, device="cuda")
+        got = ep.Bf16Experts(wt, swiglu=swiglu).product(x, xs, dev(off),
+                                                        dev(np.array(counts, np.int32)), out=out)
+        assert got is out
+        y, size = ref.product(xv, w, off, counts)
+        if not swiglu:
+            check_rows(out, y, size, K, exact)
+            continue
+        # h = silu(a) b: silu has a slope of at most 1.1, the function and the
+        # products are off by 12 half steps
+        h = N // 2
+        a, b, err = y[:, :h], y[:, h:], 0.0 * size if exact else ref.sum_error(K, size)
+        want = ref.silu(a) * b
+        e = (1.1 * err[:, :h] * (np.abs(b) + err[:, h:]) + np.abs(ref.silu(a)) * err[:, h:]
+             + 12 * U32 * np.abs(want))
+        g = out.double().cpu().numpy()
+        dead = np.isnan(want)
+        assert (g[dead] == 99.0).all()
+        tol = e + (np.abs(want) + e) * UBF16 + 1e-37
+        assert np.all(np.abs(g - want)[~dead] <= tol[~dead])
+
+
+@pytest.mark.parametrize("K,N,counts", SHAPES + [(40, 33, [5, 70]), (1001, 131, [3, 129])])
+def test_rows_gradient(K, N, counts):
+    rng = np.random.default_rng(K + N + 1)
+    off, cap = layout_of(counts, 1)
+    for exact in (True, False):
+        say(f"rows' gradient K={K} N={N} counts={counts} exact={exact}")
+        gv = draw_rows(rng, cap, N, exact)
+        g = ref.to_bf16(only_experts(gv, off, counts)).cuda()
+        wt, w = draw_w(rng, counts, N, K, exact)
+        out = torch.full((cap, K), 99.0, dtype=torch.bfloat16, device="cuda")
+        ep.Bf16Experts(wt).backward_rows(g, dev(off), dev(np.array(counts, np.int32)), out=out)
+        check_rows(out, *ref.rows_grad(gv, w, off, counts), N, exact)
+
+
+@pytest.mark.parametrize("K,N,counts", SHAPES + [(40, 33, [5, 70]), (1001, 131, [3, 129])])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("add", ["none", "apart", "in place"])
+def test_weights_gradient(K, N, counts, fp8, dtype, add):
+    if fp8 and K % 128:
+        pytest.skip("FP8 rows come in blocks of 128")
+    rng = np.random.default_rng(K + N + 2)
+    off, cap = layout_of(counts, 3)
+    E = len(counts)
+    for exact in (True, False):
+        say(f"weights' gradient K={K} N={N} counts={counts} fp8={fp8} {dtype} add={add} "
+            f"exact={exact}")
+        gv = draw_rows(rng, cap, N, exact)
+        g = ref.to_bf16(only_experts(gv, off, counts)).cuda()
+        x, xs, xv = draw_x(rng, cap, K, fp8, exact, off, counts)
+        want, size = ref.weights_grad(gv, xv, off, counts)
+        out = torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda")
+        before = None
+        if add != "none":
+            av = (rng.integers(-64, 65, size=(E, N, K)).astype(np.float64) if exact
+                  else ref.rounded(rng.normal(size=(E, N, K))))
+            before = torch.from_numpy(av.astype(np.float32)).to(dtype).cuda()
+            want, size = want + av, size + np.abs(av)
+            if add == "in place":
+                out = before
+        e = ep.Bf16Experts(torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda"))
+        e.backward_weights(x, xs, g, dev(off), dev(np.array(counts, np.int32)), out=out,
+                           add=before)
+        got = out.double().cpu().numpy()
+        if exact:
+            if dtype == torch.bfloat16:
+                want = ref.rounded(want)
+            assert np.array_equal(got, want), np.argwhere(got != want)[:4]
+            continue
+        err = ref.sum_error(max(counts) + 1, size)
+        if dtype == torch.bfloat16:
+            err = err + (np.abs(want) + err) * UBF16
+        d = np.abs(got - want)
+        assert np.all(d <= err + 1e-37), np.max(d / (err + 1e-37))
+
+
+def test_fp8_rows_are_rounded_once():
+    """Against the unrounded rows: 2^-8 of each value at most, and the product's
+    own rounding."""
+    rng = np.random.default_rng(5)
+    K, N, counts = 512, 96, [40, 3]
+    off, cap = layout_of(counts, 0)
+    x, xs, _ = draw_fp8(rng, cap, K, False)
+    raw = x.view(torch.float8_e4m3fn).float().double().cpu().numpy() * np.repeat(
+        xs.double().cpu().numpy(), 128, axis=1)
+    wt, w = draw_w(rng, counts, N, K, False)
+    say("rounding of FP8 rows")
+    got = ep.Bf16Experts(wt).product(x, xs, dev(off), dev(np.array(counts, np.int32)))
+    y, size = ref.product(raw, w, off, counts)
+    err = size * UBF16 + ref.sum_error(K, size * (1 + UBF16))
+    assert np.all(np.abs(got.double().cpu().numpy() - y) <= err + (np.abs(y) + err) * UBF16)
+
+
+@pytest.mark.parametrize("K,N", [(128, 64), (75, 33)])
+def test_rows_past_the_capacity_and_bad_offsets_are_left_alone(K, N):
+    rng = np.random.default_rng(6)
+    E, cap = 4, 10
+    off, cnt = np.array([0, 4, -3, 2 ** 31 - 1], np.int32), np.array([3, 100, 5, 7], np.int32)
+    xv, w = draw_rows(rng, cap, K, True), rng.integers(-4, 5, size=(E, N, K)).astype(np.float64)
+    gv = draw_rows(rng, cap, N, True)
+    e = ep.Bf16Experts(ref.to_bf16(w).cuda())
+    x, g = ref.to_bf16(xv).cuda(), ref.to_bf16(gv).cuda()
+    for name, call, rows, width, form in (("product", lambda o, c, out: e.product(
+            x, None, o, c, out=out), xv, N, ref.product), ("rows' gradient",
+            lambda o, c, out: e.backward_rows(g, o, c, out=out), gv, K, ref.rows_grad)):
+        say(f"{name}: rows past the capacity")
+        out = torch.full((cap + 4, width), 99.0, dtype=torch.bfloat16, device="cuda")
+        call(dev(off), dev(cnt), out)
+        want = np.full((cap + 4, width), 99.0)
+        y = form(rows, w, off, cnt)[0]
+        want[:cap] = np.where(np.isnan(y), 99.0, ref.rounded(np.nan_to_num(y)))
+        assert np.array_equal(out.double().cpu().numpy(), want)
+        say(f"{name}: no rows")
+        call(dev(off), dev(np.zeros(4, np.int32)), out)
+        call(dev(off), dev(np.full(4, -7, np.int32)), out)
+        assert np.array_equal(out.double().cpu().numpy(), want)
+    say("weights' gradient: rows past the capacity, experts without rows")
+    gw = e.backward_weights(x, None, g, dev(off), dev(cnt), dtype=torch.float32)
+    assert np.array_equal(gw.double().cpu().numpy(), ref.weights_grad(gv, xv, off, cnt)[0])
+    say("weights' gradient: no rows at all, no capacity")
+    for rows in (cap, 0):
+        gw.fill_(float("nan"))
+        e.backward_weights(x[:rows], None, g[:rows], dev(off), dev(np.zeros(4, np.int32)), out=gw)
+        assert not gw.any()
+        add = torch.randn_like(gw)
+        e.backward_weights(x[:rows], None, g[:rows], dev(off), dev(np.zeros(4, np.int32)), out=gw,
+                           add=add)
+        assert torch.equal(gw, add)
+
+
+@pytest.mark.parametrize("K,N", [(256, 128), (75, 33)])
+def test_rows_that_are_not_finite_stay_by_themselves(K, N):
+    rng = np.random.default_rng(7)
+    counts = [70, 20]
+    off, cap = layout_of(counts, 0)
+    at, cnt = dev(off), dev(np.array(counts, np.int32))
+    wt, _ = draw_w(rng, counts, N, K, False)
+    e = ep.Bf16Experts(wt)
+    for width, call in ((K, lambda v: e.product(v, None, at, cnt)),
+                        (N, lambda v: e.backward_rows(v, at, cnt))):
+        v = ref.to_bf16(draw_rows(rng, cap, width, False)).cuda()
+        say(f"rows that are not finite, width {width}")
+        clean = call(v)
+        dirty = v.clone()
+        dirty[3, width - 1], dirty[64, 0], dirty[89, 1] = float("inf"), float("nan"), -float("inf")
+        got = call(dirty)
+        bad = torch.zeros(cap, dtype=torch.bool, device="cuda")
+        bad[[3, 64, 89]] = True
+        assert torch.equal(got[~bad], clean[~bad])
+        assert not torch.isfinite(got[bad]).any()
+
+
+def test_large_and_small_values():
+    """Rows and weights of any size: sums in fp32's range are finite."""
+    K, N = 256, 64
+    for scale in (1e-30, 1e30):
+        say(f"rows of {scale}")
+        x = torch.full((70, K), scale, dtype=torch.bfloat16, device="cuda")
+        w = torch.full((1, N, K), 1 / scale, dtype=torch.bfloat16, device="cuda")
+        at = dev(np.array([0], np.int32)), dev(np.array([70], np.int32))
+        want = ref.rounded(K * float(x[0, 0]) * float(w[0, 0, 0]))
+        got = ep.Bf16Experts(w).product(x, None, *at)
+        assert np.array_equal(got.double().cpu().numpy(), np.full((70, N), want))
+
+
+def test_python_refusals():
+    e = ep.Bf16Experts(torch.zeros(2, 32, 128, dtype=torch.bfloat16, device="cuda"))
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out, gx, gw = g.clone(), x.clone(), torch.zeros(2, 32, 128, device="cuda")
+    for bad in (dict(x=x[:, :64]), dict(x=x.float()), dict(off=off[:1]), dict(cnt=off[:1]),
+                dict(out=out[:3]), dict(out=out.float()), dict(x=x.t().contiguous().t()),
+                dict(xs=torch.ones(4, 1, device="cuda")), dict(cnt=off.long()), dict(x=x.cpu()),
+                dict(out=out.t().contiguous().t())):
+        a = dict(dict(x=x, xs=None, off=off, cnt=off, out=out), **bad)
+        with pytest.raises(ValueError):
+            e.product(a["x"], a["xs"], a["off"], a["cnt"], out=a["out"])
+    for bad in (dict(g=g[:, :16]), dict(g=g.float()), dict(out=gx[:3]), dict(out=gx.half()),
+                dict(off=off.long()), dict(g=g.cpu())):
+        a = dict(dict(g=g, off=off, out=gx), **bad)
+        with pytest.raises(ValueError):
+            e.backward_rows(a["g"], a["off"], off, out=a["out"])
+    for bad in (dict(g=g[:3]), dict(x=x.float()), dict(out=gw[:1]), dict(out=gw.half()),
+                dict(add=gw.bfloat16()), dict(add=gw[:, :31]), dict(xs=torch.ones(4, device="cuda"))):
+        a = dict(dict(g=g, x=x, xs=None, out=gw, add=None), **bad)
+        with pytest.raises(ValueError):
+            e.backward_weights(a["x"], a["xs"], a["g"], off, off, out=a["out"], add=a["add"])
+    with pytest.raises(ep.EpError):  # rows that begin between 16-byte boundaries
+        e.product(torch.zeros(4 * 128 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(4, 128),
+                  None, off, off)
+    with pytest.raises(ep.EpError):  # a result over its input
+        ep.Bf16Experts(torch.zeros(2, 128, 128, dtype=torch.bfloat16, device="cuda")).product(
+            x, None, off, off, out=x)
