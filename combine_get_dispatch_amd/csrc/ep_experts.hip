@@ -154,6 +154,380 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
   }
 }
 
+// --------------------------------------------------------------------------
+// Tiles
+// --------------------------------------------------------------------------
+//
+// c[m, n] = sum_l a[m, l] b[n, l] in tiles of 256 x 256, 32 of l at a time.
+// "Rows" is the side of m, "columns" that of n.  The matrix instruction takes
+// columns first, so that a lane's results are consecutive columns of one row.
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTile = 256;            // rows and columns of a tile
+constexpr int kDepth = 32;            // of the sum, per stage
+constexpr int kStages = 4;            // in LDS: one in use, three on their way
+constexpr int kSideBytes = kTile * kDepth * 2;
+constexpr int kStageBytes = 2 * kSideBytes;  // rows, then columns
+constexpr int kTileThreads = 512;
+constexpr int kTileWorkgroups = 256;  // one per compute unit, by its LDS
+constexpr int kBand = 8;              // row tiles that go through the columns together
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+
+// 16 bytes per lane from global memory to LDS, at lds + 16 * lane; zeros where
+// the offset is outside the buffer.  Written in assembly because the compiler
+// has every LDS read wait for all of its own such loads.  Nothing comes back in
+// registers; stage_barrier() waits.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"(lds), "v"(offset), "s"(buffer)
+      : "memory");
+}
+
+// All but the newest `kLeft` loads have arrived, this wave's LDS reads are
+// done, and so for every wave of the workgroup.
+template <int kLeft>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
+}
+
+__device__ __forceinline__ u32x4 buffer_of(const void *base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)uniform((int)p), (uint32_t)uniform((int)(p >> 32)) & 0xFFFFu,
+               (uint32_t)uniform((int)bytes), 0x00020000u};
+}
+
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset outside every buffer
+
+// A piece of work: one tile of one expert.
+struct Item {
+  int e;
+  int64_t first;   // the expert's first row
+  int rows;        // rows of the tile (its rows of the weights for the weights' gradient)
+  int row0;        // of the tile, inside the expert's (or the weight's) rows
+  int col0;        // first output column
+  int length;      // of the sum
+};
+
+// The numbering of items: an expert's tiles are consecutive, in bands of kBand
+// row tiles that take the columns one after the other.
+template <Kind KIND>
+struct Items {
+  const ProductArgs &a;
+  const int32_t *starts;
+  int row_tiles, col_tiles;
+
+  __device__ __forceinline__ int64_t count() const {
+    return (KIND == kWeightsGrad ? (int64_t)a.rows.E * row_tiles : (int64_t)starts[a.rows.E]) *
+           col_tiles;
+  }
+  __device__ __forceinline__ void get(int64_t item, Item *it, int out_cols_per_tile) const {
+    const int32_t block = (int32_t)(item / col_tiles);  // as if rows came first
+    int e, tiles, before;
+    int64_t rows;
+    if (KIND == kWeightsGrad) {
+      e = uniform(block / row_tiles);
+      tiles = row_tiles;
+      before = e * row_tiles;
+    } else {
+      e = expert_of(starts, a.rows.E, block);
+      before = uniform(starts[e]);
+      tiles = uniform(starts[e + 1]) - before;
+    }
+    rows_inside(uniform(a.rows.offsets[e]), uniform(a.rows.counts[e]), a.rows.capacity, &it->first,
+                &rows);
+    const int64_t in_expert = item - (int64_t)before * col_tiles;
+    const int band = (int)(in_expert / ((int64_t)kBand * col_tiles));
+    const int in_band = (int)(in_expert - (int64_t)band * kBand * col_tiles);
+    const int high = tiles - band * kBand < kBand ? tiles - band * kBand : kBand;
+    const int rt = uniform(band * kBand + in_band % high), ct = uniform(in_band / high);
+    it->e = e;
+    it->row0 = rt * kTile;
+    it->col0 = ct * out_cols_per_tile;
+    const int64_t all = KIND == kWeightsGrad ? (int64_t)a.N : rows;
+    it->rows = (int)(all - it->row0 < kTile ? all - it->row0 : kTile);
+    it->length = KIND == kProduct ? a.K : KIND == kRowsGrad ? a.N : (int)rows;
+  }
+};
+
+// One side of a stage is two loads per wave.  "Along": l is consecutive in
+// memory; 16 rows of 64 bytes per load, the 16-byte pieces of row r in LDS at
+// piece ^ (r / 4) % 4, so that the reads of 16 lanes of one piece cover all
+// banks.  "Across": m (or n) is consecutive; two l of 512 bytes per load, pieces
+// at piece ^ 4 (l % 4), so that the four l of a transposing read do.  What is
+// past the end of the sum, or of the rows, is outside the load's buffer and
+// zero; a column that is not there spoils its own results alone.
+template <Kind KIND, bool SWIGLU, typename OUT>
+__global__ __launch_bounds__(kTileThreads, 2) void product_tile_kernel(ProductArgs a) {
+  constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
+  constexpr int kOutTile = SWIGLU ? kTile / 2 : kTile;
+  __shared__ __align__(1024) uint8_t stage[kStages * kStageBytes];
+  __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[kTileThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int wr = wave >> 2, wc = wave & 3;  // of the wave's row and column tiles
+  const int K = a.K, N = a.N;
+  const int out_cols = KIND == kProduct ? (SWIGLU ? N / 2 : N) : K;
+  if (KIND != kWeightsGrad)
+    number_blocks(a.rows, starts, totals, [](int64_t rows) { return (rows + kTile - 1) / kTile; });
+  const Items<KIND> items{a, starts, (N + kTile - 1) / kTile, (out_cols + kOutTile - 1) / kOutTile};
+  // The items of an XCD (workgroups id % 8) are consecutive, so that the
+  // workgroups that share its L2 share rows and columns.
+  const int64_t count = items.count(), per_xcd = (count + 7) / 8;
+  const int64_t from = (blockIdx.x % 8) * per_xcd;
+  const int64_t to = from + per_xcd < count ? from + per_xcd : count;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_byte *)stage;
+
+  // where a lane's 16 bytes come from, from the base of its load on
+  const int64_t row_pitch = (int64_t)(KIND == kProduct ? K : N) * 2, col_pitch = (int64_t)K * 2;
+  const int piece_along = (lane & 3) ^ (lane >> 4 & 3);
+  const int piece_across = (lane & 31) ^ ((wave * 2 + half) & 3) << 2;
+  const uint32_t row_off = (uint32_t)(kRowsAcross ? half * row_pitch + piece_across * 16
+                                                  : (lane >> 2) * row_pitch + piece_along * 16);
+  const uint32_t col_off = (uint32_t)(kColsAcross ? half * col_pitch + piece_across * 16
+                                                  : (lane >> 2) * col_pitch + piece_along * 16);
+
+  // where a lane's parts of the instructions' operands are in a stage
+  int row_at[4], col_at[2];
+  const int swizzle = (l32 >> 2 & 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 2 * i + wr;
+    row_at[i] = kRowsAcross
+                    ? (half * 8 + (lane & 15) / 4) * 512 +
+                          ((t * 4 + (lane >> 4 & 1) * 2 + (lane & 3) / 2) ^ ((lane & 15) / 4) << 2) * 16 +
+                          (lane & 1) * 8
+                    : (t * 32 + l32) * 64 + (half ^ swizzle) * 16;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = wc * 2 + j;
+    col_at[j] = kSideBytes +
+                (kColsAcross
+                     ? (half * 8 + (lane & 15) / 4) * 512 +
+                           ((t * 4 + (lane >> 4 & 1) * 2 + (lane & 3) / 2) ^ ((lane & 15) / 4) << 2) * 16 +
+                           (lane & 1) * 8
+                     : (t * 32 + l32) * 64 + (half ^ swizzle) * 16);
+  }
+  const auto read_along = [&](int at, int ks) {
+    return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 32));
+  };
+  const auto read_across = [&](int at, int ks) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    struct {
+      s16x4 lo, hi;
+    } v;
+    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at + ks * 8192));
+    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at + ks * 8192 + 2048));
+    return __builtin_bit_cast(bf16x8, v);
+  };
+
+  for (int64_t item = from + blockIdx.x / 8; item < to; item += gridDim.x / 8) {
+    Item it;
+    items.get(item, &it, kOutTile);
+    // bases of this wave's loads, at the first of the sum
+    const uint8_t *row_base[2], *col_base[2];
+    int row_bytes[2], col_bytes[2];  // along: of the rows there are
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int group = i * 8 + wave;
+      if (kRowsAcross) {
+        row_base[i] = reinterpret_cast<const uint8_t *>(a.grad) +
+                      (it.first + group * 2) * row_pitch + it.row0 * 2;
+      } else {
+        const int have = it.rows - group * 16;
+        row_base[i] = reinterpret_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
+                      (it.first + it.row0 + group * 16) * row_pitch;
+        row_bytes[i] = (have < 0 ? 0 : have < 16 ? have : 16) * (int)row_pitch;
+      }
+      if (KIND == kProduct) {
+        const int r = group * 16;
+        const int n = SWIGLU ? it.col0 + r / 64 * 32 + r % 32 : it.col0 + r;
+        const int have = out_cols - n;
+        col_base[i] = reinterpret_cast<const uint8_t *>(a.w) +
+                      ((int64_t)it.e * N + n + (SWIGLU ? r % 64 / 32 * out_cols : 0)) * col_pitch;
+        col_bytes[i] = (have < 0 ? 0 : have < 16 ? have : 16) * (int)col_pitch;
+      } else {
+        col_base[i] = (KIND == kRowsGrad
+                           ? reinterpret_cast<const uint8_t *>(a.w) +
+                                 ((int64_t)it.e * N + group * 2) * col_pitch
+                           : static_cast<const uint8_t *>(a.x) + (it.first + group * 2) * col_pitch) +
+                      it.col0 * 2;
+      }
+    }
+    uint32_t at = 0;  // of the sum, of the next stage to load
+    const auto issue = [&](int buf) {
+      const uint32_t lds = lds0 + buf * kStageBytes + wave * 1024;
+      const int left = (int)((uint32_t)it.length - at);
+      const bool in = piece_along * 8 < left;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int have = left - (i * 8 + wave) * 2;  // across: of this load's two l
+        const int n = kRowsAcross
+                          ? (have < 0 ? 0 : have < 2 ? have : 2) * (int)row_pitch - it.row0 * 2
+                          : row_bytes[i] - (int)at * 2;
+        load_to_lds(lds + i * 8192, kRowsAcross || in ? row_off : kNowhere,
+                    buffer_of(row_base[i], n < 0 ? 0 : n));
+        row_base[i] += kRowsAcross ? kDepth * row_pitch : kDepth * 2;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int have = left - (i * 8 + wave) * 2;
+        const int n = kColsAcross
+                          ? (have < 0 ? 0 : have < 2 ? have : 2) * (int)col_pitch - it.col0 * 2
+                          : col_bytes[i] - (int)at * 2;
+        load_to_lds(lds + kSideBytes + i * 8192, kColsAcross || in ? col_off : kNowhere,
+                    buffer_of(col_base[i], n < 0 ? 0 : n));
+        col_base[i] += kColsAcross ? kDepth * col_pitch : kDepth * 2;
+      }
+      at += kDepth;
+    };
+    const int steps = (int)(((uint32_t)it.length + kDepth - 1) / kDepth);
+
+    const auto tile = [&](auto count) {
+      constexpr int kM = decltype(count)::value;
+      f32x16 acc[kM][2];
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[m][j][v] = 0.0f;
+      issue(0);
+      issue(1);
+      issue(2);
+      for (int s = 0; s < steps; ++s) {
+        const int at0 = (s & 3) * kStageBytes;
+        stage_barrier<8>();  // this stage is there, and the last one's buffer is free
+        issue((s + 3) & 3);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          bf16x8 c[2], r[kM];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            c[j] = kColsAcross ? read_across(at0 + col_at[j], ks) : read_along(at0 + col_at[j], ks);
+#pragma unroll
+          for (int m = 0; m < kM; ++m)
+            r[m] = kRowsAcross ? read_across(at0 + row_at[m], ks) : read_along(at0 + row_at[m], ks);
+#pragma unroll
+          for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[m][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[j], r[m], acc[m][j], 0, 0, 0);
+        }
+      }
+      stage_barrier<0>();  // every stage is free
+      // Results go through 4 KB of LDS per wave, 32 rows at a time, to leave in
+      // whole lines; in fp32 where something is added before the rounding.  A
+      // lane has row l32 and columns 8 q + 4 half .. + 3.
+      uint8_t *mine = stage + wave * 4096;
+      const auto finish = [&](auto f32) {
+        constexpr bool kF32 = decltype(f32)::value;
+        constexpr int kPasses = kF32 ? 2 : 1;              // of columns
+        constexpr int kCols = (SWIGLU || kF32) ? 32 : 64;  // of a pass
+        constexpr int kPieces = kCols * (kF32 ? 4 : 2) / 16;  // 16-byte pieces of a row in LDS
+        constexpr int kOutCols = 16 / (int)sizeof(OUT);       // of a store
+        constexpr int kStores = kCols / kOutCols;             // of a row
+        const auto swizzled = [&](int row, int piece) {
+          return row * (kPieces * 16) + (piece ^ (kPieces == 8 ? row & 7 : row >> 1 & 3)) * 16;
+        };
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int pass = 0; pass < kPasses; ++pass) {
+#pragma unroll
+            for (int j = 0; j < kCols / 32; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                f32x4 y;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  y[v] = acc[m][kF32 ? pass : j][q * 4 + v];
+                  if (SWIGLU) y[v] = silu_of(y[v]) * acc[m][1][q * 4 + v];
+                }
+                if constexpr (kF32)
+                  *reinterpret_cast<f32x4 *>(mine + swizzled(l32, q * 2 + half)) = y;
+                else
+                  *reinterpret_cast<u32x2 *>(mine + swizzled(l32, j * 4 + q) + half * 8) =
+                      u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+              }
+#pragma unroll
+            for (int i = 0; i < kStores / 2; ++i) {
+              const int row = i * (64 / kStores) + lane / kStores, piece = lane % kStores;
+              const int r = (2 * m + wr) * 32 + row;
+              const int col = it.col0 + (SWIGLU ? wc * 32 : wc * 64 + pass * 32) + piece * kOutCols;
+              const int64_t to_row = KIND == kWeightsGrad ? (int64_t)it.e * N + it.row0 + r
+                                                          : it.first + it.row0 + r;
+              const int64_t at_out = to_row * out_cols + col;
+              u32x4 v;
+              if constexpr (!kF32) {
+                v = *reinterpret_cast<const u32x4 *>(mine + swizzled(row, piece));
+                if (r >= it.rows || col >= out_cols) continue;
+              } else {
+                f32x4 y[kOutCols / 4];
+#pragma unroll
+                for (int p = 0; p < kOutCols / 4; ++p)
+                  y[p] = *reinterpret_cast<const f32x4 *>(
+                      mine + swizzled(row, piece * (kOutCols / 4) + p));
+                if (r >= it.rows || col >= out_cols) continue;
+                if (a.add != nullptr) {
+                  const u32x4 b = *reinterpret_cast<const u32x4 *>(
+                      static_cast<const OUT *>(a.add) + at_out);
+                  if constexpr (std::is_same<OUT, float>::value) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[0][c] += __uint_as_float(b[c]);
+                  } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                      y[c / 4][c % 4] += __uint_as_float(c % 2 ? b[c / 2] & 0xFFFF0000u
+                                                               : b[c / 2] << 16);
+                  }
+                }
+                if constexpr (std::is_same<OUT, float>::value) {
+                  v = __builtin_bit_cast(u32x4, y[0]);
+                } else {
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+                    v[c] = pack_bf16(y[c / 2][c % 2 * 2], y[c / 2][c % 2 * 2 + 1]);
+                }
+              }
+              *reinterpret_cast<u32x4 *>(static_cast<OUT *>(a.out) + at_out) = v;
+            }
+          }
+      };
+      if constexpr (std::is_same<OUT, float>::value) {
+        finish(std::true_type{});
+      } else if constexpr (KIND == kWeightsGrad) {
+        if (a.add != nullptr)
+          finish(std::true_type{});
+        else
+          finish(std::false_type{});
+      } else {
+        finish(std::false_type{});
+      }
+      lds_barrier();  // the buffers are free for the next tile
+    };
+    switch ((it.rows + 63) / 64) {
+      case 1: tile(std::integral_constant<int, 1>{}); break;
+      case 2: tile(std::integral_constant<int, 2>{}); break;
+      case 3: tile(std::integral_constant<int, 3>{}); break;
+      default: tile(std::integral_constant<int, 4>{}); break;
+    }
+  }
+}
+
 #define EP_TRY(expr)                \
   do {                              \
     const ep_status_t st_ = (expr); \
@@ -247,7 +621,15 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
   a.x_scales = x_scales;
   a.w = w;
   a.out = out;
+  const bool tiled = !fp8 && K % 8 == 0 && (swiglu ? N / 2 : N) % 8 == 0 && aligned_to(out, 16);
   const auto launch = [&](auto f, auto s) {
+    if constexpr (!f.value) {
+      if (tiled) {
+        hipLaunchKernelGGL((product_tile_kernel<kProduct, s.value, uint16_t>),
+                           dim3(kTileWorkgroups), dim3(kTileThreads), 0, stream, a);
+        return;
+      }
+    }
     hipLaunchKernelGGL((product_any_kernel<kProduct, f.value, s.value, uint16_t>), dim3(kAnyGrid),
                        dim3(256), 0, stream, a);
   };
@@ -284,8 +666,12 @@ ep_status_t ep_expert_product_backward_rows(const ep_experts_t *experts, const u
   a.w = w;
   a.grad = grad_out;
   a.out = grad_x;
-  hipLaunchKernelGGL((product_any_kernel<kRowsGrad, false, false, uint16_t>), dim3(kAnyGrid),
-                     dim3(256), 0, stream, a);
+  if (a.K % 8 == 0 && a.N % 8 == 0 && aligned_to(grad_x, 16))
+    hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, uint16_t>), dim3(kTileWorkgroups),
+                       dim3(kTileThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((product_any_kernel<kRowsGrad, false, false, uint16_t>), dim3(kAnyGrid),
+                       dim3(256), 0, stream, a);
   return launched("expert rows' gradient launch");
 }
 
@@ -316,7 +702,15 @@ ep_status_t ep_expert_product_backward_weights(
   a.grad = grad_out;
   a.add = add;
   a.out = grad_w;
+  const bool tiled = !fp8 && K % 8 == 0 && N % 8 == 0;
   const auto launch = [&](auto f, auto value) {
+    if constexpr (!f.value) {
+      if (tiled) {
+        hipLaunchKernelGGL((product_tile_kernel<kWeightsGrad, false, decltype(value)>),
+                           dim3(kTileWorkgroups), dim3(kTileThreads), 0, stream, a);
+        return;
+      }
+    }
     hipLaunchKernelGGL((product_any_kernel<kWeightsGrad, f.value, false, decltype(value)>),
                        dim3(kAnyGrid), dim3(256), 0, stream, a);
   };

@@ -55,8 +55,8 @@ struct ExpertRows {
 };
 
 // First block of each expert, numbered through all of them: starts[0 .. E],
-// where blocks_of(rows) is an expert's number of blocks.  Of a workgroup of 256
-// threads; totals holds 4.
+// where blocks_of(rows) is an expert's number of blocks.  Of a workgroup of at
+// least 256 threads; totals holds one value per wave.
 template <typename F>
 __device__ __forceinline__ void number_blocks(const ExpertRows &x, int32_t *starts,
                                               int32_t *totals, F blocks_of) {
