@@ -158,21 +158,20 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 // Tiles
 // --------------------------------------------------------------------------
 //
-// c[m, n] = sum_l a[m, l] b[n, l] in tiles of 256 x 256, 32 of l at a time.
+// c[m, n] = sum_l a[m, l] b[n, l] in tiles of 256 x 256, 64 of l at a time.
 // "Rows" is the side of m, "columns" that of n.  The matrix instruction takes
 // columns first, so that a lane's results are consecutive columns of one row.
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 256;            // rows and columns of a tile
-constexpr int kDepth = 32;            // of the sum, per stage
-constexpr int kStages = 4;            // in LDS: one in use, three on their way
+constexpr int kDepth = 64;            // of the sum, per stage
 constexpr int kSideBytes = kTile * kDepth * 2;
 constexpr int kStageBytes = 2 * kSideBytes;  // rows, then columns
-constexpr int kTileThreads = 512;
+constexpr int kTileWaves = 8;
 constexpr int kTileWorkgroups = 256;  // one per compute unit, by its LDS
 constexpr int kBand = 8;              // row tiles that go through the columns together
+constexpr int kLoads = kDepth / 16;   // of a wave, side and stage
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -184,19 +183,14 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
       :
-      : "s"(lds), "v"(offset), "s"(buffer)
+      : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
       : "memory");
 }
 
-// All but the newest `kLeft` loads have arrived, this wave's LDS reads are
-// done, and so for every wave of the workgroup.
-template <int kLeft>
+// All loads have arrived, this wave's LDS reads are done, and so for every
+// wave of the workgroup.
 __device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(kLeft) : "memory");
-}
-
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -262,22 +256,26 @@ struct Items {
   }
 };
 
-// One side of a stage is two loads per wave.  "Along": l is consecutive in
-// memory; 16 rows of 64 bytes per load, the 16-byte pieces of row r in LDS at
-// piece ^ (r / 4) % 4, so that the reads of 16 lanes of one piece cover all
-// banks.  "Across": m (or n) is consecutive; two l of 512 bytes per load, pieces
-// at piece ^ 4 (l % 4), so that the four l of a transposing read do.  What is
-// past the end of the sum, or of the rows, is outside the load's buffer and
-// zero; a column that is not there spoils its own results alone.
+// One side of a stage is four loads per wave.  "Along": l is consecutive in
+// memory; 8 rows of 128 bytes per load, the 16-byte pieces of row r in LDS at
+// piece ^ (r / 2) % 8, so that the reads of 16 lanes of one piece cover all
+// banks.  "Across": m (or n) is consecutive; two l of 512 bytes per load, units
+// of 32 bytes at unit ^ across_swizzle(l), so that the 8 l of 32 lanes of a
+// transposing read do.  What is past the end of the sum, or of the rows, is
+// outside the load's buffer and zero; a column that is not there spoils its own
+// results alone.
+__device__ __forceinline__ int across_swizzle(int l) { return (l & 3) | (l >> 3 & 1) << 2; }
+
 template <Kind KIND, bool SWIGLU, typename OUT>
-__global__ __launch_bounds__(kTileThreads, 2) void product_tile_kernel(ProductArgs a) {
+__global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(ProductArgs a) {
   constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
   constexpr int kOutTile = SWIGLU ? kTile / 2 : kTile;
-  __shared__ __align__(1024) uint8_t stage[kStages * kStageBytes];
-  __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[kTileThreads / 64];
+  __shared__ __align__(1024) uint8_t stage[2 * kStageBytes];
+  __shared__ __align__(16) uint8_t results[kTileWaves][2048];
+  __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[kTileWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int half = lane >> 5, l32 = lane & 31;
-  const int wr = wave >> 2, wc = wave & 3;  // of the wave's row and column tiles
+  const int l16 = lane & 15, quad = lane >> 4;
+  const int wr = wave >> 2, wc = wave & 3;  // of the wave's rows and columns
   const int K = a.K, N = a.N;
   const int out_cols = KIND == kProduct ? (SWIGLU ? N / 2 : N) : K;
   if (KIND != kWeightsGrad)
@@ -290,149 +288,187 @@ __global__ __launch_bounds__(kTileThreads, 2) void product_tile_kernel(ProductAr
   const int64_t to = from + per_xcd < count ? from + per_xcd : count;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_byte *)stage;
 
-  // where a lane's 16 bytes come from, from the base of its load on
-  const int64_t row_pitch = (int64_t)(KIND == kProduct ? K : N) * 2, col_pitch = (int64_t)K * 2;
-  const int piece_along = (lane & 3) ^ (lane >> 4 & 3);
-  const int piece_across = (lane & 31) ^ ((wave * 2 + half) & 3) << 2;
-  const uint32_t row_off = (uint32_t)(kRowsAcross ? half * row_pitch + piece_across * 16
-                                                  : (lane >> 2) * row_pitch + piece_along * 16);
-  const uint32_t col_off = (uint32_t)(kColsAcross ? half * col_pitch + piece_across * 16
-                                                  : (lane >> 2) * col_pitch + piece_along * 16);
+  // Where a lane's 16 bytes of a side's first load come from, from the wave's
+  // base on, and how far on each further load is.
+  const int row_pitch = (KIND == kProduct ? K : N) * 2, col_pitch = K * 2;
+  const int piece_along = (lane & 7) ^ ((wave & 1) << 2 | lane >> 4);
+  const int piece_across = (lane & 31) ^ across_swizzle(wave * 2 + (lane >> 5)) << 1;
+  const uint32_t row_off = kRowsAcross ? (lane >> 5) * row_pitch + piece_across * 16
+                                       : (lane >> 3) * row_pitch + piece_along * 16;
+  const uint32_t col_off = kColsAcross ? (lane >> 5) * col_pitch + piece_across * 16
+                                       : (lane >> 3) * col_pitch + piece_along * 16;
+  const uint32_t row_step = (kRowsAcross ? 16 : 64) * row_pitch;
+  const uint32_t col_step = (kColsAcross ? 16 : SWIGLU ? 32 : 64) * col_pitch;
 
-  // where a lane's parts of the instructions' operands are in a stage
-  int row_at[4], col_at[2];
-  const int swizzle = (l32 >> 2 & 3);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = 2 * i + wr;
-    row_at[i] = kRowsAcross
-                    ? (half * 8 + (lane & 15) / 4) * 512 +
-                          ((t * 4 + (lane >> 4 & 1) * 2 + (lane & 3) / 2) ^ ((lane & 15) / 4) << 2) * 16 +
-                          (lane & 1) * 8
-                    : (t * 32 + l32) * 64 + (half ^ swizzle) * 16;
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int t = wc * 2 + j;
-    col_at[j] = kSideBytes +
-                (kColsAcross
-                     ? (half * 8 + (lane & 15) / 4) * 512 +
-                           ((t * 4 + (lane >> 4 & 1) * 2 + (lane & 3) / 2) ^ ((lane & 15) / 4) << 2) * 16 +
-                           (lane & 1) * 8
-                     : (t * 32 + l32) * 64 + (half ^ swizzle) * 16);
-  }
-  const auto read_along = [&](int at, int ks) {
-    return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 32));
-  };
-  const auto read_across = [&](int at, int ks) {
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  // Where a lane's parts of the instructions' operands are in a stage: of its
+  // first 16 rows and columns.
+  const int along = l16 * 128 + (quad ^ l16 >> 1) * 16;
+  const int across = (quad * 8 + l16 / 4) * 512 + ((quad & 1) << 2 | l16 / 4) * 32 + l16 % 4 * 8;
+  const int row_at = kRowsAcross ? across ^ wr * 32 : along + wr * 2048;
+  const int col_at = kSideBytes + (kColsAcross ? across ^ wc * 128 : along + wc * 8192);
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const auto read_across = [&](int at) {
     struct {
       s16x4 lo, hi;
     } v;
-    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at + ks * 8192));
-    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at + ks * 8192 + 2048));
+    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at));
+    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at + 4 * 512));
     return __builtin_bit_cast(bf16x8, v);
   };
+  // rows 32 f + 16 wr .. + 15, columns 64 wc + 16 j .. + 15, half ks of a stage
+  const auto read_row = [&](int at0, int ks, int f) {
+    if constexpr (kRowsAcross)
+      return read_across((at0 + row_at ^ f * 64) + ks * 32 * 512);
+    else
+      return *reinterpret_cast<const bf16x8 *>(stage + (at0 + row_at ^ ks * 64) + f * 4096);
+  };
+  const auto read_col = [&](int at0, int ks, int j) {
+    if constexpr (kColsAcross)
+      return read_across((at0 + col_at ^ j * 32) + ks * 32 * 512);
+    else
+      return *reinterpret_cast<const bf16x8 *>(stage + (at0 + col_at ^ ks * 64) + j * 2048);
+  };
 
-  for (int64_t item = from + blockIdx.x / 8; item < to; item += gridDim.x / 8) {
+  // The loads run one stage ahead of the products, through the items' ends.
+  const int64_t next = gridDim.x / 8;
+  int64_t load_item = from + blockIdx.x / 8;
+  const uint8_t *row_base = nullptr, *col_base = nullptr;
+  int row_bytes = 0, col_bytes = 0;  // along: from the base to the last row's end
+  int row_skip = 0, col_skip = 0;    // across: bytes before the tile's first column
+  int left = 0;                      // of the item's sum, from the next stage on
+  const auto start = [&]() {         // of the item that the loads are at
+    Item it;
+    items.get(load_item, &it, kOutTile);
+    left = it.length;
+    if (kRowsAcross) {
+      row_skip = it.row0 * 2;
+      row_base = reinterpret_cast<const uint8_t *>(a.grad) +
+                 (it.first + wave * 2) * (int64_t)row_pitch + row_skip;
+    } else {
+      row_base = static_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
+                 (it.first + it.row0 + wave * 8) * (int64_t)row_pitch;
+      row_bytes = (it.rows - wave * 8) * row_pitch;
+    }
+    if (kColsAcross) {
+      col_skip = it.col0 * 2;
+      col_base = (KIND == kRowsGrad
+                      ? reinterpret_cast<const uint8_t *>(a.w) +
+                            ((int64_t)it.e * N + wave * 2) * col_pitch
+                      : static_cast<const uint8_t *>(a.x) +
+                            (it.first + wave * 2) * (int64_t)col_pitch) +
+                 col_skip;
+    } else {
+      // SwiGLU: 32 columns of the gate, then the same of up, for each wc
+      const int n = it.col0 + (SWIGLU ? wave % 4 * 8 : wave * 8);
+      const int there = out_cols - n < kTile ? out_cols - n : kTile;
+      col_base = reinterpret_cast<const uint8_t *>(a.w) +
+                 ((int64_t)it.e * N + n + (SWIGLU ? wave / 4 * out_cols : 0)) * col_pitch;
+      col_bytes = there * col_pitch;
+    }
+  };
+  const auto advance = [&]() {
+    while (left <= 0 && load_item < to) {
+      load_item += next;
+      if (load_item < to) start();
+    }
+  };
+  const auto issue = [&](uint32_t stage_number) {
+    const uint32_t lds = lds0 + (stage_number & 1) * kStageBytes + wave * 1024;
+    const bool in = piece_along * 8 < left;
+    const int l2 = left - wave * 2 < kDepth ? left - wave * 2 : kDepth;
+    const int rb = left <= 0 ? 0 : kRowsAcross ? l2 * row_pitch - row_skip : row_bytes;
+    const u32x4 rows = buffer_of(row_base, rb < 0 ? 0 : rb);
+    const uint32_t ro = kRowsAcross || in ? row_off : kNowhere;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load_to_lds(lds + i * 8192, ro + i * row_step, rows);
+    const int cb = left <= 0 ? 0 : kColsAcross ? l2 * col_pitch - col_skip : col_bytes;
+    const u32x4 cols = buffer_of(col_base, cb < 0 ? 0 : cb);
+    const uint32_t co = kColsAcross || in ? col_off : kNowhere;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(lds + kSideBytes + i * 8192, co + i * col_step, cols);
+    row_base += kRowsAcross ? (int64_t)kDepth * row_pitch : kDepth * 2;
+    col_base += kColsAcross ? (int64_t)kDepth * col_pitch : kDepth * 2;
+    row_bytes -= kDepth * 2;
+    col_bytes -= kDepth * 2;
+    left -= kDepth;
+  };
+
+  if (load_item < to) start();
+  advance();
+  uint32_t g = 0;  // stages used up
+  issue(0);
+  advance();
+  stage_barrier();
+  issue(1);
+  advance();
+  // Here and at the end of each item: stage g is there, g + 1 on its way.
+  for (int64_t item = from + blockIdx.x / 8; item < to; item += next) {
     Item it;
     items.get(item, &it, kOutTile);
-    // bases of this wave's loads, at the first of the sum
-    const uint8_t *row_base[2], *col_base[2];
-    int row_bytes[2], col_bytes[2];  // along: of the rows there are
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int group = i * 8 + wave;
-      if (kRowsAcross) {
-        row_base[i] = reinterpret_cast<const uint8_t *>(a.grad) +
-                      (it.first + group * 2) * row_pitch + it.row0 * 2;
-      } else {
-        const int have = it.rows - group * 16;
-        row_base[i] = reinterpret_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
-                      (it.first + it.row0 + group * 16) * row_pitch;
-        row_bytes[i] = (have < 0 ? 0 : have < 16 ? have : 16) * (int)row_pitch;
-      }
-      if (KIND == kProduct) {
-        const int r = group * 16;
-        const int n = SWIGLU ? it.col0 + r / 64 * 32 + r % 32 : it.col0 + r;
-        const int have = out_cols - n;
-        col_base[i] = reinterpret_cast<const uint8_t *>(a.w) +
-                      ((int64_t)it.e * N + n + (SWIGLU ? r % 64 / 32 * out_cols : 0)) * col_pitch;
-        col_bytes[i] = (have < 0 ? 0 : have < 16 ? have : 16) * (int)col_pitch;
-      } else {
-        col_base[i] = (KIND == kRowsGrad
-                           ? reinterpret_cast<const uint8_t *>(a.w) +
-                                 ((int64_t)it.e * N + group * 2) * col_pitch
-                           : static_cast<const uint8_t *>(a.x) + (it.first + group * 2) * col_pitch) +
-                      it.col0 * 2;
-      }
-    }
-    uint32_t at = 0;  // of the sum, of the next stage to load
-    const auto issue = [&](int buf) {
-      const uint32_t lds = lds0 + buf * kStageBytes + wave * 1024;
-      const int left = (int)((uint32_t)it.length - at);
-      const bool in = piece_along * 8 < left;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int have = left - (i * 8 + wave) * 2;  // across: of this load's two l
-        const int n = kRowsAcross
-                          ? (have < 0 ? 0 : have < 2 ? have : 2) * (int)row_pitch - it.row0 * 2
-                          : row_bytes[i] - (int)at * 2;
-        load_to_lds(lds + i * 8192, kRowsAcross || in ? row_off : kNowhere,
-                    buffer_of(row_base[i], n < 0 ? 0 : n));
-        row_base[i] += kRowsAcross ? kDepth * row_pitch : kDepth * 2;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int have = left - (i * 8 + wave) * 2;
-        const int n = kColsAcross
-                          ? (have < 0 ? 0 : have < 2 ? have : 2) * (int)col_pitch - it.col0 * 2
-                          : col_bytes[i] - (int)at * 2;
-        load_to_lds(lds + kSideBytes + i * 8192, kColsAcross || in ? col_off : kNowhere,
-                    buffer_of(col_base[i], n < 0 ? 0 : n));
-        col_base[i] += kColsAcross ? kDepth * col_pitch : kDepth * 2;
-      }
-      at += kDepth;
-    };
     const int steps = (int)(((uint32_t)it.length + kDepth - 1) / kDepth);
 
     const auto tile = [&](auto count) {
-      constexpr int kM = decltype(count)::value;
-      f32x16 acc[kM][2];
+      constexpr int kM = decltype(count)::value;  // 64 rows each
+      f32x4 acc[2 * kM][4];
 #pragma unroll
-      for (int m = 0; m < kM; ++m)
+      for (int f = 0; f < 2 * kM; ++f)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
+      bf16x8 c[2][4], r[2][kM];
+      const auto read_cols = [&](int at0, int ks) {
 #pragma unroll
-          for (int v = 0; v < 16; ++v) acc[m][j][v] = 0.0f;
-      issue(0);
-      issue(1);
-      issue(2);
-      for (int s = 0; s < steps; ++s) {
-        const int at0 = (s & 3) * kStageBytes;
-        stage_barrier<8>();  // this stage is there, and the last one's buffer is free
-        issue((s + 3) & 3);
+        for (int j = 0; j < 4; ++j) c[ks][j] = read_col(at0, ks, j);
+      };
+      const auto read_rows = [&](int at0, int ks, int h) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          bf16x8 c[2], r[kM];
+        for (int f = 0; f < kM; ++f) r[h][f] = read_row(at0, ks, h * kM + f);
+      };
+      const auto products = [&](int ks, int h) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            c[j] = kColsAcross ? read_across(at0 + col_at[j], ks) : read_along(at0 + col_at[j], ks);
+        for (int f = 0; f < kM; ++f)
 #pragma unroll
-          for (int m = 0; m < kM; ++m)
-            r[m] = kRowsAcross ? read_across(at0 + row_at[m], ks) : read_along(at0 + row_at[m], ks);
-#pragma unroll
-          for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[m][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[j], r[m], acc[m][j], 0, 0, 0);
-        }
+          for (int j = 0; j < 4; ++j) acc[h * kM + f][j] = mul(c[ks][j], r[h][f], acc[h * kM + f][j]);
+      };
+      const auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
+      if (steps > 0) {
+        read_cols((g & 1) * kStageBytes, 0);
+        read_rows((g & 1) * kStageBytes, 0, 0);
       }
-      stage_barrier<0>();  // every stage is free
-      // Results go through 4 KB of LDS per wave, 32 rows at a time, to leave in
+      // Each quarter's operands are read during the one before.
+      for (int s = 0; s < steps; ++s, ++g) {
+        const int at0 = (g & 1) * kStageBytes;
+        read_rows(at0, 0, 1);
+        pin();
+        products(0, 0);
+        pin();
+        read_cols(at0, 1);
+        read_rows(at0, 1, 0);
+        pin();
+        products(0, 1);
+        pin();
+        read_rows(at0, 1, 1);
+        pin();
+        products(1, 0);
+        pin();
+        stage_barrier();  // the next stage is there, and this one's buffer free
+        read_cols(at0 ^ kStageBytes, 0);
+        read_rows(at0 ^ kStageBytes, 0, 0);
+        pin();
+        issue(g + 2);
+        pin();
+        products(1, 1);
+        pin();
+        if (left <= 0) advance();
+      }
+      // Results go through 2 KB of LDS per wave, 16 rows at a time, to leave in
       // whole lines; in fp32 where something is added before the rounding.  A
-      // lane has row l32 and columns 8 q + 4 half .. + 3.
-      uint8_t *mine = stage + wave * 4096;
+      // lane has row l16 and columns 4 quad .. + 3 of each 16.
+      uint8_t *mine = results[wave];
+      // kept here: worked out before the loop over items, what the results'
+      // addresses hold would stay in registers through it
+      int at_lane = lane;
+      asm volatile("" : "+v"(at_lane));
       const auto finish = [&](auto f32) {
         constexpr bool kF32 = decltype(f32)::value;
         constexpr int kPasses = kF32 ? 2 : 1;              // of columns
@@ -444,29 +480,27 @@ __global__ __launch_bounds__(kTileThreads, 2) void product_tile_kernel(ProductAr
           return row * (kPieces * 16) + (piece ^ (kPieces == 8 ? row & 7 : row >> 1 & 3)) * 16;
         };
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+        for (int f = 0; f < 2 * kM; ++f)
 #pragma unroll
           for (int pass = 0; pass < kPasses; ++pass) {
 #pragma unroll
-            for (int j = 0; j < kCols / 32; ++j)
+            for (int j = 0; j < kCols / 16; ++j) {
+              f32x4 y = acc[f][pass * 2 + j];
+              if constexpr (SWIGLU) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                f32x4 y;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                  y[v] = acc[m][kF32 ? pass : j][q * 4 + v];
-                  if (SWIGLU) y[v] = silu_of(y[v]) * acc[m][1][q * 4 + v];
-                }
-                if constexpr (kF32)
-                  *reinterpret_cast<f32x4 *>(mine + swizzled(l32, q * 2 + half)) = y;
-                else
-                  *reinterpret_cast<u32x2 *>(mine + swizzled(l32, j * 4 + q) + half * 8) =
-                      u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+                for (int v = 0; v < 4; ++v) y[v] = silu_of(y[v]) * acc[f][2 + j][v];
               }
+              if constexpr (kF32)
+                *reinterpret_cast<f32x4 *>(mine + swizzled(at_lane & 15, j * 4 + at_lane / 16)) = y;
+              else
+                *reinterpret_cast<u32x2 *>(mine + swizzled(at_lane & 15, j * 2 + at_lane / 32) +
+                                           (at_lane & 16) / 2) =
+                    u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+            }
 #pragma unroll
-            for (int i = 0; i < kStores / 2; ++i) {
-              const int row = i * (64 / kStores) + lane / kStores, piece = lane % kStores;
-              const int r = (2 * m + wr) * 32 + row;
+            for (int i = 0; i < kStores / 4; ++i) {
+              const int row = i * (64 / kStores) + at_lane / kStores, piece = at_lane % kStores;
+              const int r = f * 32 + wr * 16 + row;
               const int col = it.col0 + (SWIGLU ? wc * 32 : wc * 64 + pass * 32) + piece * kOutCols;
               const int64_t to_row = KIND == kWeightsGrad ? (int64_t)it.e * N + it.row0 + r
                                                           : it.first + it.row0 + r;
@@ -517,7 +551,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void product_tile_kernel(ProductAr
       } else {
         finish(std::false_type{});
       }
-      lds_barrier();  // the buffers are free for the next tile
     };
     switch ((it.rows + 63) / 64) {
       case 1: tile(std::integral_constant<int, 1>{}); break;
@@ -526,6 +559,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void product_tile_kernel(ProductAr
       default: tile(std::integral_constant<int, 4>{}); break;
     }
   }
+  stage_barrier();  // no load may write to LDS after the end
 }
 
 #define EP_TRY(expr)                \
@@ -626,7 +660,7 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
     if constexpr (!f.value) {
       if (tiled) {
         hipLaunchKernelGGL((product_tile_kernel<kProduct, s.value, uint16_t>),
-                           dim3(kTileWorkgroups), dim3(kTileThreads), 0, stream, a);
+                           dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
         return;
       }
     }
@@ -668,7 +702,7 @@ ep_status_t ep_expert_product_backward_rows(const ep_experts_t *experts, const u
   a.out = grad_x;
   if (a.K % 8 == 0 && a.N % 8 == 0 && aligned_to(grad_x, 16))
     hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, uint16_t>), dim3(kTileWorkgroups),
-                       dim3(kTileThreads), 0, stream, a);
+                       dim3(kTileWaves * 64), 0, stream, a);
   else
     hipLaunchKernelGGL((product_any_kernel<kRowsGrad, false, false, uint16_t>), dim3(kAnyGrid),
                        dim3(256), 0, stream, a);
@@ -707,7 +741,7 @@ ep_status_t ep_expert_product_backward_weights(
     if constexpr (!f.value) {
       if (tiled) {
         hipLaunchKernelGGL((product_tile_kernel<kWeightsGrad, false, decltype(value)>),
-                           dim3(kTileWorkgroups), dim3(kTileThreads), 0, stream, a);
+                           dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
         return;
       }
     }
