@@ -197,6 +197,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
 }
 
+// Two 16 bytes of a row per lane, rows by lane % 16, become those of rows
+// lane % 8 (a) and lane % 8 + 8 (b), the second ones in lanes 8 .. 15 of each 16.
+__device__ __forceinline__ void halve_rows(u32x4 *a, u32x4 *b) {
+  constexpr int kRor8 = 0x128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = (int)(*a)[i], y = (int)(*b)[i];
+    (*a)[i] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, kRor8, 0xF, 0xC, false);
+    (*b)[i] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, kRor8, 0xF, 0x3, false);
+  }
+}
+
 __device__ __forceinline__ u32x4 buffer_of(const void *base, uint32_t bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
   return u32x4{(uint32_t)uniform((int)p), (uint32_t)uniform((int)(p >> 32)) & 0xFFFFu,
@@ -271,9 +283,11 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
   constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
   constexpr int kOutTile = SWIGLU ? kTile / 2 : kTile;
   __shared__ __align__(1024) uint8_t stage[2 * kStageBytes];
-  __shared__ __align__(16) uint8_t results[kTileWaves][2048];
   __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[kTileWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  // non-temporal stores of the weights' gradient, which nobody reads soon (bf16, 32
+  // experts of 4096 x 7168: 2056 us, without 2140)
+  constexpr int kOnceOut = KIND == kWeightsGrad ? 2 : 0;
   const int l16 = lane & 15, quad = lane >> 4;
   const int wr = wave >> 2, wc = wave & 3;  // of the wave's rows and columns
   const int K = a.K, N = a.N;
@@ -366,43 +380,59 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
       col_bytes = there * col_pitch;
     }
   };
-  const auto advance = [&]() {
-    while (left <= 0 && load_item < to) {
-      load_item += next;
-      if (load_item < to) start();
-    }
-  };
-  const auto issue = [&](uint32_t stage_number) {
-    const uint32_t lds = lds0 + (stage_number & 1) * kStageBytes + wave * 1024;
+  // A stage's loads go out one at a time between products: together they would
+  // hold up every wave until the last was taken.
+  int row_there = 0, col_there = 0;  // bytes from the bases on
+  uint32_t row_from = 0, col_from = 0, load_lds = 0;
+  const auto begin_stage = [&](uint32_t stage_number) {
+    load_lds = lds0 + (stage_number & 1) * kStageBytes + wave * 1024;
     const bool in = piece_along * 8 < left;
     const int l2 = left - wave * 2 < kDepth ? left - wave * 2 : kDepth;
     const int rb = left <= 0 ? 0 : kRowsAcross ? l2 * row_pitch - row_skip : row_bytes;
-    const u32x4 rows = buffer_of(row_base, rb < 0 ? 0 : rb);
-    const uint32_t ro = kRowsAcross || in ? row_off : kNowhere;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_to_lds(lds + i * 8192, ro + i * row_step, rows);
     const int cb = left <= 0 ? 0 : kColsAcross ? l2 * col_pitch - col_skip : col_bytes;
-    const u32x4 cols = buffer_of(col_base, cb < 0 ? 0 : cb);
-    const uint32_t co = kColsAcross || in ? col_off : kNowhere;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      load_to_lds(lds + kSideBytes + i * 8192, co + i * col_step, cols);
+    row_there = uniform(rb < 0 ? 0 : rb);
+    col_there = uniform(cb < 0 ? 0 : cb);
+    row_from = kRowsAcross || in ? row_off : kNowhere;
+    col_from = kColsAcross || in ? col_off : kNowhere;
+  };
+  const auto load_part = [&](int i) {  // 0 .. 2 kLoads - 1
+    if (i < kLoads)
+      load_to_lds(load_lds + kSideBytes + i * 8192, col_from + i * col_step,
+                  buffer_of(col_base, col_there));
+    else
+      load_to_lds(load_lds + (i - kLoads) * 8192, row_from + (i - kLoads) * row_step,
+                  buffer_of(row_base, row_there));
+  };
+  const auto end_stage = [&]() {
     row_base += kRowsAcross ? (int64_t)kDepth * row_pitch : kDepth * 2;
     col_base += kColsAcross ? (int64_t)kDepth * col_pitch : kDepth * 2;
     row_bytes -= kDepth * 2;
     col_bytes -= kDepth * 2;
     left -= kDepth;
+    while (left <= 0 && load_item < to) {
+      load_item += next;
+      if (load_item < to) start();
+    }
   };
 
   if (load_item < to) start();
-  advance();
+  left += kDepth;  // end_stage() finds the first item that has a sum
+  row_base -= kRowsAcross ? (int64_t)kDepth * row_pitch : kDepth * 2;
+  col_base -= kColsAcross ? (int64_t)kDepth * col_pitch : kDepth * 2;
+  row_bytes += kDepth * 2;
+  col_bytes += kDepth * 2;
+  end_stage();
   uint32_t g = 0;  // stages used up
-  issue(0);
-  advance();
+  begin_stage(0);
+#pragma unroll
+  for (int i = 0; i < 2 * kLoads; ++i) load_part(i);
+  end_stage();
   stage_barrier();
-  issue(1);
-  advance();
-  // Here and at the end of each item: stage g is there, g + 1 on its way.
+  begin_stage(1);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) load_part(i);
+  // Here and at the end of each item: stage g is there, the first half of the
+  // loads of g + 1 are out.
   for (int64_t item = from + blockIdx.x / 8; item < to; item += next) {
     Item it;
     items.get(item, &it, kOutTile);
@@ -424,13 +454,21 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
 #pragma unroll
         for (int f = 0; f < kM; ++f) r[h][f] = read_row(at0, ks, h * kM + f);
       };
-      const auto products = [&](int ks, int h) {
+      const auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
+      // part: the first of the loads that go out with these products, or none
+      const auto products = [&](int ks, int h, int part) {
 #pragma unroll
-        for (int f = 0; f < kM; ++f)
+        for (int f = 0; f < kM; ++f) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[h * kM + f][j] = mul(c[ks][j], r[h][f], acc[h * kM + f][j]);
+          if (part >= 0) {
+            pin();
+#pragma unroll
+            for (int i = f * kLoads / kM; i < (f + 1) * kLoads / kM; ++i) load_part(part + i);
+            pin();
+          }
+        }
       };
-      const auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
       if (steps > 0) {
         read_cols((g & 1) * kStageBytes, 0);
         read_rows((g & 1) * kStageBytes, 0, 0);
@@ -440,116 +478,113 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
         const int at0 = (g & 1) * kStageBytes;
         read_rows(at0, 0, 1);
         pin();
-        products(0, 0);
+        products(0, 0, kLoads);
         pin();
         read_cols(at0, 1);
         read_rows(at0, 1, 0);
         pin();
-        products(0, 1);
+        end_stage();
+        products(0, 1, -1);
         pin();
         read_rows(at0, 1, 1);
         pin();
-        products(1, 0);
+        products(1, 0, -1);
         pin();
         stage_barrier();  // the next stage is there, and this one's buffer free
         read_cols(at0 ^ kStageBytes, 0);
         read_rows(at0 ^ kStageBytes, 0, 0);
+        begin_stage(g + 2);
         pin();
-        issue(g + 2);
+        products(1, 1, 0);
         pin();
-        products(1, 1);
-        pin();
-        if (left <= 0) advance();
       }
-      // Results go through 2 KB of LDS per wave, 16 rows at a time, to leave in
-      // whole lines; in fp32 where something is added before the rounding.  A
-      // lane has row l16 and columns 4 quad .. + 3 of each 16.
-      uint8_t *mine = results[wave];
-      // kept here: worked out before the loop over items, what the results'
-      // addresses hold would stay in registers through it
+      // A lane has row l16 and columns 4 quad .. + 3 of each 16.  The values
+      // change places between lanes so that a store writes whole lines (with 64
+      // bytes per row the weights' gradient of 32 experts, 4096 x 7168, takes 2232
+      // us instead of 2040; through LDS 2056).  Rows that are not there are outside
+      // the buffer of the stores.
+      constexpr int kSize = sizeof(OUT), kHere = SWIGLU ? 2 : 4;  // 16 columns each
+      const int64_t to_row =
+          KIND == kWeightsGrad ? (int64_t)it.e * N + it.row0 : it.first + it.row0;
+      const int pitch = out_cols * kSize;
+      const int64_t skip = (to_row * out_cols + it.col0) * kSize;
+      const auto out = __builtin_amdgcn_make_buffer_rsrc(
+          static_cast<uint8_t *>(a.out) + skip, 0, it.rows * pitch - it.col0 * kSize, 0x00020000);
+      const auto add = __builtin_amdgcn_make_buffer_rsrc(
+          static_cast<uint8_t *>(const_cast<void *>(a.add)) + skip, 0,
+          a.add == nullptr ? 0 : it.rows * pitch - it.col0 * kSize, 0x00020000);
+      // kept here: worked out before the loop over items, these would be held
+      // in registers through it
       int at_lane = lane;
       asm volatile("" : "+v"(at_lane));
-      const auto finish = [&](auto f32) {
-        constexpr bool kF32 = decltype(f32)::value;
-        constexpr int kPasses = kF32 ? 2 : 1;              // of columns
-        constexpr int kCols = (SWIGLU || kF32) ? 32 : 64;  // of a pass
-        constexpr int kPieces = kCols * (kF32 ? 4 : 2) / 16;  // 16-byte pieces of a row in LDS
-        constexpr int kOutCols = 16 / (int)sizeof(OUT);       // of a store
-        constexpr int kStores = kCols / kOutCols;             // of a row
-        const auto swizzled = [&](int row, int piece) {
-          return row * (kPieces * 16) + (piece ^ (kPieces == 8 ? row & 7 : row >> 1 & 3)) * 16;
-        };
+      const int row = wr * 16 + (at_lane & 15), at_quad = at_lane >> 4;
+      const int wave_col = wc * 16 * kHere;  // of the wave's first, in the tile
+      const auto from = [&](int r, int col) {  // offset of a row and a column of the wave's
+        return it.col0 + wave_col + col < out_cols
+                   ? (uint32_t)(r * pitch + (wave_col + col) * kSize) : kNowhere;
+      };
+      const int row8 = wr * 16 + (at_lane & 7), second = at_lane >> 3 & 1;
 #pragma unroll
-        for (int f = 0; f < 2 * kM; ++f)
+      for (int f = 0; f < 2 * kM; ++f) {
+        const uint32_t down = f * 32 * pitch;
+        if constexpr (kSize == 4) {
 #pragma unroll
-          for (int pass = 0; pass < kPasses; ++pass) {
+          for (int j = 0; j < 4; j += 2) {
+            u32x4 y[2] = {__builtin_bit_cast(u32x4, acc[f][j]),
+                          __builtin_bit_cast(u32x4, acc[f][j + 1])};
+            halve_rows(&y[0], &y[1]);
 #pragma unroll
-            for (int j = 0; j < kCols / 16; ++j) {
-              f32x4 y = acc[f][pass * 2 + j];
-              if constexpr (SWIGLU) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) y[v] = silu_of(y[v]) * acc[f][2 + j][v];
-              }
-              if constexpr (kF32)
-                *reinterpret_cast<f32x4 *>(mine + swizzled(at_lane & 15, j * 4 + at_lane / 16)) = y;
-              else
-                *reinterpret_cast<u32x2 *>(mine + swizzled(at_lane & 15, j * 2 + at_lane / 32) +
-                                           (at_lane & 16) / 2) =
-                    u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-            }
-#pragma unroll
-            for (int i = 0; i < kStores / 4; ++i) {
-              const int row = i * (64 / kStores) + at_lane / kStores, piece = at_lane % kStores;
-              const int r = f * 32 + wr * 16 + row;
-              const int col = it.col0 + (SWIGLU ? wc * 32 : wc * 64 + pass * 32) + piece * kOutCols;
-              const int64_t to_row = KIND == kWeightsGrad ? (int64_t)it.e * N + it.row0 + r
-                                                          : it.first + it.row0 + r;
-              const int64_t at_out = to_row * out_cols + col;
-              u32x4 v;
-              if constexpr (!kF32) {
-                v = *reinterpret_cast<const u32x4 *>(mine + swizzled(row, piece));
-                if (r >= it.rows || col >= out_cols) continue;
-              } else {
-                f32x4 y[kOutCols / 4];
-#pragma unroll
-                for (int p = 0; p < kOutCols / 4; ++p)
-                  y[p] = *reinterpret_cast<const f32x4 *>(
-                      mine + swizzled(row, piece * (kOutCols / 4) + p));
-                if (r >= it.rows || col >= out_cols) continue;
-                if (a.add != nullptr) {
-                  const u32x4 b = *reinterpret_cast<const u32x4 *>(
-                      static_cast<const OUT *>(a.add) + at_out);
-                  if constexpr (std::is_same<OUT, float>::value) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) y[0][c] += __uint_as_float(b[c]);
-                  } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                      y[c / 4][c % 4] += __uint_as_float(c % 2 ? b[c / 2] & 0xFFFF0000u
-                                                               : b[c / 2] << 16);
-                  }
-                }
-                if constexpr (std::is_same<OUT, float>::value) {
-                  v = __builtin_bit_cast(u32x4, y[0]);
-                } else {
-#pragma unroll
-                  for (int c = 0; c < 4; ++c)
-                    v[c] = pack_bf16(y[c / 2][c % 2 * 2], y[c / 2][c % 2 * 2 + 1]);
-                }
-              }
-              *reinterpret_cast<u32x4 *>(static_cast<OUT *>(a.out) + at_out) = v;
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t at = from(row8 + h * 8, (j + second) * 16 + at_quad * 4) + down;
+              if (a.add != nullptr)
+                y[h] = __builtin_bit_cast(
+                    u32x4, __builtin_bit_cast(f32x4, y[h]) +
+                               __builtin_bit_cast(
+                                   f32x4, __builtin_amdgcn_raw_buffer_load_b128(add, at, 0, 0)));
+              __builtin_amdgcn_raw_buffer_store_b128(y[h], out, at, 0, kOnceOut);
             }
           }
-      };
-      if constexpr (std::is_same<OUT, float>::value) {
-        finish(std::true_type{});
-      } else if constexpr (KIND == kWeightsGrad) {
-        if (a.add != nullptr)
-          finish(std::true_type{});
-        else
-          finish(std::false_type{});
-      } else {
-        finish(std::false_type{});
+        } else {
+          uint32_t w[kHere][2];
+#pragma unroll
+          for (int j = 0; j < kHere; ++j) {
+            f32x4 y = acc[f][j];
+            if constexpr (SWIGLU) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) y[v] = silu_of(y[v]) * acc[f][2 + j][v];
+            }
+            if (KIND == kWeightsGrad && a.add != nullptr) {
+              const u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(
+                  add, from(row, j * 16 + at_quad * 4) + down, 0, 0);
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                y[v] += __uint_as_float(v % 2 ? b[v / 2] & 0xFFFF0000u : b[v / 2] << 16);
+            }
+            w[j][0] = pack_bf16(y[0], y[1]);
+            w[j][1] = pack_bf16(y[2], y[3]);
+          }
+          // lane quad (q1, q0) with 16 columns (j1, j0) becomes lane quad (j0, q1)
+          // with 8 columns q0 of piece j1
+          u32x4 v[kHere / 2];
+#pragma unroll
+          for (int j = 0; j < kHere; j += 2)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const auto x = __builtin_amdgcn_permlane32_swap(w[j][p], w[j + 1][p], false, false);
+              const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+              v[j / 2][p] = y[0];
+              v[j / 2][2 + p] = y[1];
+            }
+          if constexpr (SWIGLU) {
+            __builtin_amdgcn_raw_buffer_store_b128(v[0], out, from(row, at_quad * 8) + down, 0, 0);
+          } else {
+            halve_rows(&v[0], &v[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  v[h], out, from(row8 + h * 8, second * 32 + at_quad * 8) + down, 0, kOnceOut);
+          }
+        }
       }
     };
     switch ((it.rows + 63) / 64) {
