@@ -167,7 +167,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kTile = 256;            // rows and columns of a tile
 constexpr int kDepth = 64;            // of the sum, per stage
 constexpr int kSideBytes = kTile * kDepth * 2;
-constexpr int kStageBytes = 2 * kSideBytes;  // rows, then columns
+constexpr int kSlots = 5;             // of a side in LDS: all of it
 constexpr int kTileWaves = 8;
 constexpr int kTileWorkgroups = 256;  // one per compute unit, by its LDS
 constexpr int kBand = 8;              // row tiles that go through the columns together
@@ -187,10 +187,11 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4
       : "memory");
 }
 
-// All loads have arrived, this wave's LDS reads are done, and so for every
-// wave of the workgroup.
+// All but the newest kLeft loads and stores are done, and this wave's LDS
+// reads, and so for every wave of the workgroup.
+template <int kLeft>
 __device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(kLeft) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -227,37 +228,73 @@ struct Item {
   int length;      // of the sum
 };
 
+// Row tiles of an expert.
+__device__ __forceinline__ int row_tiles_of(int64_t rows) {
+  return (int)((rows + kTile - 1) / kTile);
+}
+
 // The numbering of items: an expert's tiles are consecutive, in bands of kBand
-// row tiles that take the columns one after the other.
+// row tiles that take the columns one after the other.  A wave finds its items
+// in ascending order by itself: it holds the row tiles of 64 experts, one per
+// lane, and goes on to the next 64 when it is past them.
 template <Kind KIND>
 struct Items {
   const ProductArgs &a;
-  const int32_t *starts;
-  int row_tiles, col_tiles;
+  int row_tiles, col_tiles;  // of the weights' gradient; of all kinds
+  int chunk = -1;            // experts 64 chunk .. + 63
+  int32_t before = 0, end = 0;     // row tiles before the chunk's, and through it
+  int32_t first_tile = 0, tiles = 0;  // of this lane's expert
 
-  __device__ __forceinline__ int64_t count() const {
-    return (KIND == kWeightsGrad ? (int64_t)a.rows.E * row_tiles : (int64_t)starts[a.rows.E]) *
-           col_tiles;
+  __device__ __forceinline__ int lane_tiles(int c) const {
+    const int e = c * 64 + (threadIdx.x & 63);
+    int64_t first, rows = 0;
+    if (e < a.rows.E)
+      rows_inside(a.rows.offsets[e], a.rows.counts[e], a.rows.capacity, &first, &rows);
+    return row_tiles_of(rows);
   }
-  __device__ __forceinline__ void get(int64_t item, Item *it, int out_cols_per_tile) const {
-    const int32_t block = (int32_t)(item / col_tiles);  // as if rows came first
-    int e, tiles, before;
-    int64_t rows;
+  __device__ __forceinline__ int64_t count() const {
+    if (KIND == kWeightsGrad) return (int64_t)a.rows.E * row_tiles * col_tiles;
+    int total = 0;
+    for (int c = 0; c * 64 < a.rows.E; ++c) total += lane_tiles(c);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+    return (int64_t)uniform(total) * col_tiles;
+  }
+  // item is less than count(), and not less than at the call before
+  __device__ __forceinline__ void get(int64_t item, Item *it, int out_cols_per_tile) {
+    const int32_t block = uniform((int)(item / col_tiles));  // as if rows came first
+    int e, high, start;
     if (KIND == kWeightsGrad) {
       e = uniform(block / row_tiles);
-      tiles = row_tiles;
-      before = e * row_tiles;
+      high = row_tiles;
+      start = e * row_tiles;
     } else {
-      e = expert_of(starts, a.rows.E, block);
-      before = uniform(starts[e]);
-      tiles = uniform(starts[e + 1]) - before;
+      while (block >= end) {
+        ++chunk;
+        before = end;
+        tiles = lane_tiles(chunk);
+        int at = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const int up = __shfl_up(at, d);
+          at += (int)(threadIdx.x & 63) >= d ? up : 0;
+        }
+        first_tile = before + at - tiles;
+        end = before + __builtin_amdgcn_readlane(at, 63);
+      }
+      const uint64_t from_here = __ballot(tiles > 0 && first_tile <= block);
+      const int l = 63 - __builtin_clzll(from_here);
+      e = chunk * 64 + l;
+      start = __builtin_amdgcn_readlane(first_tile, l);
+      high = __builtin_amdgcn_readlane(tiles, l);
     }
+    int64_t rows;
     rows_inside(uniform(a.rows.offsets[e]), uniform(a.rows.counts[e]), a.rows.capacity, &it->first,
                 &rows);
-    const int64_t in_expert = item - (int64_t)before * col_tiles;
+    const int64_t in_expert = item - (int64_t)start * col_tiles;
     const int band = (int)(in_expert / ((int64_t)kBand * col_tiles));
     const int in_band = (int)(in_expert - (int64_t)band * kBand * col_tiles);
-    const int high = tiles - band * kBand < kBand ? tiles - band * kBand : kBand;
+    high = high - band * kBand < kBand ? high - band * kBand : kBand;
     const int rt = uniform(band * kBand + in_band % high), ct = uniform(in_band / high);
     it->e = e;
     it->row0 = rt * kTile;
@@ -282,19 +319,18 @@ template <Kind KIND, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(ProductArgs a) {
   constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
   constexpr int kOutTile = SWIGLU ? kTile / 2 : kTile;
-  __shared__ __align__(1024) uint8_t stage[2 * kStageBytes];
-  __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[kTileWaves];
+  __shared__ __align__(1024) uint8_t stage[kSlots * kSideBytes];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   // non-temporal stores of the weights' gradient, which nobody reads soon (bf16, 32
   // experts of 4096 x 7168: 2056 us, without 2140)
   constexpr int kOnceOut = KIND == kWeightsGrad ? 2 : 0;
+  constexpr int kSize = sizeof(OUT);
+  constexpr int kStores = SWIGLU ? 2 : kSize * 2;  // of a wave, per 64 rows of a tile
   const int l16 = lane & 15, quad = lane >> 4;
   const int wr = wave >> 2, wc = wave & 3;  // of the wave's rows and columns
   const int K = a.K, N = a.N;
   const int out_cols = KIND == kProduct ? (SWIGLU ? N / 2 : N) : K;
-  if (KIND != kWeightsGrad)
-    number_blocks(a.rows, starts, totals, [](int64_t rows) { return (rows + kTile - 1) / kTile; });
-  const Items<KIND> items{a, starts, (N + kTile - 1) / kTile, (out_cols + kOutTile - 1) / kOutTile};
+  Items<KIND> items{a, (N + kTile - 1) / kTile, (out_cols + kOutTile - 1) / kOutTile};
   // The items of an XCD (workgroups id % 8) are consecutive, so that the
   // workgroups that share its L2 share rows and columns.
   const int64_t count = items.count(), per_xcd = (count + 7) / 8;
@@ -314,12 +350,12 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
   const uint32_t row_step = (kRowsAcross ? 16 : 64) * row_pitch;
   const uint32_t col_step = (kColsAcross ? 16 : SWIGLU ? 32 : 64) * col_pitch;
 
-  // Where a lane's parts of the instructions' operands are in a stage: of its
+  // Where a lane's parts of the instructions' operands are in a slot: of its
   // first 16 rows and columns.
   const int along = l16 * 128 + (quad ^ l16 >> 1) * 16;
   const int across = (quad * 8 + l16 / 4) * 512 + ((quad & 1) << 2 | l16 / 4) * 32 + l16 % 4 * 8;
   const int row_at = kRowsAcross ? across ^ wr * 32 : along + wr * 2048;
-  const int col_at = kSideBytes + (kColsAcross ? across ^ wc * 128 : along + wc * 8192);
+  const int col_at = kColsAcross ? across ^ wc * 128 : along + wc * 8192;
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   const auto read_across = [&](int at) {
     struct {
@@ -343,96 +379,114 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
       return *reinterpret_cast<const bf16x8 *>(stage + (at0 + col_at ^ ks * 64) + j * 2048);
   };
 
-  // The loads run one stage ahead of the products, through the items' ends.
+  // The loads run ahead of the products, through the items' ends: stage g's
+  // columns and rows are in slots 2 g and 2 g + 1 (mod 5), so that columns go out
+  // two stages ahead and rows one.  (Two slots of both: 100 KB fewer, and a third
+  // of the time goes in waiting for loads.)
+  struct Loads {
+    const uint8_t *base = nullptr;
+    int bytes = 0;  // along: from the base to the last row's end
+    int skip = 0;   // across: bytes before the tile's first column
+    int left = 0;   // of the item's sum, from the next stage on
+    int there = 0;  // bytes of the next stage from the base on
+    uint32_t off = 0;  // of this lane's first load
+  };
+  Loads rows, next_rows, cols;
   const int64_t next = gridDim.x / 8;
   int64_t load_item = from + blockIdx.x / 8;
-  const uint8_t *row_base = nullptr, *col_base = nullptr;
-  int row_bytes = 0, col_bytes = 0;  // along: from the base to the last row's end
-  int row_skip = 0, col_skip = 0;    // across: bytes before the tile's first column
-  int left = 0;                      // of the item's sum, from the next stage on
-  const auto start = [&]() {         // of the item that the loads are at
+  Items<KIND> load_items = items;
+  const auto start = [&]() {  // of the item that the columns are at
     Item it;
-    items.get(load_item, &it, kOutTile);
-    left = it.length;
+    load_items.get(load_item, &it, kOutTile);
+    cols.left = next_rows.left = it.length;
     if (kRowsAcross) {
-      row_skip = it.row0 * 2;
-      row_base = reinterpret_cast<const uint8_t *>(a.grad) +
-                 (it.first + wave * 2) * (int64_t)row_pitch + row_skip;
+      next_rows.skip = it.row0 * 2;
+      next_rows.base = reinterpret_cast<const uint8_t *>(a.grad) +
+                       (it.first + wave * 2) * (int64_t)row_pitch + next_rows.skip;
     } else {
-      row_base = static_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
-                 (it.first + it.row0 + wave * 8) * (int64_t)row_pitch;
-      row_bytes = (it.rows - wave * 8) * row_pitch;
+      next_rows.base = static_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
+                       (it.first + it.row0 + wave * 8) * (int64_t)row_pitch;
+      next_rows.bytes = (it.rows - wave * 8) * row_pitch;
     }
     if (kColsAcross) {
-      col_skip = it.col0 * 2;
-      col_base = (KIND == kRowsGrad
-                      ? reinterpret_cast<const uint8_t *>(a.w) +
-                            ((int64_t)it.e * N + wave * 2) * col_pitch
-                      : static_cast<const uint8_t *>(a.x) +
-                            (it.first + wave * 2) * (int64_t)col_pitch) +
-                 col_skip;
+      cols.skip = it.col0 * 2;
+      cols.base = (KIND == kRowsGrad
+                       ? reinterpret_cast<const uint8_t *>(a.w) +
+                             ((int64_t)it.e * N + wave * 2) * col_pitch
+                       : static_cast<const uint8_t *>(a.x) +
+                             (it.first + wave * 2) * (int64_t)col_pitch) +
+                  cols.skip;
     } else {
       // SwiGLU: 32 columns of the gate, then the same of up, for each wc
       const int n = it.col0 + (SWIGLU ? wave % 4 * 8 : wave * 8);
       const int there = out_cols - n < kTile ? out_cols - n : kTile;
-      col_base = reinterpret_cast<const uint8_t *>(a.w) +
-                 ((int64_t)it.e * N + n + (SWIGLU ? wave / 4 * out_cols : 0)) * col_pitch;
-      col_bytes = there * col_pitch;
+      cols.base = reinterpret_cast<const uint8_t *>(a.w) +
+                  ((int64_t)it.e * N + n + (SWIGLU ? wave / 4 * out_cols : 0)) * col_pitch;
+      cols.bytes = there * col_pitch;
     }
   };
-  // A stage's loads go out one at a time between products: together they would
-  // hold up every wave until the last was taken.
-  int row_there = 0, col_there = 0;  // bytes from the bases on
-  uint32_t row_from = 0, col_from = 0, load_lds = 0;
-  const auto begin_stage = [&](uint32_t stage_number) {
-    load_lds = lds0 + (stage_number & 1) * kStageBytes + wave * 1024;
-    const bool in = piece_along * 8 < left;
-    const int l2 = left - wave * 2 < kDepth ? left - wave * 2 : kDepth;
-    const int rb = left <= 0 ? 0 : kRowsAcross ? l2 * row_pitch - row_skip : row_bytes;
-    const int cb = left <= 0 ? 0 : kColsAcross ? l2 * col_pitch - col_skip : col_bytes;
-    row_there = uniform(rb < 0 ? 0 : rb);
-    col_there = uniform(cb < 0 ? 0 : cb);
-    row_from = kRowsAcross || in ? row_off : kNowhere;
-    col_from = kColsAcross || in ? col_off : kNowhere;
+  // Loads go out one at a time between products: together they would hold up
+  // every wave until the last was taken.
+  const auto load = [&](const Loads &x, int slot, uint32_t step, int i) {
+    load_to_lds(lds0 + slot * kSideBytes + wave * 1024 + i * 8192, x.off + i * step,
+                buffer_of(x.base, x.there));
   };
-  const auto load_part = [&](int i) {  // 0 .. 2 kLoads - 1
-    if (i < kLoads)
-      load_to_lds(load_lds + kSideBytes + i * 8192, col_from + i * col_step,
-                  buffer_of(col_base, col_there));
-    else
-      load_to_lds(load_lds + (i - kLoads) * 8192, row_from + (i - kLoads) * row_step,
-                  buffer_of(row_base, row_there));
+  const auto see = [&](Loads *x, bool is_across, int pitch, uint32_t off) {
+    const int l2 = x->left - wave * 2 < kDepth ? x->left - wave * 2 : kDepth;
+    const int n = x->left <= 0 ? 0 : is_across ? l2 * pitch - x->skip : x->bytes;
+    x->there = uniform(n < 0 ? 0 : n);
+    x->off = is_across || piece_along * 8 < x->left ? off : kNowhere;
   };
-  const auto end_stage = [&]() {
-    row_base += kRowsAcross ? (int64_t)kDepth * row_pitch : kDepth * 2;
-    col_base += kColsAcross ? (int64_t)kDepth * col_pitch : kDepth * 2;
-    row_bytes -= kDepth * 2;
-    col_bytes -= kDepth * 2;
-    left -= kDepth;
-    while (left <= 0 && load_item < to) {
+  const auto load_rows = [&](int slot, int i) {
+    load(rows, slot, row_step, i);
+  };
+  const auto load_cols = [&](int slot, int i) {
+    load(cols, slot, col_step, i);
+  };
+  const auto on = [&](Loads *x, bool is_across, int pitch) {
+    x->base += is_across ? (int64_t)kDepth * pitch : kDepth * 2;
+    x->bytes -= kDepth * 2;
+    x->left -= kDepth;
+  };
+  const auto cols_on = [&]() {
+    on(&cols, kColsAcross, col_pitch);
+    while (cols.left <= 0 && load_item < to) {
       load_item += next;
       if (load_item < to) start();
     }
+    see(&cols, kColsAcross, col_pitch, col_off);
+  };
+  const auto rows_on = [&]() {  // after cols_on() of the same stage
+    on(&rows, kRowsAcross, row_pitch);
+    if (rows.left <= 0) rows = next_rows;
+    see(&rows, kRowsAcross, row_pitch, row_off);
   };
 
   if (load_item < to) start();
-  left += kDepth;  // end_stage() finds the first item that has a sum
-  row_base -= kRowsAcross ? (int64_t)kDepth * row_pitch : kDepth * 2;
-  col_base -= kColsAcross ? (int64_t)kDepth * col_pitch : kDepth * 2;
-  row_bytes += kDepth * 2;
-  col_bytes += kDepth * 2;
-  end_stage();
-  uint32_t g = 0;  // stages used up
-  begin_stage(0);
+  while (cols.left <= 0 && load_item < to) {  // to the first item that has a sum
+    load_item += next;
+    if (load_item < to) start();
+  }
+  rows = next_rows;
+  see(&cols, kColsAcross, col_pitch, col_off);
+  see(&rows, kRowsAcross, row_pitch, row_off);
 #pragma unroll
-  for (int i = 0; i < 2 * kLoads; ++i) load_part(i);
-  end_stage();
-  stage_barrier();
-  begin_stage(1);
+  for (int i = 0; i < kLoads; ++i) load_cols(0, i);
+  cols_on();
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) load_part(i);
-  // Here and at the end of each item: stage g is there, the first half of the
-  // loads of g + 1 are out.
+  for (int i = 0; i < kLoads; ++i) load_rows(1, i);
+  rows_on();
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) load_cols(2, i);
+  cols_on();
+  stage_barrier<kLoads>();
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) load_rows(3, i);
+  rows_on();
+  int slot = 0;    // of the next stage's columns
+  int stored = 0;  // stores behind the newest loads
+  // Here and at the end of each item: the next stage is there, and the columns
+  // and rows of the one after it are on their way.
   for (int64_t item = from + blockIdx.x / 8; item < to; item += next) {
     Item it;
     items.get(item, &it, kOutTile);
@@ -446,64 +500,63 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
       bf16x8 c[2][4], r[2][kM];
-      const auto read_cols = [&](int at0, int ks) {
+      const auto read_cols = [&](int slot, int ks) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[ks][j] = read_col(at0, ks, j);
+        for (int j = 0; j < 4; ++j) c[ks][j] = read_col(slot * kSideBytes, ks, j);
       };
-      const auto read_rows = [&](int at0, int ks, int h) {
+      const auto read_rows = [&](int slot, int ks, int h) {
 #pragma unroll
-        for (int f = 0; f < kM; ++f) r[h][f] = read_row(at0, ks, h * kM + f);
+        for (int f = 0; f < kM; ++f) r[h][f] = read_row(slot * kSideBytes, ks, h * kM + f);
       };
-      const auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
-      // part: the first of the loads that go out with these products, or none
-      const auto products = [&](int ks, int h, int part) {
+      const auto products = [&](int ks, int h, auto between) {
 #pragma unroll
         for (int f = 0; f < kM; ++f) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[h * kM + f][j] = mul(c[ks][j], r[h][f], acc[h * kM + f][j]);
-          if (part >= 0) {
-            pin();
 #pragma unroll
-            for (int i = f * kLoads / kM; i < (f + 1) * kLoads / kM; ++i) load_part(part + i);
-            pin();
-          }
+          for (int i = f * kLoads / kM; i < (f + 1) * kLoads / kM; ++i) between(i);
         }
       };
+      const auto nothing = [](int) {};
       if (steps > 0) {
-        read_cols((g & 1) * kStageBytes, 0);
-        read_rows((g & 1) * kStageBytes, 0, 0);
+        read_cols(slot, 0);
+        read_rows(slot == 4 ? 0 : slot + 1, 0, 0);
       }
       // Each quarter's operands are read during the one before.
-      for (int s = 0; s < steps; ++s, ++g) {
-        const int at0 = (g & 1) * kStageBytes;
-        read_rows(at0, 0, 1);
-        pin();
-        products(0, 0, kLoads);
-        pin();
-        read_cols(at0, 1);
-        read_rows(at0, 1, 0);
-        pin();
-        end_stage();
-        products(0, 1, -1);
-        pin();
-        read_rows(at0, 1, 1);
-        pin();
-        products(1, 0, -1);
-        pin();
-        stage_barrier();  // the next stage is there, and this one's buffer free
-        read_cols(at0 ^ kStageBytes, 0);
-        read_rows(at0 ^ kStageBytes, 0, 0);
-        begin_stage(g + 2);
-        pin();
-        products(1, 1, 0);
-        pin();
+      for (int s = 0; s < steps; ++s) {
+        const int row_slot = slot == 4 ? 0 : slot + 1;
+        const int next_slot = slot >= 3 ? slot - 3 : slot + 2;
+        const int last_slot = slot == 0 ? 4 : slot - 1;  // of the stage before, its rows
+        read_rows(row_slot, 0, 1);
+        products(0, 0, [&](int i) {
+          if (i < kLoads / 2) load_cols(last_slot, i);
+        });
+        read_cols(slot, 1);
+        read_rows(row_slot, 1, 0);
+        products(0, 1, [&](int i) {
+          if (i < kLoads / 2) load_cols(last_slot, i + kLoads / 2);
+        });
+        cols_on();
+        read_rows(row_slot, 1, 1);
+        products(1, 0, nothing);
+        // the next stage is there, and this one's slots are free
+        if (s == 0 && stored == kStores * 4)
+          stage_barrier<kLoads + kStores * 4>();
+        else
+          stage_barrier<kLoads>();
+        read_cols(next_slot, 0);
+        read_rows(next_slot == 4 ? 0 : next_slot + 1, 0, 0);
+        products(1, 1, [&](int i) { load_rows(slot, i); });
+        rows_on();
+        slot = next_slot;
       }
       // A lane has row l16 and columns 4 quad .. + 3 of each 16.  The values
       // change places between lanes so that a store writes whole lines (with 64
       // bytes per row the weights' gradient of 32 experts, 4096 x 7168, takes 2232
       // us instead of 2040; through LDS 2056).  Rows that are not there are outside
       // the buffer of the stores.
-      constexpr int kSize = sizeof(OUT), kHere = SWIGLU ? 2 : 4;  // 16 columns each
+      constexpr int kHere = SWIGLU ? 2 : 4;  // 16 columns each
+      stored = steps > 0 ? kStores * kM : 0;
       const int64_t to_row =
           KIND == kWeightsGrad ? (int64_t)it.e * N + it.row0 : it.first + it.row0;
       const int pitch = out_cols * kSize;
@@ -594,7 +647,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
       default: tile(std::integral_constant<int, 4>{}); break;
     }
   }
-  stage_barrier();  // no load may write to LDS after the end
+  stage_barrier<0>();  // no load may write to LDS after the end
 }
 
 #define EP_TRY(expr)                \
