@@ -35,7 +35,7 @@ __device__ __forceinline__ f32x4 mul(bf16x8 x, bf16x8 w, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
-// A value of an FP8 row as it enters the products.
+// A value of an FP8 row as bf16, rounded (exact where the scale is 1).
 __device__ __forceinline__ uint16_t fp8_bf16(uint8_t code, float scale) {
   return f32_to_bf16(__builtin_amdgcn_cvt_f32_fp8((int)code, 0) * scale);
 }
@@ -87,8 +87,7 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
       if (l >= length) return 0;
       if (KIND == kProduct) {
         if (m >= rows) return 0;
-        if (FP8)
-          return fp8_bf16(x8[(first + m) * K + l], a.x_scales[(first + m) * (K / 128) + l / 128]);
+        if (FP8) return fp8_bf16(x8[(first + m) * K + l], 1.0f);
         return x16[(first + m) * K + l];
       }
       if (KIND == kRowsGrad) return m < rows ? a.grad[(first + m) * N + l] : (uint16_t)0;
@@ -107,9 +106,10 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
         return fp8_bf16(x8[(first + l) * K + c], a.x_scales[(first + l) * (K / 128) + c / 128]);
       return x16[(first + l) * K + c];
     };
-    f32x4 acc[4];
+    // the product's FP8 rows: acc sums 128 of l, part their products with the scale
+    f32x4 acc[4], part[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = f32x4{0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i) acc[i] = part[i] = f32x4{0, 0, 0, 0};
     for (int64_t l0 = 0; l0 < length; l0 += kAnyDepth) {
       for (int i = tid; i < kAnyTile * kAnyDepth; i += 256) {
         // neighbouring threads read neighbouring values
@@ -129,7 +129,24 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         acc[i] = mul(av, *reinterpret_cast<const bf16x8 *>(&bs[i * 16 + col][quad * 8]), acc[i]);
+      if (KIND == kProduct && FP8 && l0 % 128 == 128 - kAnyDepth) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int m = wave * 16 + quad * 4 + v;
+          const float scale =
+              m < rows ? a.x_scales[(first + m) * (K / 128) + l0 / 128] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            part[i][v] = __builtin_fmaf(scale, acc[i][v], part[i][v]);
+            acc[i][v] = 0.0f;
+          }
+        }
+      }
       __syncthreads();
+    }
+    if (KIND == kProduct && FP8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = part[i];
     }
     constexpr int kOut = SWIGLU ? 2 : 4;
 #pragma unroll
@@ -163,15 +180,14 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 // columns first, so that a lane's results are consecutive columns of one row.
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 256;            // rows and columns of a tile
 constexpr int kDepth = 64;            // of the sum, per stage
-constexpr int kSideBytes = kTile * kDepth * 2;
-constexpr int kSlots = 5;             // of a side in LDS: all of it
+constexpr int kColSlots = 3, kRowSlots = 2;  // stages in LDS: 160 KB, all of it, in bf16
 constexpr int kTileWaves = 8;
 constexpr int kTileWorkgroups = 256;  // one per compute unit, by its LDS
 constexpr int kBand = 8;              // row tiles that go through the columns together
-constexpr int kLoads = kDepth / 16;   // of a wave, side and stage
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -187,15 +203,50 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4
       : "memory");
 }
 
+// 4 bytes per lane, at lds + 4 * lane.
+__device__ __forceinline__ void load_word_to_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+      :
+      : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
+}
+
+// Eight FP8 codes as bf16, which holds every E4M3 number.
+__device__ __forceinline__ bf16x8 codes_bf16(u32x2 codes) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[2 * i] = __builtin_bit_cast(
+        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], 1.0f, false));
+    w[2 * i + 1] = __builtin_bit_cast(
+        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], 1.0f, true));
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+// Eight FP8 codes times their scales, rounded to bf16.
+__device__ __forceinline__ bf16x8 scaled_bf16(u32x2 codes, const f32x4 *scales) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[i], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[i], true);
+    w[2 * i] = pack_bf16(lo[0] * scales[i][0], lo[1] * scales[i][1]);
+    w[2 * i + 1] = pack_bf16(hi[0] * scales[i][2], hi[1] * scales[i][3]);
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+
 // All but the newest kLeft loads and stores are done, and this wave's LDS
 // reads, and so for every wave of the workgroup.
 template <int kLeft>
 __device__ __forceinline__ void stage_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(kLeft) : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
 }
 
 // Two 16 bytes of a row per lane, rows by lane % 16, become those of rows
@@ -228,16 +279,11 @@ struct Item {
   int length;      // of the sum
 };
 
-// Row tiles of an expert.
-__device__ __forceinline__ int row_tiles_of(int64_t rows) {
-  return (int)((rows + kTile - 1) / kTile);
-}
-
 // The numbering of items: an expert's tiles are consecutive, in bands of kBand
 // row tiles that take the columns one after the other.  A wave finds its items
 // in ascending order by itself: it holds the row tiles of 64 experts, one per
 // lane, and goes on to the next 64 when it is past them.
-template <Kind KIND>
+template <Kind KIND, int kRowTile>
 struct Items {
   const ProductArgs &a;
   int row_tiles, col_tiles;  // of the weights' gradient; of all kinds
@@ -250,7 +296,7 @@ struct Items {
     int64_t first, rows = 0;
     if (e < a.rows.E)
       rows_inside(a.rows.offsets[e], a.rows.counts[e], a.rows.capacity, &first, &rows);
-    return row_tiles_of(rows);
+    return (int)((rows + kRowTile - 1) / kRowTile);
   }
   __device__ __forceinline__ int64_t count() const {
     if (KIND == kWeightsGrad) return (int64_t)a.rows.E * row_tiles * col_tiles;
@@ -297,10 +343,10 @@ struct Items {
     high = high - band * kBand < kBand ? high - band * kBand : kBand;
     const int rt = uniform(band * kBand + in_band % high), ct = uniform(in_band / high);
     it->e = e;
-    it->row0 = rt * kTile;
+    it->row0 = rt * kRowTile;
     it->col0 = ct * out_cols_per_tile;
     const int64_t all = KIND == kWeightsGrad ? (int64_t)a.N : rows;
-    it->rows = (int)(all - it->row0 < kTile ? all - it->row0 : kTile);
+    it->rows = (int)(all - it->row0 < kRowTile ? all - it->row0 : kRowTile);
     it->length = KIND == kProduct ? a.K : KIND == kRowsGrad ? a.N : (int)rows;
   }
 };
@@ -315,22 +361,37 @@ struct Items {
 // results alone.
 __device__ __forceinline__ int across_swizzle(int l) { return (l & 3) | (l >> 3 & 1) << 2; }
 
-template <Kind KIND, bool SWIGLU, typename OUT>
+template <Kind KIND, bool FP8, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(ProductArgs a) {
   constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
+  // Which side is x in FP8.  Rows: codes enter the instructions exactly and the
+  // scales are applied to the sums of 128, in accumulators of their own, for which
+  // 128 rows leave the registers.  Columns (weights' gradient): x is rounded to
+  // bf16, as the scales go by the rows that are summed over.
+  constexpr bool kRows8 = KIND == kProduct && FP8, kCols8 = KIND == kWeightsGrad && FP8;
+  constexpr int kRowTile = kRows8 ? kTile / 2 : kTile;
   constexpr int kOutTile = SWIGLU ? kTile / 2 : kTile;
-  __shared__ __align__(1024) uint8_t stage[kSlots * kSideBytes];
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  constexpr int kRowElem = kRows8 ? 1 : 2, kColElem = kCols8 ? 1 : 2;
+  constexpr int kRowBytes = kRowTile * kDepth * kRowElem, kColBytes = kTile * kDepth * kColElem;
+  constexpr int kRowLoads = kRowBytes / (kTileWaves * 1024);  // of a wave and stage
+  constexpr int kColLoads = kColBytes / (kTileWaves * 1024);
+  constexpr int kColPart = kColLoads + kCols8;  // with the scales
+  constexpr int kRowsAt = kColSlots * kColBytes, kScalesAt = kRowsAt + kRowSlots * kRowBytes;
+  constexpr int kScaleBytes = 512;  // of a stage: 128 rows, or 64 of l for two blocks
+  __shared__ __align__(1024) uint8_t
+      stage[kScalesAt + (FP8 ? (kColSlots + 1) * kScaleBytes : 0)];
   // non-temporal stores of the weights' gradient, which nobody reads soon (bf16, 32
   // experts of 4096 x 7168: 2056 us, without 2140)
   constexpr int kOnceOut = KIND == kWeightsGrad ? 2 : 0;
   constexpr int kSize = sizeof(OUT);
   constexpr int kStores = SWIGLU ? 2 : kSize * 2;  // of a wave, per 64 rows of a tile
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   const int wr = wave >> 2, wc = wave & 3;  // of the wave's rows and columns
   const int K = a.K, N = a.N;
   const int out_cols = KIND == kProduct ? (SWIGLU ? N / 2 : N) : K;
-  Items<KIND> items{a, (N + kTile - 1) / kTile, (out_cols + kOutTile - 1) / kOutTile};
+  typedef Items<KIND, kRowTile> AllItems;
+  AllItems items{a, (N + kTile - 1) / kTile, (out_cols + kOutTile - 1) / kOutTile};
   // The items of an XCD (workgroups id % 8) are consecutive, so that the
   // workgroups that share its L2 share rows and columns.
   const int64_t count = items.count(), per_xcd = (count + 7) / 8;
@@ -340,23 +401,34 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
 
   // Where a lane's 16 bytes of a side's first load come from, from the wave's
   // base on, and how far on each further load is.
-  const int row_pitch = (KIND == kProduct ? K : N) * 2, col_pitch = K * 2;
+  const int row_pitch = (KIND == kProduct ? K : N) * kRowElem, col_pitch = K * kColElem;
   const int piece_along = (lane & 7) ^ ((wave & 1) << 2 | lane >> 4);
   const int piece_across = (lane & 31) ^ across_swizzle(wave * 2 + (lane >> 5)) << 1;
-  const uint32_t row_off = kRowsAcross ? (lane >> 5) * row_pitch + piece_across * 16
-                                       : (lane >> 3) * row_pitch + piece_along * 16;
-  const uint32_t col_off = kColsAcross ? (lane >> 5) * col_pitch + piece_across * 16
-                                       : (lane >> 3) * col_pitch + piece_along * 16;
+  const int piece_along8 = (lane & 3) ^ lane >> 4;
+  const int piece_across8 = l16 ^ ((wave & 3) << 2 | quad);
+  const uint32_t row_off = kRows8        ? (lane >> 2) * row_pitch + piece_along8 * 16
+                           : kRowsAcross ? (lane >> 5) * row_pitch + piece_across * 16
+                                         : (lane >> 3) * row_pitch + piece_along * 16;
+  const uint32_t col_off = kCols8        ? quad * col_pitch + piece_across8 * 16
+                           : kColsAcross ? (lane >> 5) * col_pitch + piece_across * 16
+                                         : (lane >> 3) * col_pitch + piece_along * 16;
   const uint32_t row_step = (kRowsAcross ? 16 : 64) * row_pitch;
-  const uint32_t col_step = (kColsAcross ? 16 : SWIGLU ? 32 : 64) * col_pitch;
+  const uint32_t col_step = (kCols8 ? 32 : kColsAcross ? 16 : SWIGLU ? 32 : 64) * col_pitch;
+  constexpr int kRowPer = kRows8 ? 16 : kRowsAcross ? 2 : 8;  // rows, or l, of a load
+  constexpr int kColPer = kCols8 ? 4 : kColsAcross ? 2 : 8;
 
   // Where a lane's parts of the instructions' operands are in a slot: of its
   // first 16 rows and columns.
   const int along = l16 * 128 + (quad ^ l16 >> 1) * 16;
   const int across = (quad * 8 + l16 / 4) * 512 + ((quad & 1) << 2 | l16 / 4) * 32 + l16 % 4 * 8;
-  const int row_at = kRowsAcross ? across ^ wr * 32 : along + wr * 2048;
-  const int col_at = kColsAcross ? across ^ wc * 128 : along + wc * 8192;
+  const int along8 = l16 * 64 + (quad >> 1 ^ l16 >> 2) * 16 + (quad & 1) * 8;
+  const int across8 = (quad * 8 + l16 / 2) * 256 + ((quad & 1) << 3 | l16 / 2) * 16 + l16 % 2 * 8;
+  const int row_at = kRowsAt + (kRows8        ? along8 + wr * 1024
+                                : kRowsAcross ? across ^ wr * 32
+                                              : along + wr * 2048);
+  const int col_at = kCols8 ? across8 ^ wc * 64 : kColsAcross ? across ^ wc * 128 : along + wc * 8192;
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
   const auto read_across = [&](int at) {
     struct {
       s16x4 lo, hi;
@@ -366,35 +438,42 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
     return __builtin_bit_cast(bf16x8, v);
   };
   // rows 32 f + 16 wr .. + 15, columns 64 wc + 16 j .. + 15, half ks of a stage
-  const auto read_row = [&](int at0, int ks, int f) {
-    if constexpr (kRowsAcross)
-      return read_across((at0 + row_at ^ f * 64) + ks * 32 * 512);
+  const auto read_row = [&](int slot, int ks, int f) {
+    const int at = slot * kRowBytes + row_at;
+    if constexpr (kRows8)
+      return *reinterpret_cast<const u32x2 *>(stage + (at ^ ks * 32) + f * 2048);
+    else if constexpr (kRowsAcross)
+      return read_across((at ^ f * 64) + ks * 32 * 512);
     else
-      return *reinterpret_cast<const bf16x8 *>(stage + (at0 + row_at ^ ks * 64) + f * 4096);
+      return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 64) + f * 4096);
   };
-  const auto read_col = [&](int at0, int ks, int j) {
-    if constexpr (kColsAcross)
-      return read_across((at0 + col_at ^ j * 32) + ks * 32 * 512);
+  const auto read_col = [&](int slot, int ks, int j) {
+    const int at = slot * kColBytes + col_at;
+    if constexpr (kCols8)
+      return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                                           (lds_i32x2 *)(stage + (at ^ j * 16) + ks * 32 * 256)));
+    else if constexpr (kColsAcross)
+      return read_across((at ^ j * 32) + ks * 32 * 512);
     else
-      return *reinterpret_cast<const bf16x8 *>(stage + (at0 + col_at ^ ks * 64) + j * 2048);
+      return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 64) + j * 2048);
   };
 
-  // The loads run ahead of the products, through the items' ends: stage g's
-  // columns and rows are in slots 2 g and 2 g + 1 (mod 5), so that columns go out
-  // two stages ahead and rows one.  (Two slots of both: 100 KB fewer, and a third
-  // of the time goes in waiting for loads.)
+  // The loads run ahead of the products, through the items' ends: columns two
+  // stages ahead, in three slots, and rows one, in two.  (With two slots of both
+  // the decode share in bf16 takes 364 us, so 311.)
   struct Loads {
-    const uint8_t *base = nullptr;
+    const uint8_t *base = nullptr, *scales = nullptr;
     int bytes = 0;  // along: from the base to the last row's end
     int skip = 0;   // across: bytes before the tile's first column
-    int left = 0;   // of the item's sum, from the next stage on
-    int there = 0;  // bytes of the next stage from the base on
+    int scale_bytes = 0, scale_skip = 0;  // the same of the scales
+    int left = 0;      // of the item's sum, from the next stage on
+    int there = 0;     // bytes of the next stage from the base on
     uint32_t off = 0;  // of this lane's first load
   };
   Loads rows, next_rows, cols;
   const int64_t next = gridDim.x / 8;
   int64_t load_item = from + blockIdx.x / 8;
-  Items<KIND> load_items = items;
+  AllItems load_items = items;
   const auto start = [&]() {  // of the item that the columns are at
     Item it;
     load_items.get(load_item, &it, kOutTile);
@@ -402,19 +481,24 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
     if (kRowsAcross) {
       next_rows.skip = it.row0 * 2;
       next_rows.base = reinterpret_cast<const uint8_t *>(a.grad) +
-                       (it.first + wave * 2) * (int64_t)row_pitch + next_rows.skip;
+                       (it.first + wave * kRowPer) * (int64_t)row_pitch + next_rows.skip;
     } else {
       next_rows.base = static_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
-                       (it.first + it.row0 + wave * 8) * (int64_t)row_pitch;
-      next_rows.bytes = (it.rows - wave * 8) * row_pitch;
+                       (it.first + it.row0 + wave * kRowPer) * (int64_t)row_pitch;
+      next_rows.bytes = (it.rows - wave * kRowPer) * row_pitch;
+    }
+    if (kRows8) {
+      next_rows.scales = reinterpret_cast<const uint8_t *>(a.x_scales) +
+                         (it.first + it.row0) * (int64_t)(K / 128) * 4;
+      next_rows.scale_bytes = it.rows * (K / 128) * 4;
     }
     if (kColsAcross) {
-      cols.skip = it.col0 * 2;
+      cols.skip = it.col0 * kColElem;
       cols.base = (KIND == kRowsGrad
                        ? reinterpret_cast<const uint8_t *>(a.w) +
-                             ((int64_t)it.e * N + wave * 2) * col_pitch
+                             ((int64_t)it.e * N + wave * kColPer) * col_pitch
                        : static_cast<const uint8_t *>(a.x) +
-                             (it.first + wave * 2) * (int64_t)col_pitch) +
+                             (it.first + wave * kColPer) * (int64_t)col_pitch) +
                   cols.skip;
     } else {
       // SwiGLU: 32 columns of the gate, then the same of up, for each wc
@@ -424,42 +508,75 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
                   ((int64_t)it.e * N + n + (SWIGLU ? wave / 4 * out_cols : 0)) * col_pitch;
       cols.bytes = there * col_pitch;
     }
+    if (kCols8) {
+      cols.scale_skip = (it.col0 / 128 + (wave & 1)) * 4;
+      cols.scales = reinterpret_cast<const uint8_t *>(a.x_scales) +
+                    it.first * (int64_t)(K / 128) * 4 + cols.scale_skip;
+    }
   };
   // Loads go out one at a time between products: together they would hold up
   // every wave until the last was taken.
-  const auto load = [&](const Loads &x, int slot, uint32_t step, int i) {
-    load_to_lds(lds0 + slot * kSideBytes + wave * 1024 + i * 8192, x.off + i * step,
-                buffer_of(x.base, x.there));
+  const auto load = [&](const Loads &x, int at, uint32_t step, int i) {
+    load_to_lds(lds0 + at + wave * 1024 + i * 8192, x.off + i * step, buffer_of(x.base, x.there));
   };
-  const auto see = [&](Loads *x, bool is_across, int pitch, uint32_t off) {
-    const int l2 = x->left - wave * 2 < kDepth ? x->left - wave * 2 : kDepth;
+  const auto see = [&](Loads *x, bool is_across, int pitch, uint32_t off, int per) {
+    const int l2 = x->left - wave * per < kDepth ? x->left - wave * per : kDepth;
     const int n = x->left <= 0 ? 0 : is_across ? l2 * pitch - x->skip : x->bytes;
     x->there = uniform(n < 0 ? 0 : n);
-    x->off = is_across || piece_along * 8 < x->left ? off : kNowhere;
+    // FP8 rows end with whole stages
+    x->off = is_across || kRows8 || piece_along * 8 < x->left ? off : kNowhere;
+  };
+  const auto see_cols = [&]() {
+    // a sum's end in the columns: rows of 128 in FP8 have none within a stage
+    see(&cols, kColsAcross, col_pitch, col_off, kColPer);
+  };
+  const auto see_rows = [&]() { see(&rows, kRowsAcross, row_pitch, row_off, kRowPer); };
+  // The scales of a stage, by the first two waves; the others' loads bring
+  // zeros to a place that nobody reads, so that all waves count alike.
+  const auto load_row_scales = [&](int slot) {
+    if constexpr (kRows8) {
+      const uint32_t at = kScalesAt + (wave < 2 ? slot * kScaleBytes + wave * 256
+                                                : kColSlots * kScaleBytes);
+      const uint32_t off = (wave * 64 + lane) * (uint32_t)(K / 128) * 4 + (K - rows.left) / 128 * 4;
+      load_word_to_lds(lds0 + at, off,
+                       buffer_of(rows.scales, wave < 2 && rows.left > 0 ? rows.scale_bytes : 0));
+    }
+  };
+  const auto load_col_scales = [&](int slot) {
+    if constexpr (kCols8) {
+      const uint32_t at = kScalesAt + (wave < 2 ? slot * kScaleBytes + wave * 256
+                                                : kColSlots * kScaleBytes);
+      const int there = (cols.left < kDepth ? cols.left : kDepth) * (K / 128) * 4 - cols.scale_skip;
+      load_word_to_lds(lds0 + at, lane * (uint32_t)(K / 128) * 4,
+                       buffer_of(cols.scales, wave < 2 && there > 0 ? there : 0));
+    }
   };
   const auto load_rows = [&](int slot, int i) {
-    load(rows, slot, row_step, i);
+    load(rows, kRowsAt + slot * kRowBytes, row_step, i);
+    if (i == kRowLoads - 1) load_row_scales(slot);
   };
   const auto load_cols = [&](int slot, int i) {
-    load(cols, slot, col_step, i);
+    load(cols, slot * kColBytes, col_step, i);
+    if (i == kColLoads - 1) load_col_scales(slot);
   };
-  const auto on = [&](Loads *x, bool is_across, int pitch) {
-    x->base += is_across ? (int64_t)kDepth * pitch : kDepth * 2;
-    x->bytes -= kDepth * 2;
+  const auto on = [&](Loads *x, bool is_across, int pitch, int elem) {
+    x->base += is_across ? (int64_t)kDepth * pitch : kDepth * elem;
+    x->bytes -= kDepth * elem;
     x->left -= kDepth;
   };
   const auto cols_on = [&]() {
-    on(&cols, kColsAcross, col_pitch);
+    on(&cols, kColsAcross, col_pitch, kColElem);
+    if (kCols8) cols.scales += (int64_t)kDepth * (K / 128) * 4;
     while (cols.left <= 0 && load_item < to) {
       load_item += next;
       if (load_item < to) start();
     }
-    see(&cols, kColsAcross, col_pitch, col_off);
+    see_cols();
   };
   const auto rows_on = [&]() {  // after cols_on() of the same stage
-    on(&rows, kRowsAcross, row_pitch);
+    on(&rows, kRowsAcross, row_pitch, kRowElem);
     if (rows.left <= 0) rows = next_rows;
-    see(&rows, kRowsAcross, row_pitch, row_off);
+    see_rows();
   };
 
   if (load_item < to) start();
@@ -468,23 +585,23 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
     if (load_item < to) start();
   }
   rows = next_rows;
-  see(&cols, kColsAcross, col_pitch, col_off);
-  see(&rows, kRowsAcross, row_pitch, row_off);
+  see_cols();
+  see_rows();
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) load_cols(0, i);
+  for (int i = 0; i < kColLoads; ++i) load_cols(0, i);
   cols_on();
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) load_rows(1, i);
+  for (int i = 0; i < kRowLoads; ++i) load_rows(0, i);
   rows_on();
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) load_cols(2, i);
+  for (int i = 0; i < kColLoads; ++i) load_cols(1, i);
   cols_on();
-  stage_barrier<kLoads>();
+  stage_barrier<kColPart>();
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) load_rows(3, i);
+  for (int i = 0; i < kRowLoads; ++i) load_rows(1, i);
   rows_on();
-  int slot = 0;    // of the next stage's columns
-  int stored = 0;  // stores behind the newest loads
+  int col_slot = 0, row_slot = 0;  // of the next stage
+  int stored = 0;                  // stores behind the newest loads
   // Here and at the end of each item: the next stage is there, and the columns
   // and rows of the one after it are on their way.
   for (int64_t item = from + blockIdx.x / 8; item < to; item += next) {
@@ -494,61 +611,127 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
 
     const auto tile = [&](auto count) {
       constexpr int kM = decltype(count)::value;  // 64 rows each
-      f32x4 acc[2 * kM][4];
+      f32x4 acc[2 * kM][4], part[kRows8 ? 2 * kM : 1][4];
 #pragma unroll
       for (int f = 0; f < 2 * kM; ++f)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
-      bf16x8 c[2][4], r[2][kM];
+      typedef typename std::conditional<kRows8, u32x2, bf16x8>::type RowRaw;
+      typedef typename std::conditional<kCols8, u32x2, bf16x8>::type ColRaw;
+      bf16x8 c[4];
+      ColRaw c_raw[2][4];
+      RowRaw r[2][kM];
+      f32x4 col_scale[2];          // of the lane's 8 l
+      float row_scale[2][kM];
       const auto read_cols = [&](int slot, int ks) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[ks][j] = read_col(slot * kSideBytes, ks, j);
+        for (int j = 0; j < 4; ++j) c_raw[ks][j] = read_col(slot, ks, j);
+        if constexpr (kCols8) {
+          const f32x4 *s = reinterpret_cast<const f32x4 *>(
+              stage + kScalesAt + slot * kScaleBytes + (wc >> 1) * 256 + ks * 128 + quad * 32);
+          col_scale[0] = s[0];
+          col_scale[1] = s[1];
+        }
+      };
+      const auto take_cols = [&](int ks) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (kCols8)
+            c[j] = scaled_bf16(c_raw[ks][j], col_scale);
+          else
+            c[j] = c_raw[ks][j];
+        }
       };
       const auto read_rows = [&](int slot, int ks, int h) {
 #pragma unroll
-        for (int f = 0; f < kM; ++f) r[h][f] = read_row(slot * kSideBytes, ks, h * kM + f);
+        for (int f = 0; f < kM; ++f) r[h][f] = read_row(slot, ks, h * kM + f);
       };
-      const auto products = [&](int ks, int h, auto between) {
+      const auto products = [&](bool fresh, int h, auto loads, auto load_one) {
+        constexpr int kCount = decltype(loads)::value;
 #pragma unroll
         for (int f = 0; f < kM; ++f) {
+          bf16x8 x;
+          if constexpr (kRows8)
+            x = codes_bf16(r[h][f]);
+          else
+            x = r[h][f];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[h * kM + f][j] = mul(c[ks][j], r[h][f], acc[h * kM + f][j]);
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (kRows8)
+              part[h * kM + f][j] =
+                  mul(c[j], x, fresh ? f32x4{0, 0, 0, 0} : part[h * kM + f][j]);
+            else
+              acc[h * kM + f][j] = mul(c[j], x, acc[h * kM + f][j]);
+          }
 #pragma unroll
-          for (int i = f * kLoads / kM; i < (f + 1) * kLoads / kM; ++i) between(i);
+          for (int i = f * kCount / kM; i < (f + 1) * kCount / kM; ++i) load_one(i);
         }
       };
+      const auto add_scaled = [&](int h) {
+#pragma unroll
+        for (int f = 0; f < kM; ++f)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              acc[h * kM + f][j][v] = __builtin_fmaf(row_scale[h][f], part[h * kM + f][j][v],
+                                                     acc[h * kM + f][j][v]);
+      };
+      const auto none = std::integral_constant<int, 0>{};
       const auto nothing = [](int) {};
       if (steps > 0) {
-        read_cols(slot, 0);
-        read_rows(slot == 4 ? 0 : slot + 1, 0, 0);
+        read_cols(col_slot, 0);
+        read_rows(row_slot, 0, 0);
       }
-      // Each quarter's operands are read during the one before.
-      for (int s = 0; s < steps; ++s) {
-        const int row_slot = slot == 4 ? 0 : slot + 1;
-        const int next_slot = slot >= 3 ? slot - 3 : slot + 2;
-        const int last_slot = slot == 0 ? 4 : slot - 1;  // of the stage before, its rows
+      // A stage.  Each quarter's operands are read during the one before.
+      // second: of the two that share a scale of FP8 rows.
+      const auto step = [&](int s, auto second) {
+        constexpr bool kSecond = decltype(second)::value, kFresh = !kSecond;
+        constexpr int kEarly = (kColLoads + 1) / 2;
+        const int next_col = col_slot == 2 ? 0 : col_slot + 1;
+        const int free_col = col_slot == 0 ? 2 : col_slot - 1;  // of the stage before
         read_rows(row_slot, 0, 1);
-        products(0, 0, [&](int i) {
-          if (i < kLoads / 2) load_cols(last_slot, i);
-        });
-        read_cols(slot, 1);
+        take_cols(0);
+        products(kFresh, 0, std::integral_constant<int, kEarly>{},
+                 [&](int i) { load_cols(free_col, i); });
+        read_cols(col_slot, 1);
         read_rows(row_slot, 1, 0);
-        products(0, 1, [&](int i) {
-          if (i < kLoads / 2) load_cols(last_slot, i + kLoads / 2);
-        });
+        products(kFresh, 1, std::integral_constant<int, kColLoads - kEarly>{},
+                 [&](int i) { load_cols(free_col, i + kEarly); });
         cols_on();
         read_rows(row_slot, 1, 1);
-        products(1, 0, nothing);
+        if constexpr (kRows8 && kSecond) {
+#pragma unroll
+          for (int f = 0; f < 2 * kM; ++f)
+            row_scale[f / kM][f % kM] = *reinterpret_cast<const float *>(
+                stage + kScalesAt + row_slot * kScaleBytes + (f * 32 + wr * 16 + l16) * 4);
+        }
+        take_cols(1);
+        products(false, 0, none, nothing);
         // the next stage is there, and this one's slots are free
-        if (s == 0 && stored == kStores * 4)
-          stage_barrier<kLoads + kStores * 4>();
+        if (s == 0 && stored == kStores * (kRowTile / 64))
+          stage_barrier<kColPart + kStores * (kRowTile / 64)>();
         else
-          stage_barrier<kLoads>();
-        read_cols(next_slot, 0);
-        read_rows(next_slot == 4 ? 0 : next_slot + 1, 0, 0);
-        products(1, 1, [&](int i) { load_rows(slot, i); });
+          stage_barrier<kColPart>();
+        read_cols(next_col, 0);
+        read_rows(row_slot ^ 1, 0, 0);
+        products(false, 1, std::integral_constant<int, kRowLoads>{},
+                 [&](int i) { load_rows(row_slot, i); });
         rows_on();
-        slot = next_slot;
+        if constexpr (kRows8 && kSecond) {
+          add_scaled(0);
+          add_scaled(1);
+        }
+        col_slot = next_col;
+        row_slot ^= 1;
+      };
+      if constexpr (kRows8) {
+        for (int s = 0; s < steps; s += 2) {  // rows of whole blocks of 128
+          step(s, std::false_type{});
+          step(s + 1, std::true_type{});
+        }
+      } else {
+        for (int s = 0; s < steps; ++s) step(s, std::false_type{});
       }
       // A lane has row l16 and columns 4 quad .. + 3 of each 16.  The values
       // change places between lanes so that a store writes whole lines (with 64
@@ -640,11 +823,18 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
         }
       }
     };
-    switch ((it.rows + 63) / 64) {
-      case 1: tile(std::integral_constant<int, 1>{}); break;
-      case 2: tile(std::integral_constant<int, 2>{}); break;
-      case 3: tile(std::integral_constant<int, 3>{}); break;
-      default: tile(std::integral_constant<int, 4>{}); break;
+    if constexpr (kRows8) {
+      if (it.rows <= 64)
+        tile(std::integral_constant<int, 1>{});
+      else
+        tile(std::integral_constant<int, 2>{});
+    } else {
+      switch ((it.rows + 63) / 64) {
+        case 1: tile(std::integral_constant<int, 1>{}); break;
+        case 2: tile(std::integral_constant<int, 2>{}); break;
+        case 3: tile(std::integral_constant<int, 3>{}); break;
+        default: tile(std::integral_constant<int, 4>{}); break;
+      }
     }
   }
   stage_barrier<0>();  // no load may write to LDS after the end
@@ -743,17 +933,14 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
   a.x_scales = x_scales;
   a.w = w;
   a.out = out;
-  const bool tiled = !fp8 && K % 8 == 0 && (swiglu ? N / 2 : N) % 8 == 0 && aligned_to(out, 16);
+  const bool tiled = K % 8 == 0 && (swiglu ? N / 2 : N) % 8 == 0 && aligned_to(out, 16);
   const auto launch = [&](auto f, auto s) {
-    if constexpr (!f.value) {
-      if (tiled) {
-        hipLaunchKernelGGL((product_tile_kernel<kProduct, s.value, uint16_t>),
-                           dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
-        return;
-      }
-    }
-    hipLaunchKernelGGL((product_any_kernel<kProduct, f.value, s.value, uint16_t>), dim3(kAnyGrid),
-                       dim3(256), 0, stream, a);
+    if (tiled)
+      hipLaunchKernelGGL((product_tile_kernel<kProduct, f.value, s.value, uint16_t>),
+                         dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
+    else
+      hipLaunchKernelGGL((product_any_kernel<kProduct, f.value, s.value, uint16_t>),
+                         dim3(kAnyGrid), dim3(256), 0, stream, a);
   };
   const auto by_swiglu = [&](auto f) {
     if (swiglu)
@@ -789,7 +976,7 @@ ep_status_t ep_expert_product_backward_rows(const ep_experts_t *experts, const u
   a.grad = grad_out;
   a.out = grad_x;
   if (a.K % 8 == 0 && a.N % 8 == 0 && aligned_to(grad_x, 16))
-    hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, uint16_t>), dim3(kTileWorkgroups),
+    hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, false, uint16_t>), dim3(kTileWorkgroups),
                        dim3(kTileWaves * 64), 0, stream, a);
   else
     hipLaunchKernelGGL((product_any_kernel<kRowsGrad, false, false, uint16_t>), dim3(kAnyGrid),
@@ -824,17 +1011,14 @@ ep_status_t ep_expert_product_backward_weights(
   a.grad = grad_out;
   a.add = add;
   a.out = grad_w;
-  const bool tiled = !fp8 && K % 8 == 0 && N % 8 == 0;
+  const bool tiled = K % 8 == 0 && N % 8 == 0;
   const auto launch = [&](auto f, auto value) {
-    if constexpr (!f.value) {
-      if (tiled) {
-        hipLaunchKernelGGL((product_tile_kernel<kWeightsGrad, false, decltype(value)>),
-                           dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
-        return;
-      }
-    }
-    hipLaunchKernelGGL((product_any_kernel<kWeightsGrad, f.value, false, decltype(value)>),
-                       dim3(kAnyGrid), dim3(256), 0, stream, a);
+    if (tiled)
+      hipLaunchKernelGGL((product_tile_kernel<kWeightsGrad, f.value, false, decltype(value)>),
+                         dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
+    else
+      hipLaunchKernelGGL((product_any_kernel<kWeightsGrad, f.value, false, decltype(value)>),
+                         dim3(kAnyGrid), dim3(256), 0, stream, a);
   };
   const auto by_type = [&](auto f) {
     if (f32)

@@ -258,10 +258,9 @@ typedef struct ep_experts {
  *     y[r, n] = sum_c x[r, c] * w_e[n, c]
  * summed in fp32, and out[r, n] = bf16(y[r, n]), or with swiglu
  * bf16(silu(y[r, n]) * y[r, N / 2 + n]), the gate's rows of w before the up
- * projection's.  FP8 rows enter as bf16(code * scale): one rounding, off by at
- * most 2^-8 of a value whose code is itself off by up to 2^-4; a scale that is
- * a power of two loses nothing.  (The gradient for the weights sums over the
- * rows, where the scales cannot be left to the sum; both see the same values.)
+ * projection's.  Codes and rows enter the matrix instructions exactly, the
+ * scales of FP8 rows are applied in fp32 to the sums of 128; the output's is
+ * the only rounding below fp32.
  *
  *   x_dtype       EP_DTYPE_BF16: x bf16 [capacity, K]
  *                 EP_DTYPE_FP8_E4M3: x uint8 [capacity, K] and x_scales fp32
@@ -302,7 +301,10 @@ ep_status_t ep_expert_product_backward_rows(const ep_experts_t *experts, const u
  * summed in fp32 and rounded once to grad_dtype.  An expert without rows gets
  * add, or zeros.
  *
- *   x_dtype, x, x_scales   as in ep_expert_product (FP8 rows rounded as there)
+ *   x_dtype, x, x_scales   as in ep_expert_product.  FP8 rows enter as
+ *              bf16(code * scale), as the scales go by the rows that are summed
+ *              over: one rounding, at most 2^-8 of a value whose code is itself
+ *              off by up to 2^-4; none where the scale is a power of two
  *   grad_out   bf16 [capacity, N]
  *   grad_dtype EP_DTYPE_BF16 or EP_DTYPE_F32: the type of add and grad_w
  *   add        [experts, N, K] or NULL; may be grad_w itself (gradients of
@@ -322,8 +324,8 @@ ep_status_t ep_expert_product_backward_weights(
  *     scale = 2^e, e the smallest integer from -100 on with max |v| <= 448 * 2^e
  *     code  = E4M3(v / scale), rounded to nearest even.
  * A power of two costs E4M3 no precision, and what a code stands for, code *
- * scale, is a bf16 number: products that take the checkpoint as FP8 rows round
- * nothing.  A value that is not finite is kept as NaN and has no part in the
+ * scale, is a bf16 number: a gradient for the weights that takes the checkpoint
+ * as FP8 rows rounds nothing.  A value that is not finite is kept as NaN and has no part in the
  * scale; one within 2^-5 of bf16's largest may come back infinite.
  *
  *   num_experts  1 .. EP_MAX_EXPERTS;  features  F: 1 <= F < 2^20

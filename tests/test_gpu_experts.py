@@ -3,8 +3,9 @@
 Where inputs are small integers (and scales powers of two) every sum is exact
 in fp32, and the result has to be the rounding of the exact one, bit for bit.
 Elsewhere a sum of L terms of fp32 is off by at most L + 8 half steps of the
-sum of magnitudes, the output by a half step of its type.  FP8 rows enter as
-bf16(code * scale), so that is what the reference multiplies.
+sum of magnitudes, the output by a half step of its type.  FP8 rows enter the
+product unrounded (a sum of 128 codes is scaled, one more half step), and the
+weights' gradient as bf16(code * scale): that is what the reference multiplies.
 
 Rows that are no expert's, and weights of experts without rows, are NaN: they
 may enter no result."""
@@ -40,22 +41,23 @@ def draw_rows(rng, cap, K, exact):
         rng.normal(size=(cap, K)))
 
 
-def draw_fp8(rng, cap, K, exact):
-    """(codes, scales on the device, the bf16 values that enter the product)"""
+def draw_fp8(rng, cap, K, exact, round_to_bf16):
+    """(codes, scales on the device, the values that enter the product)"""
     v = draw_rows(rng, cap, K, exact)
     t = torch.from_numpy(v.astype(np.float32)).to(torch.float8_e4m3fn)
     if exact:
         s = 2.0 ** rng.integers(-2, 3, size=(cap, K // 128))
     else:
         s = (rng.random((cap, K // 128)) + 0.1).astype(np.float32).astype(np.float64)
-    # a product of 4 and 24 bits, rounded to 24, then to 8
-    val = (t.float().numpy() * np.repeat(s, 128, axis=1).astype(np.float32)).astype(np.float32)
-    return t.view(torch.uint8).cuda(), dev(s.astype(np.float32)), ref.rounded(val)
+    val = t.float().double().numpy() * np.repeat(s, 128, axis=1)
+    if round_to_bf16:  # a product of 4 and 24 bits, rounded to 24, then to 8
+        val = ref.rounded(val.astype(np.float32))
+    return t.view(torch.uint8).cuda(), dev(s.astype(np.float32)), val
 
 
-def draw_x(rng, cap, K, fp8, exact, off, counts):
+def draw_x(rng, cap, K, fp8, exact, off, counts, round_to_bf16=False):
     if fp8:
-        x, xs, xv = draw_fp8(rng, cap, K, exact)
+        x, xs, xv = draw_fp8(rng, cap, K, exact, round_to_bf16)
         dead = torch.from_numpy(np.isnan(only_experts(xv, off, counts)[:, 0])).cuda()
         x[dead] = 0x7F
         xs[dead] = float("nan")
@@ -162,7 +164,7 @@ def test_weights_gradient(K, N, counts, fp8, dtype, add):
             f"exact={exact}")
         gv = draw_rows(rng, cap, N, exact)
         g = ref.to_bf16(only_experts(gv, off, counts)).cuda()
-        x, xs, xv = draw_x(rng, cap, K, fp8, exact, off, counts)
+        x, xs, xv = draw_x(rng, cap, K, fp8, exact, off, counts, round_to_bf16=True)
         want, size = ref.weights_grad(gv, xv, off, counts)
         out = torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda")
         before = None
@@ -190,20 +192,20 @@ def test_weights_gradient(K, N, counts, fp8, dtype, add):
 
 
 def test_fp8_rows_are_rounded_once():
-    """Against the unrounded rows: 2^-8 of each value at most, and the product's
-    own rounding."""
+    """The weights' gradient against the unrounded rows: 2^-8 of each value at
+    most, and the sum's own rounding."""
     rng = np.random.default_rng(5)
     K, N, counts = 512, 96, [40, 3]
     off, cap = layout_of(counts, 0)
-    x, xs, _ = draw_fp8(rng, cap, K, False)
-    raw = x.view(torch.float8_e4m3fn).float().double().cpu().numpy() * np.repeat(
-        xs.double().cpu().numpy(), 128, axis=1)
-    wt, w = draw_w(rng, counts, N, K, False)
+    x, xs, raw = draw_fp8(rng, cap, K, False, False)
+    gv = draw_rows(rng, cap, N, False)
     say("rounding of FP8 rows")
-    got = ep.Bf16Experts(wt).product(x, xs, dev(off), dev(np.array(counts, np.int32)))
-    y, size = ref.product(raw, w, off, counts)
-    err = size * UBF16 + ref.sum_error(K, size * (1 + UBF16))
-    assert np.all(np.abs(got.double().cpu().numpy() - y) <= err + (np.abs(y) + err) * UBF16)
+    e = ep.Bf16Experts(torch.zeros(2, N, K, dtype=torch.bfloat16, device="cuda"))
+    got = e.backward_weights(x, xs, ref.to_bf16(gv).cuda(), dev(off),
+                             dev(np.array(counts, np.int32)), dtype=torch.float32)
+    y, size = ref.weights_grad(gv, raw, off, counts)
+    err = size * UBF16 + ref.sum_error(40, size * (1 + UBF16))
+    assert np.all(np.abs(got.double().cpu().numpy() - y) <= err)
 
 
 @pytest.mark.parametrize("K,N", [(128, 64), (75, 33)])
