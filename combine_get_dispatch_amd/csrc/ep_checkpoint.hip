@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ep.h"
 #include "ep_host.h"
 #include "ep_moe.h"
@@ -12,8 +14,9 @@
 namespace ep {
 namespace {
 
-constexpr int kBlockCols = 128;   // columns that share a scale
-constexpr int kItemRows = 4;      // rows of an item: one per wave
+constexpr int kBlockCols = 128;  // columns that share a scale: 16 lanes x 8
+constexpr int kUnroll = 4;       // blocks of gate and up in flight per 16 lanes
+constexpr int kItemBlocks = 16 * kUnroll;  // at least; 16 x 16 lanes per workgroup
 constexpr int kGrid = 256 * 8;
 
 struct CheckpointArgs {
@@ -22,7 +25,7 @@ struct CheckpointArgs {
   uint8_t *codes;
   float *scales;
   uint16_t *h, *grad_gate_up;
-  int32_t F;
+  int32_t F, blocks, item_rows;
 };
 
 // The scale's exponent for values of at most this magnitude: 448 = 1.75 * 2^8.
@@ -39,87 +42,260 @@ __device__ __forceinline__ bool finite(float v) {
   return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
 }
 
-__device__ __forceinline__ uint8_t code_of(float v, float inverse) {
-  if (!finite(v)) return 0x7F;
-  return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v * inverse, 0.0f, 0, false);
+// Largest over the 16 lanes of a block.
+__device__ __forceinline__ float most_of_block(float v) {
+  const auto turn = [](float x, auto by) {
+    const int i = __builtin_bit_cast(int, x);
+    return fmaxf(x, __builtin_bit_cast(
+                        float, __builtin_amdgcn_update_dpp(i, i, 0x120 + decltype(by)::value, 0xF,
+                                                           0xF, false)));
+  };
+  v = turn(v, std::integral_constant<int, 8>{});
+  v = turn(v, std::integral_constant<int, 4>{});
+  v = turn(v, std::integral_constant<int, 2>{});
+  return turn(v, std::integral_constant<int, 1>{});
 }
 
-// A wave takes a row's blocks of gate and up, two columns of each per lane.
-__global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(CheckpointArgs a) {
+// Rows of odd widths begin anywhere: the hardware loads and stores 16 bytes at
+// any address.
+struct __attribute__((packed, aligned(1))) Any16 {
+  u32x4 v;
+};
+struct __attribute__((packed, aligned(1))) Any8 {
+  u32x2 v;
+};
+
+// Eight columns of a row, of which there are n.
+__device__ __forceinline__ u32x4 load_bf16(const uint16_t *p, int n) {
+  if (n >= 8) return reinterpret_cast<const Any16 *>(p)->v;
+  u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) v[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+  return v;
+}
+
+__device__ __forceinline__ void store_bf16(uint16_t *p, int n, const float *y) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = f32_to_bf16(y[2 * i]) | (uint32_t)f32_to_bf16(y[2 * i + 1]) << 16;
+  if (n >= 8) {
+    reinterpret_cast<Any16 *>(p)->v = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
+}
+
+__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n) {
+  if (n >= 8) return reinterpret_cast<const Any8 *>(p)->v;
+  u32x2 v = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) v[i / 4] |= (uint32_t)p[i] << (i % 4 * 8);
+  return v;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t *p, int n, u32x2 v) {
+  if (n >= 8) {
+    reinterpret_cast<Any8 *>(p)->v = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = (uint8_t)(v[i / 4] >> (i % 4 * 8));
+}
+
+__device__ __forceinline__ void unpack(u32x4 v, float *y) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    y[i] = __uint_as_float(i % 2 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+}
+
+// 1 / (1 + exp(-y)) and 1 minus it of eight values, by t = exp(-|y|): the
+// hardware's exp2 of y log2 e, whose rounding is put back to first order, and
+// its reciprocal; off by few half steps.  Past 80 t comes near the smallest
+// normal number, where exp2 ends: there by expf.
+__device__ __forceinline__ void sigmoids8(const float *y, float *s, float *rest) {
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(y[i]));
+  if (__any(most > 80.0f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sigmoids(y[i], &s[i], &rest[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+    const float x = -fabsf(y[i]), n = x * kLog2e;
+    const float lost = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -n));
+    const float e = __builtin_amdgcn_exp2f(n);
+    const float t = __builtin_fmaf(e * kLn2, lost, e);
+    const float d = __builtin_amdgcn_rcpf(1.0f + t), td = t * d;
+    s[i] = y[i] < 0.0f ? td : d;
+    rest[i] = y[i] < 0.0f ? d : td;
+  }
+}
+
+// Eight codes of 16 lanes' values, and the block's scale.
+__device__ __forceinline__ u32x2 encode(const float *y, float *scale) {
+  float most = 0.0f, v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = y[i];
+    most = fmaxf(most, fabsf(v[i]));  // passes over NaN
+  }
+  if (__any(!finite(most))) {
+    most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (finite(v[i]))
+        most = fmaxf(most, fabsf(v[i]));
+      else
+        v[i] = __builtin_nanf("");
+    }
+  }
+  const int e = scale_exponent(most_of_block(most));
+  *scale = power_of_two(e);
+  const float inverse = power_of_two(-e);
+  u32x2 codes;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inverse, v[4 * i + 1] * inverse, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inverse, v[4 * i + 3] * inverse, w, true);
+    codes[i] = (uint32_t)w;
+  }
+  return codes;
+}
+
+// Calls f(row, block) for the blocks of all rows, each with 16 lanes, kUnroll
+// calls of load before those of work.
+template <typename Load, typename Work>
+__device__ __forceinline__ void for_blocks(const CheckpointArgs &a, Load load, Work work) {
   __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[4];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int item_rows = a.item_rows;
   number_blocks(a.rows, starts, totals,
-                [](int64_t rows) { return (rows + kItemRows - 1) / kItemRows; });
-  const int F = a.F, blocks = (F + kBlockCols - 1) / kBlockCols;
+                [=](int64_t rows) { return (rows + item_rows - 1) / item_rows; });
   const int64_t items = starts[a.rows.E];
   for (int64_t i0 = blockIdx.x; i0 < items; i0 += gridDim.x) {
     const int32_t item = (int32_t)i0;
     const int e = expert_of(starts, a.rows.E, item);
     int64_t first, rows;
     rows_inside(a.rows.offsets[e], a.rows.counts[e], a.rows.capacity, &first, &rows);
-    const int64_t r = (int64_t)(item - starts[e]) * kItemRows + wave;
-    if (r >= rows) continue;
-    const uint16_t *in = a.gate_up + (first + r) * 2 * F;
-    for (int b = 0; b < blocks; ++b) {
-      float v[2][2];
+    const int64_t skip = (int64_t)(item - starts[e]) * item_rows;
+    const int n = (int)(rows - skip < item_rows ? rows - skip : item_rows) * a.blocks;
+    for (int q0 = threadIdx.x / 16; q0 < n; q0 += kItemBlocks) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float most = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = b * kBlockCols + lane + 64 * i;
-          v[half][i] = c < F ? bf16_to_f32(in[half * F + c]) : 0.0f;
-          if (finite(v[half][i])) most = fmaxf(most, fabsf(v[half][i]));
-        }
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-        const int x = scale_exponent(most);
-        if (lane == 0) a.scales[((first + r) * 2 + half) * blocks + b] = power_of_two(x);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = b * kBlockCols + lane + 64 * i;
-          if (c < F)
-            a.codes[((first + r) * 2 + half) * F + c] = code_of(v[half][i], power_of_two(-x));
-        }
+      for (int u = 0; u < kUnroll; ++u) {
+        const int q = q0 + 16 * u;
+        if (q < n) load(u, first + skip + q / a.blocks, q % a.blocks);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = b * kBlockCols + lane + 64 * i;
-        if (c < F) a.h[(first + r) * F + c] = f32_to_bf16(silu_of(v[0][i]) * v[1][i]);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int q = q0 + 16 * u;
+        if (q < n) work(u, first + skip + q / a.blocks, q % a.blocks);
       }
     }
   }
+}
+
+__global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(CheckpointArgs a) {
+  const int l16 = threadIdx.x & 15;
+  const int F = a.F, blocks = a.blocks;
+  u32x4 gate[kUnroll], up[kUnroll];
+  for_blocks(
+      a,
+      [&](int u, int64_t row, int b) {
+        const int c = b * kBlockCols + l16 * 8;
+        const uint16_t *p = a.gate_up + row * 2 * F + c;
+        gate[u] = load_bf16(p, F - c);
+        up[u] = load_bf16(p + F, F - c);
+      },
+      [&](int u, int64_t row, int b) {
+        const int c = b * kBlockCols + l16 * 8;
+        float x[8], y[8], s[8], rest[8], scale;
+        unpack(gate[u], x);
+        unpack(up[u], y);
+        uint8_t *codes = a.codes + row * 2 * F + c;
+        float *scales = a.scales + row * 2 * blocks + b;
+        store_codes(codes, F - c, encode(x, &scale));
+        if (l16 == 0) scales[0] = scale;
+        store_codes(codes + F, F - c, encode(y, &scale));
+        if (l16 == 0) scales[blocks] = scale;
+        sigmoids8(x, s, rest);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * s[i] * y[i];
+        store_bf16(a.h + row * F + c, F - c, x);
+      });
 }
 
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(CheckpointArgs a) {
-  __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[4];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  number_blocks(a.rows, starts, totals,
-                [](int64_t rows) { return (rows + kItemRows - 1) / kItemRows; });
-  const int F = a.F, blocks = (F + kBlockCols - 1) / kBlockCols;
-  const int64_t items = starts[a.rows.E];
-  for (int64_t i0 = blockIdx.x; i0 < items; i0 += gridDim.x) {
-    const int32_t item = (int32_t)i0;
-    const int e = expert_of(starts, a.rows.E, item);
-    int64_t first, rows;
-    rows_inside(a.rows.offsets[e], a.rows.counts[e], a.rows.capacity, &first, &rows);
-    const int64_t r = (int64_t)(item - starts[e]) * kItemRows + wave;
-    if (r >= rows) continue;
-    const uint8_t *codes = a.codes + (first + r) * 2 * F;
-    const float *scales = a.scales + (first + r) * 2 * blocks;
-    for (int c = lane; c < F; c += 64) {
-      const int b = c / kBlockCols;
-      const float g = __builtin_amdgcn_cvt_f32_fp8((int)codes[c], 0) * scales[b];
-      const float u = __builtin_amdgcn_cvt_f32_fp8((int)codes[F + c], 0) * scales[blocks + b];
-      const float d = bf16_to_f32(a.grad_h[(first + r) * F + c]);
-      float s, t;
-      sigmoids(g, &s, &t);
-      uint16_t *out = a.grad_gate_up + (first + r) * 2 * F + c;
-      out[0] = f32_to_bf16(s * (1.0f + g * t) * u * d);
-      out[F] = f32_to_bf16(g * s * d);
-      if (a.h != nullptr) a.h[(first + r) * F + c] = f32_to_bf16(g * s * u);
-    }
-  }
+  const int l16 = threadIdx.x & 15;
+  const int F = a.F, blocks = a.blocks;
+  u32x2 gate[kUnroll], up[kUnroll];
+  u32x4 grad[kUnroll];
+  float gate_scale[kUnroll], up_scale[kUnroll];
+  for_blocks(
+      a,
+      [&](int u, int64_t row, int b) {
+        const int c = b * kBlockCols + l16 * 8;
+        const uint8_t *codes = a.codes + row * 2 * F + c;
+        const float *scales = a.scales + row * 2 * blocks + b;
+        gate[u] = load_codes(codes, F - c);
+        up[u] = load_codes(codes + F, F - c);
+        gate_scale[u] = scales[0];
+        up_scale[u] = scales[blocks];
+        grad[u] = load_bf16(a.grad_h + row * F + c, F - c);
+      },
+      [&](int u, int64_t row, int b) {
+        const int c = b * kBlockCols + l16 * 8;
+        float x[8], y[8], d[8], s[8], rest[8], dx[8], dy[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const auto g = i % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)gate[u][i / 2], true)
+                               : __builtin_amdgcn_cvt_pk_f32_fp8((int)gate[u][i / 2], false);
+          const auto p = i % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)up[u][i / 2], true)
+                               : __builtin_amdgcn_cvt_pk_f32_fp8((int)up[u][i / 2], false);
+          x[2 * i] = g[0] * gate_scale[u];
+          x[2 * i + 1] = g[1] * gate_scale[u];
+          y[2 * i] = p[0] * up_scale[u];
+          y[2 * i + 1] = p[1] * up_scale[u];
+        }
+        unpack(grad[u], d);
+        sigmoids8(x, s, rest);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // the sigmoid first: where it is 0 no product before it may overflow
+          const float silu = x[i] * s[i];
+          dx[i] = s[i] * __builtin_fmaf(x[i], rest[i], 1.0f) * y[i] * d[i];
+          dy[i] = silu * d[i];
+          x[i] = silu * y[i];
+        }
+        uint16_t *out = a.grad_gate_up + row * 2 * F + c;
+        store_bf16(out, F - c, dx);
+        store_bf16(out + F, F - c, dy);
+        if (a.h != nullptr) store_bf16(a.h + row * F + c, F - c, x);
+      });
+}
+
+// Rows, their blocks, and how many rows make an item.
+CheckpointArgs checkpoint_args(int32_t E, int32_t F, const int32_t *offsets,
+                               const int32_t *counts, int64_t capacity) {
+  CheckpointArgs a = {};
+  a.rows = ExpertRows{offsets, counts, capacity, E};
+  a.F = F;
+  a.blocks = (F + kBlockCols - 1) / kBlockCols;
+  a.item_rows = (kItemBlocks + a.blocks - 1) / a.blocks;
+  if (a.item_rows < 4) a.item_rows = 4;
+  return a;
+}
+
+int checkpoint_grid(const CheckpointArgs &a) {
+  const int64_t items = a.rows.capacity / a.item_rows + a.rows.E;
+  return (int)(items < kGrid ? items : kGrid);
 }
 
 ep_status_t check_checkpoint(int32_t E, int32_t F, const int32_t *offsets, const int32_t *counts,
@@ -130,7 +306,7 @@ ep_status_t check_checkpoint(int32_t E, int32_t F, const int32_t *offsets, const
     return failf(EP_ERR_INVALID_ARG, "features %d outside [1, 2^20)", F);
   if (capacity < 0 || capacity >= INT32_MAX)
     return failf(EP_ERR_INVALID_ARG, "capacity %lld outside [0, 2^31 - 1)", (long long)capacity);
-  if ((capacity / kItemRows + 1) * E >= INT32_MAX)
+  if ((capacity / 4 + 1) * E >= INT32_MAX)
     return failf(EP_ERR_INVALID_ARG, "capacity %lld x %d experts has too many row blocks",
                  (long long)capacity, E);
   if (offsets == nullptr || counts == nullptr)
@@ -179,14 +355,14 @@ ep_status_t ep_swiglu_checkpoint(int32_t num_experts, int32_t features, const ui
   for (int i = 0; i < 4; ++i)
     for (int j = 0; j < i; ++j)
       if (!apart(all[i], all[j])) return failf(EP_ERR_INVALID_ARG, "two of the arrays overlap");
-  CheckpointArgs a = {};
-  a.rows = ExpertRows{expert_offsets, num_tokens_per_expert, capacity, num_experts};
+  CheckpointArgs a =
+      checkpoint_args(num_experts, features, expert_offsets, num_tokens_per_expert, capacity);
   a.gate_up = gate_up;
   a.h = h;
   a.codes = codes;
   a.scales = scales;
-  a.F = features;
-  hipLaunchKernelGGL(swiglu_checkpoint_kernel, dim3(kGrid), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(swiglu_checkpoint_kernel, dim3(checkpoint_grid(a)), dim3(256), 0,
+                     stream, a);
   return launched("checkpoint launch");
 }
 
@@ -211,15 +387,15 @@ ep_status_t ep_swiglu_checkpoint_backward(int32_t num_experts, int32_t features,
   for (int i = 0; i < 2; ++i)  // the outputs against all
     for (int j = i + 1; j < 5; ++j)
       if (!apart(all[i], all[j])) return failf(EP_ERR_INVALID_ARG, "two of the arrays overlap");
-  CheckpointArgs a = {};
-  a.rows = ExpertRows{expert_offsets, num_tokens_per_expert, capacity, num_experts};
+  CheckpointArgs a =
+      checkpoint_args(num_experts, features, expert_offsets, num_tokens_per_expert, capacity);
   a.codes = const_cast<uint8_t *>(codes);
   a.scales = const_cast<float *>(scales);
   a.grad_h = grad_h;
   a.grad_gate_up = grad_gate_up;
   a.h = h;
-  a.F = features;
-  hipLaunchKernelGGL(swiglu_backward_kernel, dim3(kGrid), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(swiglu_backward_kernel, dim3(checkpoint_grid(a)), dim3(256), 0,
+                     stream, a);
   return launched("checkpoint backward launch");
 }
 

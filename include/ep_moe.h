@@ -330,8 +330,9 @@ ep_status_t ep_expert_product_backward_weights(
  *
  *   num_experts  1 .. EP_MAX_EXPERTS;  features  F: 1 <= F < 2^20
  *   gate_up  bf16 [capacity, 2 F], as ep_expert_product writes it; 16-byte aligned
- *   expert_offsets, num_tokens_per_expert, capacity   as in ep_expert_product;
- *            only the experts' rows are read and written
+ *   expert_offsets, num_tokens_per_expert, capacity   as in ep_expert_product,
+ *            but (capacity / 4 + 1) * num_experts < 2^31 - 1; only the experts'
+ *            rows are read and written
  *   h        bf16 [capacity, F];  codes uint8 [capacity, 2 F];
  *   scales   fp32 [capacity, 2 * ceil(F / 128)]; all apart from gate_up,
  *            h and codes 16-byte aligned
