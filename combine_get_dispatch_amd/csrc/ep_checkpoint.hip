@@ -56,25 +56,6 @@ __device__ __forceinline__ float most_of_block(float v) {
   return turn(v, std::integral_constant<int, 1>{});
 }
 
-// Rows of odd widths begin anywhere: the hardware loads and stores 16 bytes at
-// any address.
-struct __attribute__((packed, aligned(1))) Any16 {
-  u32x4 v;
-};
-struct __attribute__((packed, aligned(1))) Any8 {
-  u32x2 v;
-};
-
-// Eight columns of a row, of which there are n.
-__device__ __forceinline__ u32x4 load_bf16(const uint16_t *p, int n) {
-  if (n >= 8) return reinterpret_cast<const Any16 *>(p)->v;
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) v[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
-  return v;
-}
-
 __device__ __forceinline__ void store_bf16(uint16_t *p, int n, const float *y) {
   u32x4 v;
 #pragma unroll
@@ -87,15 +68,6 @@ __device__ __forceinline__ void store_bf16(uint16_t *p, int n, const float *y) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) p[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
-}
-
-__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n) {
-  if (n >= 8) return reinterpret_cast<const Any8 *>(p)->v;
-  u32x2 v = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) v[i / 4] |= (uint32_t)p[i] << (i % 4 * 8);
-  return v;
 }
 
 __device__ __forceinline__ void store_codes(uint8_t *p, int n, u32x2 v) {

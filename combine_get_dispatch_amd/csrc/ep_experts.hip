@@ -29,31 +29,66 @@ struct ProductArgs {
   const void *add;        // weights' gradient, or NULL
   void *out;
   int32_t K, N;
+  int32_t out_any;  // product: out is not 16-byte aligned
 };
 
 __device__ __forceinline__ f32x4 mul(bf16x8 x, bf16x8 w, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
-// A value of an FP8 row as bf16, rounded (exact where the scale is 1).
-__device__ __forceinline__ uint16_t fp8_bf16(uint8_t code, float scale) {
-  return f32_to_bf16(__builtin_amdgcn_cvt_f32_fp8((int)code, 0) * scale);
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
 }
 
-// Any sizes and alignments: tiles of 64 x 64 x 32, loaded value by value.
-constexpr int kAnyTile = 64, kAnyDepth = 32, kAnyGrid = 1024;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Two transposing reads, at l 0 .. 3 and 4 .. 7 of a lane's eight.
+__device__ __forceinline__ bf16x8 read_transposed(const uint8_t *lo, const uint8_t *hi) {
+  struct {
+    s16x4 lo, hi;
+  } v;
+  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)lo);
+  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)hi);
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// Eight FP8 codes times their scale, rounded to bf16.
+__device__ __forceinline__ u32x4 scaled_bf16(u32x2 codes, float scale) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[i], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[i], true);
+    w[2 * i] = pack_bf16(lo[0] * scale, lo[1] * scale);
+    w[2 * i + 1] = pack_bf16(hi[0] * scale, hi[1] * scale);
+  }
+  return w;
+}
+
+// Rows that begin between 16-byte boundaries (K or N no multiple of 8): tiles of
+// 64 x 64, 64 of the sum at a time, through registers, two stages ahead of their
+// use.  Layouts in LDS as in the large tiles: "along", where l is consecutive,
+// 64 rows of 128 bytes; "across", where m or n is, 64 l of 128 bytes.
+// 333 rows of 11 experts, rows' gradient of 1480 x 1001: 19 us, bound by the
+// latency of 16 stages; 32768 rows of 32 experts, 2047 x 7168: 3.94 ms, 244 TFLOP/s.
+constexpr int kAnyTile = 64, kAnyDepth = 64, kAnyGrid = 1024;
+constexpr int kAnySide = kAnyTile * kAnyDepth * 2;
 
 template <Kind KIND, bool FP8, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
-  __shared__ __align__(16) uint16_t as[kAnyTile][kAnyDepth + 8], bs[kAnyTile][kAnyDepth + 8];
+  static_assert(KIND == kWeightsGrad || !FP8, "FP8 rows of a product are in whole pieces");
+  constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
+  constexpr int kCols = SWIGLU ? kAnyTile / 2 : kAnyTile;  // output columns of a tile
+  __shared__ __align__(16) uint8_t stage[2][2][kAnySide];  // of a buffer: rows, columns
   __shared__ int32_t starts[EP_MAX_EXPERTS + 1], totals[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int col = lane & 15, quad = lane >> 4;
+  const int l16 = lane & 15, quad = lane >> 4;
+  const int wr = wave >> 1, wc = wave & 1;
   const int E = a.rows.E, K = a.K, N = a.N;
   const uint8_t *x8 = static_cast<const uint8_t *>(a.x);
   const uint16_t *x16 = static_cast<const uint16_t *>(a.x);
   const int out_cols = KIND == kProduct ? (SWIGLU ? N / 2 : N) : K;
-  constexpr int kCols = SWIGLU ? kAnyTile / 2 : kAnyTile;  // output columns of a tile
   const int col_tiles = (out_cols + kCols - 1) / kCols;
   const int row_tiles = (N + kAnyTile - 1) / kAnyTile;  // weights' gradient
   int64_t items;
@@ -83,91 +118,128 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
     }
     const int64_t length = KIND == kProduct ? K : KIND == kRowsGrad ? N : rows;
     const uint16_t *w = a.w + (int64_t)e * N * K;
-    const auto a_value = [&](int m, int64_t l) -> uint16_t {
-      if (l >= length) return 0;
-      if (KIND == kProduct) {
-        if (m >= rows) return 0;
-        if (FP8) return fp8_bf16(x8[(first + m) * K + l], 1.0f);
-        return x16[(first + m) * K + l];
+    // Piece i of this thread: eight values, of row i of the side and l on from l0
+    // (along), or of l i and on from the tile's first row or column (across).
+    const auto there = [](int64_t n) { return (int)(n < 0 ? 0 : n < 8 ? n : 8); };
+    const auto row_piece = [&](int64_t l0, int i) -> u32x4 {
+      const int at = i >> 3, p = (i & 7) * 8;
+      if (kRowsAcross) {
+        if (l0 + at >= length) return u32x4{0, 0, 0, 0};
+        return load_bf16(a.grad + (first + l0 + at) * N + m0 + p, there(N - m0 - p));
       }
-      if (KIND == kRowsGrad) return m < rows ? a.grad[(first + m) * N + l] : (uint16_t)0;
-      return m0 + m < N ? a.grad[(first + l) * N + m0 + m] : (uint16_t)0;
+      if (at >= rows) return u32x4{0, 0, 0, 0};
+      const uint16_t *from = KIND == kProduct ? x16 + (first + at) * K : a.grad + (first + at) * N;
+      return load_bf16(from + l0 + p, there(length - l0 - p));
     };
-    const auto b_value = [&](int n, int64_t l) -> uint16_t {
-      if (l >= length) return 0;
-      if (KIND == kProduct) {
-        const int c = n0 + n % kCols;
-        return c < out_cols ? w[(int64_t)(c + n / kCols * out_cols) * K + l] : (uint16_t)0;
+    const auto col_piece = [&](int64_t l0, int i) -> u32x4 {
+      const int at = i >> 3, p = (i & 7) * 8;
+      if (!kColsAcross) {
+        const int c = n0 + at % kCols;
+        if (c >= out_cols) return u32x4{0, 0, 0, 0};
+        return load_bf16(w + (int64_t)(c + at / kCols * out_cols) * K + l0 + p,
+                         there(length - l0 - p));
       }
-      const int c = n0 + n;
-      if (c >= K) return 0;
-      if (KIND == kRowsGrad) return w[l * K + c];
-      if (FP8)
-        return fp8_bf16(x8[(first + l) * K + c], a.x_scales[(first + l) * (K / 128) + c / 128]);
-      return x16[(first + l) * K + c];
+      if (l0 + at >= length) return u32x4{0, 0, 0, 0};
+      if (KIND == kRowsGrad)
+        return load_bf16(w + (l0 + at) * K + n0 + p, there(K - n0 - p));
+      const int64_t r = first + l0 + at;
+      if (FP8) {  // K is a multiple of 128
+        if (n0 + p >= K) return u32x4{0, 0, 0, 0};
+        return scaled_bf16(load_codes(x8 + r * K + n0 + p, 8),
+                           a.x_scales[r * (K / 128) + (n0 + p) / 128]);
+      }
+      return load_bf16(x16 + r * K + n0 + p, there(K - n0 - p));
     };
-    // the product's FP8 rows: acc sums 128 of l, part their products with the scale
-    f32x4 acc[4], part[4];
+    const auto place = [](bool across, int i) {  // of piece i in LDS
+      const int at = i >> 3, p = i & 7;
+      return at * 128 + (p ^ (across ? (at >> 1 & 3) << 1 : at >> 1 & 7)) * 16;
+    };
+    struct Pieces {
+      u32x4 rows[2], cols[2];
+    };
+    const auto load = [&](int64_t l0, Pieces *p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = part[i] = f32x4{0, 0, 0, 0};
-    for (int64_t l0 = 0; l0 < length; l0 += kAnyDepth) {
-      for (int i = tid; i < kAnyTile * kAnyDepth; i += 256) {
-        // neighbouring threads read neighbouring values
-        const int across = i % kAnyTile, al = i / kAnyTile;
-        const int along = i % kAnyDepth, am = i / kAnyDepth;
-        if (KIND == kWeightsGrad)
-          as[across][al] = a_value(across, l0 + al);
-        else
-          as[am][along] = a_value(am, l0 + along);
-        if (KIND == kProduct)
-          bs[am][along] = b_value(am, l0 + along);
-        else
-          bs[across][al] = b_value(across, l0 + al);
+      for (int i = 0; i < 2; ++i) {
+        p->rows[i] = row_piece(l0, tid + i * 256);
+        p->cols[i] = col_piece(l0, tid + i * 256);
       }
-      __syncthreads();
-      const bf16x8 av = *reinterpret_cast<const bf16x8 *>(&as[wave * 16 + col][quad * 8]);
+    };
+    const auto put = [&](int buffer, const Pieces &p) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[i] = mul(av, *reinterpret_cast<const bf16x8 *>(&bs[i * 16 + col][quad * 8]), acc[i]);
-      if (KIND == kProduct && FP8 && l0 % 128 == 128 - kAnyDepth) {
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<u32x4 *>(&stage[buffer][0][place(kRowsAcross, tid + i * 256)]) = p.rows[i];
+        *reinterpret_cast<u32x4 *>(&stage[buffer][1][place(kColsAcross, tid + i * 256)]) = p.cols[i];
+      }
+    };
+    // 16 rows (or columns) from `from` on, l 32 ks .. + 31
+    const auto read = [&](const uint8_t *side, bool across, int from, int ks) -> bf16x8 {
+      if (across) {
+        const int l = ks * 32 + quad * 8 + l16 / 4, p = from / 8 + l16 % 4 / 2;
+        const auto at = [&](int l) { return l * 128 + (p ^ (l >> 1 & 3) << 1) * 16 + l16 % 2 * 8; };
+        return read_transposed(side + at(l), side + at(l + 4));
+      }
+      const int r = from + l16;
+      return *reinterpret_cast<const bf16x8 *>(side + r * 128 + ((ks * 4 + quad) ^ (r >> 1 & 7)) * 16);
+    };
+    f32x4 acc[2][2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
+    const int64_t steps = (length + kAnyDepth - 1) / kAnyDepth;
+    const auto step = [&](int64_t s, Pieces *mine, const Pieces *next) {
+      const int buffer = (int)(s & 1);
+      __syncthreads();  // this stage is in LDS, the other buffer free
+      put(buffer ^ 1, *next);
+      load((s + 3) * kAnyDepth, mine);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        bf16x8 r[2], c[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) r[f] = read(stage[buffer][0], kRowsAcross, wr * 32 + f * 16, ks);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) c[j] = read(stage[buffer][1], kColsAcross, j * 32 + wc * 16, ks);
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[f][j] = mul(c[j], r[f], acc[f][j]);
+      }
+    };
+    if (steps > 0) {
+      Pieces p[2];
+      load(0, &p[0]);
+      __syncthreads();  // the buffers are free of the last item
+      put(0, p[0]);
+      load(kAnyDepth, &p[1]);
+      load(2 * kAnyDepth, &p[0]);
+      // stage s + 1 is in p[(s + 1) & 1], s + 2 in the other
+      for (int64_t s = 0; s < steps; s += 2) {
+        step(s, &p[1], &p[1]);
+        if (s + 1 < steps) step(s + 1, &p[0], &p[0]);
+      }
+    }
+    constexpr int kOut = SWIGLU ? 1 : 2;
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int j = 0; j < kOut; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const int m = wave * 16 + quad * 4 + v;
-          const float scale =
-              m < rows ? a.x_scales[(first + m) * (K / 128) + l0 / 128] : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            part[i][v] = __builtin_fmaf(scale, acc[i][v], part[i][v]);
-            acc[i][v] = 0.0f;
+          const int m = wr * 32 + f * 16 + l16, c = n0 + j * 32 + wc * 16 + quad * 4 + v;
+          if (c >= out_cols || (KIND == kWeightsGrad ? m0 + m >= N : m >= rows)) continue;
+          float y = acc[f][j][v];
+          if (SWIGLU) y = silu_of(y) * acc[f][1][v];
+          const int64_t at = KIND == kWeightsGrad ? ((int64_t)e * N + m0 + m) * K + c
+                                                  : (first + m) * out_cols + c;
+          if constexpr (std::is_same<OUT, float>::value) {
+            if (a.add != nullptr) y += static_cast<const float *>(a.add)[at];
+            static_cast<float *>(a.out)[at] = y;
+          } else {
+            if (KIND == kWeightsGrad && a.add != nullptr)
+              y += bf16_to_f32(static_cast<const uint16_t *>(a.add)[at]);
+            static_cast<uint16_t *>(a.out)[at] = f32_to_bf16(y);
           }
         }
-      }
-      __syncthreads();
-    }
-    if (KIND == kProduct && FP8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = part[i];
-    }
-    constexpr int kOut = SWIGLU ? 2 : 4;
-#pragma unroll
-    for (int i = 0; i < kOut; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int m = wave * 16 + quad * 4 + v, c = n0 + i * 16 + col;
-        if (c >= out_cols || (KIND == kWeightsGrad ? m0 + m >= N : m >= rows)) continue;
-        float y = acc[i][v];
-        if (SWIGLU) y = silu_of(y) * acc[2 + i][v];
-        const int64_t at = KIND == kWeightsGrad ? ((int64_t)e * N + m0 + m) * K + c
-                                                : (first + m) * out_cols + c;
-        if constexpr (std::is_same<OUT, float>::value) {
-          if (a.add != nullptr) y += static_cast<const float *>(a.add)[at];
-          static_cast<float *>(a.out)[at] = y;
-        } else {
-          if (KIND == kWeightsGrad && a.add != nullptr)
-            y += bf16_to_f32(static_cast<const uint16_t *>(a.add)[at]);
-          static_cast<uint16_t *>(a.out)[at] = f32_to_bf16(y);
-        }
-      }
   }
 }
 
@@ -179,7 +251,6 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 // "Rows" is the side of m, "columns" that of n.  The matrix instruction takes
 // columns first, so that a lane's results are consecutive columns of one row.
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 256;            // rows and columns of a tile
@@ -210,10 +281,6 @@ __device__ __forceinline__ void load_word_to_lds(uint32_t lds, uint32_t offset, 
       :
       : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
       : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
 }
 
 // Eight FP8 codes as bf16, which holds every E4M3 number.
@@ -427,15 +494,9 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
                                 : kRowsAcross ? across ^ wr * 32
                                               : along + wr * 2048);
   const int col_at = kCols8 ? across8 ^ wc * 64 : kColsAcross ? across ^ wc * 128 : along + wc * 8192;
-  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
   const auto read_across = [&](int at) {
-    struct {
-      s16x4 lo, hi;
-    } v;
-    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at));
-    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(stage + at + 4 * 512));
-    return __builtin_bit_cast(bf16x8, v);
+    return read_transposed(stage + at, stage + at + 4 * 512);
   };
   // rows 32 f + 16 wr .. + 15, columns 64 wc + 16 j .. + 15, half ks of a stage
   const auto read_row = [&](int slot, int ks, int f) {
@@ -739,7 +800,9 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
       // us instead of 2040; through LDS 2056).  Rows that are not there are outside
       // the buffer of the stores.
       constexpr int kHere = SWIGLU ? 2 : 4;  // 16 columns each
-      stored = steps > 0 ? kStores * kM : 0;
+      // rows of results that begin between 16-byte boundaries
+      const bool any_store = KIND == kProduct && (out_cols % 8 != 0 || a.out_any);
+      stored = steps > 0 && !any_store ? kStores * kM : 0;
       const int64_t to_row =
           KIND == kWeightsGrad ? (int64_t)it.e * N + it.row0 : it.first + it.row0;
       const int pitch = out_cols * kSize;
@@ -811,7 +874,15 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
               v[j / 2][p] = y[0];
               v[j / 2][2 + p] = y[1];
             }
-          if constexpr (SWIGLU) {
+          if (KIND == kProduct && any_store) {
+#pragma unroll
+            for (int j = 0; j < kHere; j += 2)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                __builtin_amdgcn_raw_buffer_store_b16(
+                    (uint16_t)(v[j / 2][i / 2] >> (i % 2 * 16)), out,
+                    from(row, j * 16 + at_quad * 8 + i) + down, 0, 0);
+          } else if constexpr (SWIGLU) {
             __builtin_amdgcn_raw_buffer_store_b128(v[0], out, from(row, at_quad * 8) + down, 0, 0);
           } else {
             halve_rows(&v[0], &v[1]);
@@ -933,13 +1004,13 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
   a.x_scales = x_scales;
   a.w = w;
   a.out = out;
-  const bool tiled = K % 8 == 0 && (swiglu ? N / 2 : N) % 8 == 0 && aligned_to(out, 16);
+  a.out_any = !aligned_to(out, 16);
   const auto launch = [&](auto f, auto s) {
-    if (tiled)
+    if (f.value || K % 8 == 0)
       hipLaunchKernelGGL((product_tile_kernel<kProduct, f.value, s.value, uint16_t>),
                          dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
     else
-      hipLaunchKernelGGL((product_any_kernel<kProduct, f.value, s.value, uint16_t>),
+      hipLaunchKernelGGL((product_any_kernel<kProduct, false, s.value, uint16_t>),
                          dim3(kAnyGrid), dim3(256), 0, stream, a);
   };
   const auto by_swiglu = [&](auto f) {

@@ -39,6 +39,34 @@ __device__ __forceinline__ float silu_of(float y) {
   return y * ((y < 0.0f ? t : 1.0f) / (1.0f + t));
 }
 
+// Rows of odd widths begin anywhere: the hardware loads and stores 16 bytes at
+// any address.
+struct __attribute__((packed, aligned(1))) Any16 {
+  u32x4 v;
+};
+struct __attribute__((packed, aligned(1))) Any8 {
+  u32x2 v;
+};
+
+// Eight columns of a row, of which there are n.
+__device__ __forceinline__ u32x4 load_bf16(const uint16_t *p, int n) {
+  if (n >= 8) return reinterpret_cast<const Any16 *>(p)->v;
+  u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) v[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+  return v;
+}
+
+__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n) {
+  if (n >= 8) return reinterpret_cast<const Any8 *>(p)->v;
+  u32x2 v = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) v[i / 4] |= (uint32_t)p[i] << (i % 4 * 8);
+  return v;
+}
+
 // Rows of an expert inside the buffers.
 __device__ __forceinline__ void rows_inside(int32_t offset, int32_t count, int64_t capacity,
                                             int64_t *first, int64_t *rows) {
