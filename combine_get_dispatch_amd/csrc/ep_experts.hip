@@ -309,6 +309,15 @@ __device__ __forceinline__ bf16x8 scaled_bf16(u32x2 codes, const f32x4 *scales) 
   return __builtin_bit_cast(bf16x8, w);
 }
 
+template <int kLeft>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void lds_done() {
+  asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+}
+
 // All but the newest kLeft loads and stores are done, and this wave's LDS
 // reads, and so for every wave of the workgroup.
 template <int kLeft>
@@ -911,6 +920,154 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
   stage_barrier<0>();  // no load may write to LDS after the end
 }
 
+// --------------------------------------------------------------------------
+// Few rows
+// --------------------------------------------------------------------------
+//
+// A workgroup has 32 rows of one expert's weights (SwiGLU: 16 of the gate and 16
+// of up), all of the sum and 16 rows of x at a time; the sum is dealt to its
+// waves in chunks, and theirs are added in LDS at the end.  Each wave loads for
+// itself, three chunks ahead and without barriers: reading the weights is the
+// bound, and what counts is how much of it is on its way (STREAM_NOTE).
+constexpr int kStreamWaves = 4, kStreamStages = 3, kStreamRows = 16, kStreamCols = 32;
+
+template <bool FP8, bool SWIGLU>
+__global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(ProductArgs a) {
+  // 128 bytes of each row of x are a chunk
+  constexpr int kChunk = FP8 ? 128 : 64;
+  constexpr int kWBytes = kStreamCols * kChunk * 2, kXBytes = kStreamRows * 128;
+  constexpr int kWLoads = kWBytes / 1024, kXLoads = kXBytes / 1024;
+  constexpr int kLoads = kWLoads + kXLoads + FP8;
+  constexpr int kStages = kStreamStages;
+  constexpr int kBytes = kWBytes + kXBytes + (FP8 ? 256 : 0);
+  constexpr int kOutCols = SWIGLU ? kStreamCols / 2 : kStreamCols;
+  __shared__ __align__(1024) uint8_t stage[kStreamWaves][kStages][kBytes];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int l16 = lane & 15, quad = lane >> 4;
+  const int e = blockIdx.y, K = a.K, N = a.N;
+  const int out_cols = SWIGLU ? N / 2 : N;
+  const int n0 = blockIdx.x * kOutCols;
+  int64_t first, rows;
+  rows_inside(uniform(a.rows.offsets[e]), uniform(a.rows.counts[e]), a.rows.capacity, &first, &rows);
+  if (rows == 0) return;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_byte *)&stage[wave][0][0];
+  const int chunks = (K + kChunk - 1) / kChunk;
+  const int x_pitch = K * (FP8 ? 1 : 2), w_pitch = K * 2;
+  // Rows of 128 bytes in LDS, 8 per load; in FP8 a row of the weights is two, of
+  // 64 columns each.  Pieces swizzled as in the tiles.
+  const int at_row = lane >> 3, piece = (lane & 7) ^ (lane >> 4);  // rows 0 .. 7; 8 .. 15: ^ 4
+  const uint8_t *w0 = reinterpret_cast<const uint8_t *>(a.w) + ((int64_t)e * N + n0) * w_pitch;
+  const int there = out_cols - n0 < kOutCols ? out_cols - n0 : kOutCols;
+  for (int64_t r0 = 0; r0 < rows; r0 += kStreamRows) {
+    const int left = (int)(rows - r0 < kStreamRows ? rows - r0 : kStreamRows);
+    const uint8_t *x0 = static_cast<const uint8_t *>(a.x) + (first + r0) * x_pitch;
+    const uint8_t *s0 = reinterpret_cast<const uint8_t *>(a.x_scales) + (first + r0) * (K / 128) * 4;
+    const auto issue = [&](int c, int slot) {  // chunk c, or zeros past the last
+      const uint32_t lds = lds0 + slot * kBytes;
+      const int k0 = c * kChunk;
+      const int k_left = c < chunks ? K - k0 : 0;
+#pragma unroll
+      for (int i = 0; i < kWLoads; ++i) {
+        constexpr int kParts = kChunk / 64;           // of a row
+        const int part = i % kParts, group = i / kParts;  // 8 rows
+        const int p = piece ^ (group & 1) << 2;
+        // SwiGLU: rows 0 .. 15 are the gate's, the others up's
+        const int n = SWIGLU ? group % 2 * 8 : group * 8;
+        const int have = there - n;
+        const uint8_t *base = w0 + (int64_t)(n + (SWIGLU ? group / 2 * out_cols : 0)) * w_pitch +
+                              (k0 + part * 64) * 2;
+        const int bytes = have <= 0 || k_left <= 0
+                              ? 0 : (have < 8 ? have : 8) * w_pitch - (k0 + part * 64) * 2;
+        const bool in = part * 64 + p * 8 < k_left;
+        load_to_lds(lds + i * 1024, in ? (uint32_t)(at_row * w_pitch + p * 16) : kNowhere,
+                    buffer_of(base, bytes < 0 ? 0 : bytes));
+      }
+#pragma unroll
+      for (int i = 0; i < kXLoads; ++i) {
+        const int p = piece ^ (i & 1) << 2, have = left - i * 8;
+        const uint8_t *base = x0 + (int64_t)i * 8 * x_pitch + k0 * (FP8 ? 1 : 2);
+        const int bytes = have <= 0 || k_left <= 0
+                              ? 0 : (have < 8 ? have : 8) * x_pitch - k0 * (FP8 ? 1 : 2);
+        const bool in = p * (FP8 ? 16 : 8) < k_left;
+        load_to_lds(lds + kWBytes + i * 1024, in ? (uint32_t)(at_row * x_pitch + p * 16) : kNowhere,
+                    buffer_of(base, bytes < 0 ? 0 : bytes));
+      }
+      if constexpr (FP8)
+        load_word_to_lds(lds + kWBytes + kXBytes, (lane * (uint32_t)(K / 128) + c) * 4,
+                         buffer_of(s0, k_left > 0 ? left * (K / 128) * 4 : 0));
+    };
+    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(wave + i * kStreamWaves, i);
+    int slot = 0;
+    for (int c = wave; c < chunks; c += kStreamWaves) {
+      issue(c + (kStages - 1) * kStreamWaves, slot == 0 ? kStages - 1 : slot - 1);
+      wait_loads<(kStages - 1) * kLoads>();
+      const uint8_t *here = stage[wave][slot];
+      // lane l16: row l16 of 16, eight columns from 32 ks + 8 quad on
+      const auto read = [&](int at, int ks) {
+        return *reinterpret_cast<const bf16x8 *>(
+            here + at + l16 * 128 + ((ks * 4 + quad) ^ (l16 >> 1)) * 16);
+      };
+      if constexpr (FP8) {
+        f32x4 part[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          // 16 codes are a piece
+          const u32x2 raw = *reinterpret_cast<const u32x2 *>(
+              here + kWBytes + l16 * 128 + ((ks * 2 + (quad >> 1)) ^ (l16 >> 1)) * 16 + (quad & 1) * 8);
+          const bf16x8 x = codes_bf16(raw);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            // rows 8 g .. + 7 of the weights: part 0 at 2048 g, part 1 1024 on
+            const bf16x8 w = *reinterpret_cast<const bf16x8 *>(
+                here + j * 4096 + (l16 >> 3) * 2048 + (ks >> 1) * 1024 + (l16 & 7) * 128 +
+                (((ks & 1) * 4 + quad) ^ (l16 >> 1)) * 16);
+            part[j] = mul(w, x, part[j]);
+          }
+        }
+        const float scale = *reinterpret_cast<const float *>(here + kWBytes + kXBytes + l16 * 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[j][v] = __builtin_fmaf(scale, part[j][v], acc[j][v]);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const bf16x8 x = read(kWBytes, ks);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[j] = mul(read(j * 2048, ks), x, acc[j]);
+        }
+      }
+      lds_done();  // the slot is free
+      slot = slot == kStages - 1 ? 0 : slot + 1;
+    }
+    // sums of the waves: [wave][row][column]
+    stage_barrier<0>();
+    float *sums = reinterpret_cast<float *>(&stage[0][0][0]);
+    constexpr int kPitch = kStreamCols + 4;
+    static_assert(kStreamWaves * kStreamRows * kPitch * 4 <= (int)sizeof(stage), "sums fit");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<f32x4 *>(sums + (wave * kStreamRows + l16) * kPitch + j * 16 + quad * 4) = acc[j];
+    __syncthreads();
+    for (int o = tid; o < kStreamRows * kOutCols; o += kStreamWaves * 64) {
+      const int m = o / kOutCols, n = o % kOutCols;
+      float y = 0.0f, up = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kStreamWaves; ++w) {
+        const float *p = sums + (w * kStreamRows + m) * kPitch + n;
+        y += p[0];
+        if (SWIGLU) up += p[kOutCols];
+      }
+      if (SWIGLU) y = silu_of(y) * up;
+      if (m < left && n < there)
+        static_cast<uint16_t *>(a.out)[(first + r0 + m) * out_cols + n0 + n] = f32_to_bf16(y);
+    }
+    __syncthreads();
+  }
+}
+
 #define EP_TRY(expr)                \
   do {                              \
     const ep_status_t st_ = (expr); \
@@ -1006,7 +1163,18 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
   a.out = out;
   a.out_any = !aligned_to(out, 16);
   const auto launch = [&](auto f, auto s) {
-    if (f.value || K % 8 == 0)
+    const int64_t columns = s.value ? N / 2 : N, tile_cols = s.value ? kTile / 2 : kTile;
+    const int64_t hit = capacity < experts->num_experts ? capacity : experts->num_experts;
+    const bool few = capacity <= kStreamRows ||
+                     (capacity <= 4 * kStreamRows &&
+                      hit * ((columns + tile_cols - 1) / tile_cols) < kTileWorkgroups);
+    if (few && (f.value || K % 8 == 0)) {
+      constexpr int kCols = s.value ? kStreamCols / 2 : kStreamCols;
+      hipLaunchKernelGGL((product_stream_kernel<f.value, s.value>),
+                         dim3((unsigned)((columns + kCols - 1) / kCols),
+                              (unsigned)experts->num_experts),
+                         dim3(kStreamWaves * 64), 0, stream, a);
+    } else if (f.value || K % 8 == 0)
       hipLaunchKernelGGL((product_tile_kernel<kProduct, f.value, s.value, uint16_t>),
                          dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
     else

@@ -95,7 +95,8 @@ SHAPES = [  # K, N, counts
     (1, 1, [1]), (8, 8, [1]), (33, 18, [3, 0]), (128, 40, [0, 1, 17]), (256, 130, [65, 1, 0, 64]),
     (1024, 100, [0, 7]), (640, 264, [33, 1, 0, 129, 2]), (384, 96, [9, 8, 7, 6, 5, 4, 3, 200]),
     (512, 520, [300]), (136, 1002, [257, 31]), (384, 512, [130, 256, 0, 511]), (72, 64, [16] * 9),
-    (1920, 256, [2, 4, 1, 15, 16, 17]), (2048, 24, [100, 31, 32, 33]), (904, 776, [64, 128, 192]),
+    (1920, 256, [2, 4, 1, 15, 16, 17]), (512, 128, [3, 0, 5]), (2176, 80, [1, 0, 0, 14]),
+    (896, 34, [16]), (640, 96, [0, 40, 9]), (136, 66, [2, 30, 1]), (2048, 24, [100, 31, 32, 33]), (904, 776, [64, 128, 192]),
 ]
 
 
