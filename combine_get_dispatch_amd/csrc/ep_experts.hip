@@ -437,18 +437,26 @@ struct Items {
 // results alone.
 __device__ __forceinline__ int across_swizzle(int l) { return (l & 3) | (l >> 3 & 1) << 2; }
 
-template <Kind KIND, bool FP8, bool SWIGLU, typename OUT>
-__global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(ProductArgs a) {
+// Of FP8 codes: 16-byte pieces, for 16 l of 32 lanes, lines of 256 or 128 bytes.
+__device__ __forceinline__ int across_swizzle8(int line, int l) {
+  return line == 256 ? l & 15 : l >> 1 & 7;
+}
+
+template <Kind KIND, bool FP8, bool SWIGLU, typename OUT, bool SMALL>
+__global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_kernel(
+    ProductArgs a) {
   constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
   // Which side is x in FP8.  Rows: codes enter the instructions exactly and the
   // scales are applied to the sums of 128, in accumulators of their own, for which
   // 128 rows leave the registers.  Columns (weights' gradient): x is rounded to
   // bf16, as the scales go by the rows that are summed over.
   constexpr bool kRows8 = KIND == kProduct && FP8, kCols8 = KIND == kWeightsGrad && FP8;
-  constexpr int kRowTile = kRows8 ? kTile / 2 : kTile;
-  constexpr int kOutTile = SWIGLU ? kTile / 2 : kTile;
+  constexpr int kRowTile = SMALL || kRows8 ? kTile / 2 : kTile;
+  constexpr int kColTile = SMALL ? kTile / 2 : kTile;
+  constexpr int kOutTile = SWIGLU ? kColTile / 2 : kColTile;
+  constexpr int kJ = kColTile / 64;  // 16 columns each, of a wave
   constexpr int kRowElem = kRows8 ? 1 : 2, kColElem = kCols8 ? 1 : 2;
-  constexpr int kRowBytes = kRowTile * kDepth * kRowElem, kColBytes = kTile * kDepth * kColElem;
+  constexpr int kRowBytes = kRowTile * kDepth * kRowElem, kColBytes = kColTile * kDepth * kColElem;
   constexpr int kRowLoads = kRowBytes / (kTileWaves * 1024);  // of a wave and stage
   constexpr int kColLoads = kColBytes / (kTileWaves * 1024);
   constexpr int kColPart = kColLoads + kCols8;  // with the scales
@@ -458,16 +466,18 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
       stage[kScalesAt + (FP8 ? (kColSlots + 1) * kScaleBytes : 0)];
   // non-temporal stores of the weights' gradient, which nobody reads soon (bf16, 32
   // experts of 4096 x 7168: 2056 us, without 2140)
-  constexpr int kOnceOut = KIND == kWeightsGrad ? 2 : 0;
+  constexpr int kOnceOut = KIND == kWeightsGrad && !SMALL ? 2 : 0;
   constexpr int kSize = sizeof(OUT);
-  constexpr int kStores = SWIGLU ? 2 : kSize * 2;  // of a wave, per 64 rows of a tile
+  constexpr int kHere = SWIGLU ? kJ / 2 : kJ;  // 16 columns of the results each
+  // stores of a wave, per 64 rows of a tile
+  constexpr int kStores = kSize == 4 ? 2 * kHere : kHere == 4 ? 4 : 2;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   const int wr = wave >> 2, wc = wave & 3;  // of the wave's rows and columns
   const int K = a.K, N = a.N;
   const int out_cols = KIND == kProduct ? (SWIGLU ? N / 2 : N) : K;
   typedef Items<KIND, kRowTile> AllItems;
-  AllItems items{a, (N + kTile - 1) / kTile, (out_cols + kOutTile - 1) / kOutTile};
+  AllItems items{a, (N + kRowTile - 1) / kRowTile, (out_cols + kOutTile - 1) / kOutTile};
   // The items of an XCD (workgroups id % 8) are consecutive, so that the
   // workgroups that share its L2 share rows and columns.
   const int64_t count = items.count(), per_xcd = (count + 7) / 8;
@@ -478,52 +488,61 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
   // Where a lane's 16 bytes of a side's first load come from, from the wave's
   // base on, and how far on each further load is.
   const int row_pitch = (KIND == kProduct ? K : N) * kRowElem, col_pitch = K * kColElem;
+  // Across, a row in LDS is one l.
+  constexpr int kRowLine = kRowTile * 2, kColLine = kColTile * kColElem;
+  constexpr int kRowPer = kRows8 ? 16 : kRowsAcross ? 1024 / kRowLine : 8;  // rows, or l, of a load
+  constexpr int kColPer = kColsAcross ? 1024 / kColLine : 8;
   const int piece_along = (lane & 7) ^ ((wave & 1) << 2 | lane >> 4);
-  const int piece_across = (lane & 31) ^ across_swizzle(wave * 2 + (lane >> 5)) << 1;
   const int piece_along8 = (lane & 3) ^ lane >> 4;
-  const int piece_across8 = l16 ^ ((wave & 3) << 2 | quad);
+  const auto across_from = [&](int line, int per, int pitch, bool codes) -> uint32_t {
+    const int l = lane / (line / 16), piece = lane % (line / 16), at = wave * per + l;
+    return l * pitch + (piece ^ (codes ? across_swizzle8(line, at) : across_swizzle(at) << 1)) * 16;
+  };
   const uint32_t row_off = kRows8        ? (lane >> 2) * row_pitch + piece_along8 * 16
-                           : kRowsAcross ? (lane >> 5) * row_pitch + piece_across * 16
+                           : kRowsAcross ? across_from(kRowLine, kRowPer, row_pitch, false)
                                          : (lane >> 3) * row_pitch + piece_along * 16;
-  const uint32_t col_off = kCols8        ? quad * col_pitch + piece_across8 * 16
-                           : kColsAcross ? (lane >> 5) * col_pitch + piece_across * 16
-                                         : (lane >> 3) * col_pitch + piece_along * 16;
-  const uint32_t row_step = (kRowsAcross ? 16 : 64) * row_pitch;
-  const uint32_t col_step = (kCols8 ? 32 : kColsAcross ? 16 : SWIGLU ? 32 : 64) * col_pitch;
-  constexpr int kRowPer = kRows8 ? 16 : kRowsAcross ? 2 : 8;  // rows, or l, of a load
-  constexpr int kColPer = kCols8 ? 4 : kColsAcross ? 2 : 8;
+  const uint32_t col_off = kColsAcross ? across_from(kColLine, kColPer, col_pitch, kCols8)
+                                       : (lane >> 3) * col_pitch + piece_along * 16;
+  const uint32_t row_step = (kRowsAcross ? 8 * kRowPer : 64) * row_pitch;
+  const uint32_t col_step = (kColsAcross ? 8 * kColPer : SWIGLU ? 32 : 64) * col_pitch;
 
   // Where a lane's parts of the instructions' operands are in a slot: of its
   // first 16 rows and columns.
   const int along = l16 * 128 + (quad ^ l16 >> 1) * 16;
-  const int across = (quad * 8 + l16 / 4) * 512 + ((quad & 1) << 2 | l16 / 4) * 32 + l16 % 4 * 8;
-  const int along8 = l16 * 64 + (quad >> 1 ^ l16 >> 2) * 16 + (quad & 1) * 8;
-  const int across8 = (quad * 8 + l16 / 2) * 256 + ((quad & 1) << 3 | l16 / 2) * 16 + l16 % 2 * 8;
-  const int row_at = kRowsAt + (kRows8        ? along8 + wr * 1024
-                                : kRowsAcross ? across ^ wr * 32
-                                              : along + wr * 2048);
-  const int col_at = kCols8 ? across8 ^ wc * 64 : kColsAcross ? across ^ wc * 128 : along + wc * 8192;
-  typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
-  const auto read_across = [&](int at) {
-    return read_transposed(stage + at, stage + at + 4 * 512);
+  const auto across = [&](int line) {
+    return (quad * 8 + l16 / 4) * line + ((quad & 1) << 2 | l16 / 4) * 32 + l16 % 4 * 8;
   };
-  // rows 32 f + 16 wr .. + 15, columns 64 wc + 16 j .. + 15, half ks of a stage
+  const int along8 = l16 * 64 + (quad >> 1 ^ l16 >> 2) * 16 + (quad & 1) * 8;
+  const int across8 = (quad * 8 + l16 / 2) * kColLine +
+                      across_swizzle8(kColLine, quad * 8 + l16 / 2) * 16 + l16 % 2 * 8;
+  const int row_at = kRowsAt + (kRows8        ? along8 + wr * 1024
+                                : kRowsAcross ? across(kRowLine) ^ wr * 32
+                                              : along + wr * 2048);
+  const int col_at = kCols8        ? across8 ^ wc * kJ * 16
+                     : kColsAcross ? across(kColLine) ^ wc * kJ * 32
+                                   : along + wc * kJ * 2048;
+  typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+  const auto read_across = [&](int at, int line) {
+    return read_transposed(stage + at, stage + at + 4 * line);
+  };
+  // rows 32 f + 16 wr .. + 15, columns 16 (kJ wc + j) .. + 15, half ks of a stage
   const auto read_row = [&](int slot, int ks, int f) {
     const int at = slot * kRowBytes + row_at;
     if constexpr (kRows8)
       return *reinterpret_cast<const u32x2 *>(stage + (at ^ ks * 32) + f * 2048);
     else if constexpr (kRowsAcross)
-      return read_across((at ^ f * 64) + ks * 32 * 512);
+      return read_across((at ^ f * 64) + ks * 32 * kRowLine, kRowLine);
     else
       return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 64) + f * 4096);
   };
   const auto read_col = [&](int slot, int ks, int j) {
     const int at = slot * kColBytes + col_at;
     if constexpr (kCols8)
-      return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                                           (lds_i32x2 *)(stage + (at ^ j * 16) + ks * 32 * 256)));
+      return __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                     (lds_i32x2 *)(stage + (at ^ j * 16) + ks * 32 * kColLine)));
     else if constexpr (kColsAcross)
-      return read_across((at ^ j * 32) + ks * 32 * 512);
+      return read_across((at ^ j * 32) + ks * 32 * kColLine, kColLine);
     else
       return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 64) + j * 2048);
   };
@@ -571,11 +590,11 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
                              (it.first + wave * kColPer) * (int64_t)col_pitch) +
                   cols.skip;
     } else {
-      // SwiGLU: 32 columns of the gate, then the same of up, for each wc
-      const int n = it.col0 + (SWIGLU ? wave % 4 * 8 : wave * 8);
+      // SwiGLU: 8 kJ columns of the gate, then the same of up, for each wc
+      const int n = it.col0 + (SWIGLU ? wave / (2 * kJ) * 8 * kJ + wave % kJ * 8 : wave * 8);
       const int there = out_cols - n < kTile ? out_cols - n : kTile;
       cols.base = reinterpret_cast<const uint8_t *>(a.w) +
-                  ((int64_t)it.e * N + n + (SWIGLU ? wave / 4 * out_cols : 0)) * col_pitch;
+                  ((int64_t)it.e * N + n + (SWIGLU ? wave / kJ % 2 * out_cols : 0)) * col_pitch;
       cols.bytes = there * col_pitch;
     }
     if (kCols8) {
@@ -681,31 +700,31 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
 
     const auto tile = [&](auto count) {
       constexpr int kM = decltype(count)::value;  // 64 rows each
-      f32x4 acc[2 * kM][4], part[kRows8 ? 2 * kM : 1][4];
+      f32x4 acc[2 * kM][kJ], part[kRows8 ? 2 * kM : 1][kJ];
 #pragma unroll
       for (int f = 0; f < 2 * kM; ++f)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
+        for (int j = 0; j < kJ; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
       typedef typename std::conditional<kRows8, u32x2, bf16x8>::type RowRaw;
       typedef typename std::conditional<kCols8, u32x2, bf16x8>::type ColRaw;
-      bf16x8 c[4];
-      ColRaw c_raw[2][4];
+      bf16x8 c[kJ];
+      ColRaw c_raw[2][kJ];
       RowRaw r[2][kM];
       f32x4 col_scale[2];          // of the lane's 8 l
       float row_scale[2][kM];
       const auto read_cols = [&](int slot, int ks) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c_raw[ks][j] = read_col(slot, ks, j);
+        for (int j = 0; j < kJ; ++j) c_raw[ks][j] = read_col(slot, ks, j);
         if constexpr (kCols8) {
           const f32x4 *s = reinterpret_cast<const f32x4 *>(
-              stage + kScalesAt + slot * kScaleBytes + (wc >> 1) * 256 + ks * 128 + quad * 32);
+              stage + kScalesAt + slot * kScaleBytes + wc * kJ / 8 * 256 + ks * 128 + quad * 32);
           col_scale[0] = s[0];
           col_scale[1] = s[1];
         }
       };
       const auto take_cols = [&](int ks) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kJ; ++j) {
           if constexpr (kCols8)
             c[j] = scaled_bf16(c_raw[ks][j], col_scale);
           else
@@ -726,7 +745,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
           else
             x = r[h][f];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < kJ; ++j) {
             if constexpr (kRows8)
               part[h * kM + f][j] =
                   mul(c[j], x, fresh ? f32x4{0, 0, 0, 0} : part[h * kM + f][j]);
@@ -741,7 +760,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
 #pragma unroll
         for (int f = 0; f < kM; ++f)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < kJ; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               acc[h * kM + f][j][v] = __builtin_fmaf(row_scale[h][f], part[h * kM + f][j][v],
@@ -808,7 +827,6 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
       // bytes per row the weights' gradient of 32 experts, 4096 x 7168, takes 2232
       // us instead of 2040; through LDS 2056).  Rows that are not there are outside
       // the buffer of the stores.
-      constexpr int kHere = SWIGLU ? 2 : 4;  // 16 columns each
       // rows of results that begin between 16-byte boundaries
       const bool any_store = KIND == kProduct && (out_cols % 8 != 0 || a.out_any);
       stored = steps > 0 && !any_store ? kStores * kM : 0;
@@ -837,7 +855,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
         const uint32_t down = f * 32 * pitch;
         if constexpr (kSize == 4) {
 #pragma unroll
-          for (int j = 0; j < 4; j += 2) {
+          for (int j = 0; j < kHere; j += 2) {
             u32x4 y[2] = {__builtin_bit_cast(u32x4, acc[f][j]),
                           __builtin_bit_cast(u32x4, acc[f][j + 1])};
             halve_rows(&y[0], &y[1]);
@@ -859,7 +877,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
             f32x4 y = acc[f][j];
             if constexpr (SWIGLU) {
 #pragma unroll
-              for (int v = 0; v < 4; ++v) y[v] = silu_of(y[v]) * acc[f][2 + j][v];
+              for (int v = 0; v < 4; ++v) y[v] = silu_of(y[v]) * acc[f][kJ / 2 + j][v];
             }
             if (KIND == kWeightsGrad && a.add != nullptr) {
               const u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(
@@ -871,39 +889,52 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void product_tile_kernel(Produc
             w[j][0] = pack_bf16(y[0], y[1]);
             w[j][1] = pack_bf16(y[2], y[3]);
           }
-          // lane quad (q1, q0) with 16 columns (j1, j0) becomes lane quad (j0, q1)
-          // with 8 columns q0 of piece j1
-          u32x4 v[kHere / 2];
+          if constexpr (kHere == 1) {
+            if (any_store) {
 #pragma unroll
-          for (int j = 0; j < kHere; j += 2)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const auto x = __builtin_amdgcn_permlane32_swap(w[j][p], w[j + 1][p], false, false);
-              const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
-              v[j / 2][p] = y[0];
-              v[j / 2][2 + p] = y[1];
+              for (int i = 0; i < 4; ++i)
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[0][i / 2] >> (i % 2 * 16)), out,
+                                                      from(row, at_quad * 4 + i) + down, 0, 0);
+            } else {
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{w[0][0], w[0][1]}, out,
+                                                    from(row, at_quad * 4) + down, 0, 0);
             }
-          if (KIND == kProduct && any_store) {
+          } else {
+            // lane quad (q1, q0) with 16 columns (j1, j0) becomes lane quad (j0, q1)
+            // with 8 columns q0 of piece j1
+            u32x4 v[kHere / 2];
 #pragma unroll
             for (int j = 0; j < kHere; j += 2)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                __builtin_amdgcn_raw_buffer_store_b16(
-                    (uint16_t)(v[j / 2][i / 2] >> (i % 2 * 16)), out,
-                    from(row, j * 16 + at_quad * 8 + i) + down, 0, 0);
-          } else if constexpr (SWIGLU) {
-            __builtin_amdgcn_raw_buffer_store_b128(v[0], out, from(row, at_quad * 8) + down, 0, 0);
-          } else {
-            halve_rows(&v[0], &v[1]);
+              for (int p = 0; p < 2; ++p) {
+                const auto x = __builtin_amdgcn_permlane32_swap(w[j][p], w[j + 1][p], false, false);
+                const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+                v[j / 2][p] = y[0];
+                v[j / 2][2 + p] = y[1];
+              }
+            if (any_store) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              __builtin_amdgcn_raw_buffer_store_b128(
-                  v[h], out, from(row8 + h * 8, second * 32 + at_quad * 8) + down, 0, kOnceOut);
+              for (int j = 0; j < kHere; j += 2)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  __builtin_amdgcn_raw_buffer_store_b16(
+                      (uint16_t)(v[j / 2][i / 2] >> (i % 2 * 16)), out,
+                      from(row, j * 16 + at_quad * 8 + i) + down, 0, 0);
+            } else if constexpr (kHere == 2) {
+              __builtin_amdgcn_raw_buffer_store_b128(v[0], out, from(row, at_quad * 8) + down, 0,
+                                                     kOnceOut);
+            } else {
+              halve_rows(&v[0], &v[1]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    v[h], out, from(row8 + h * 8, second * 32 + at_quad * 8) + down, 0, kOnceOut);
+            }
           }
         }
       }
     };
-    if constexpr (kRows8) {
+    if constexpr (kRowTile < kTile) {
       if (it.rows <= 64)
         tile(std::integral_constant<int, 1>{});
       else
@@ -1074,6 +1105,29 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
     if (st_ != EP_OK) return st_;   \
   } while (0)
 
+// Calls f with the tiles' size: 128 x 128, two workgroups per compute unit,
+// where tiles of 256 x 256 would leave half the chip idle (kSmallTiles).  Of the
+// experts' rows only the buffer's are known.
+//   SMALL_NOTE
+constexpr int64_t kSmallTiles = 160;
+
+template <typename F>
+void with_tiles(int64_t tiles, F f) {
+  if (tiles <= kSmallTiles)
+    f(std::true_type{}, dim3(2 * kTileWorkgroups));
+  else
+    f(std::false_type{}, dim3(kTileWorkgroups));
+}
+
+int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
+
+// Row tiles of a buffer's rows: an expert's last tile is half full.
+int64_t row_tiles_of(const ProductArgs &a) {
+  const int64_t hit = a.rows.capacity < a.rows.E ? a.rows.capacity : a.rows.E;
+  const int64_t n = a.rows.capacity / kTile + (hit + 1) / 2;
+  return n > hit ? n : hit;
+}
+
 // The checks that the three calls share.
 ep_status_t check_experts(const ep_experts_t *x, const int32_t *offsets, const int32_t *counts,
                           int64_t capacity) {
@@ -1174,10 +1228,12 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
                          dim3((unsigned)((columns + kCols - 1) / kCols),
                               (unsigned)experts->num_experts),
                          dim3(kStreamWaves * 64), 0, stream, a);
-    } else if (f.value || K % 8 == 0)
-      hipLaunchKernelGGL((product_tile_kernel<kProduct, f.value, s.value, uint16_t>),
-                         dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
-    else
+    } else if (f.value || K % 8 == 0) {
+      with_tiles(row_tiles_of(a) * tiles_of(N), [&](auto small, dim3 grid) {
+        hipLaunchKernelGGL((product_tile_kernel<kProduct, f.value, s.value, uint16_t, small.value>),
+                           grid, dim3(kTileWaves * 64), 0, stream, a);
+      });
+    } else
       hipLaunchKernelGGL((product_any_kernel<kProduct, false, s.value, uint16_t>),
                          dim3(kAnyGrid), dim3(256), 0, stream, a);
   };
@@ -1215,8 +1271,10 @@ ep_status_t ep_expert_product_backward_rows(const ep_experts_t *experts, const u
   a.grad = grad_out;
   a.out = grad_x;
   if (a.K % 8 == 0 && a.N % 8 == 0 && aligned_to(grad_x, 16))
-    hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, false, uint16_t>), dim3(kTileWorkgroups),
-                       dim3(kTileWaves * 64), 0, stream, a);
+    with_tiles(row_tiles_of(a) * tiles_of(a.K), [&](auto small, dim3 grid) {
+      hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, false, uint16_t, small.value>), grid,
+                         dim3(kTileWaves * 64), 0, stream, a);
+    });
   else
     hipLaunchKernelGGL((product_any_kernel<kRowsGrad, false, false, uint16_t>), dim3(kAnyGrid),
                        dim3(256), 0, stream, a);
@@ -1253,8 +1311,11 @@ ep_status_t ep_expert_product_backward_weights(
   const bool tiled = K % 8 == 0 && N % 8 == 0;
   const auto launch = [&](auto f, auto value) {
     if (tiled)
-      hipLaunchKernelGGL((product_tile_kernel<kWeightsGrad, f.value, false, decltype(value)>),
-                         dim3(kTileWorkgroups), dim3(kTileWaves * 64), 0, stream, a);
+      with_tiles(a.rows.E * tiles_of(N) * tiles_of(K), [&](auto small, dim3 grid) {
+        hipLaunchKernelGGL(
+            (product_tile_kernel<kWeightsGrad, f.value, false, decltype(value), small.value>), grid,
+            dim3(kTileWaves * 64), 0, stream, a);
+      });
     else
       hipLaunchKernelGGL((product_any_kernel<kWeightsGrad, f.value, false, decltype(value)>),
                          dim3(kAnyGrid), dim3(256), 0, stream, a);

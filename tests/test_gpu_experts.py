@@ -91,7 +91,17 @@ def check_rows(got, want, size, terms, exact):
     assert np.all(d[~dead] <= tol[~dead]), np.max((d / tol)[~dead])
 
 
+def many(seed, experts, *large):
+    """Experts enough for the large tiles: a few rows each, and some of many."""
+    rng = np.random.default_rng(seed)
+    c = rng.integers(0, 4, experts)
+    c[rng.choice(experts, len(large), replace=False)] = large
+    return [int(n) for n in c]
+
+
 SHAPES = [  # K, N, counts
+    (128, 80, many(1, 180, 513, 64, 65)), (264, 272, many(2, 190, 300, 129)),
+    (384, 48, many(3, 200, 255, 192, 128)), (72, 536, many(4, 170, 257, 700)),
     (1, 1, [1]), (8, 8, [1]), (33, 18, [3, 0]), (128, 40, [0, 1, 17]), (256, 130, [65, 1, 0, 64]),
     (1024, 100, [0, 7]), (640, 264, [33, 1, 0, 129, 2]), (384, 96, [9, 8, 7, 6, 5, 4, 3, 200]),
     (512, 520, [300]), (136, 1002, [257, 31]), (384, 512, [130, 256, 0, 511]), (72, 64, [16] * 9),
@@ -100,7 +110,12 @@ SHAPES = [  # K, N, counts
 ]
 
 
-@pytest.mark.parametrize("K,N,counts", SHAPES)
+def name(v):
+    """of a test's counts"""
+    return f"{len(v)}x{max(v)}" if isinstance(v, list) and len(v) > 12 else None
+
+
+@pytest.mark.parametrize("K,N,counts", SHAPES, ids=name)
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_product(K, N, counts, fp8, swiglu):
@@ -111,7 +126,7 @@ def test_product(K, N, counts, fp8, swiglu):
     rng = np.random.default_rng(K + N)
     off, cap = layout_of(counts, 2)
     for exact in (True, False):
-        say(f"product K={K} N={N} counts={counts} fp8={fp8} swiglu={swiglu} exact={exact}")
+        say(f"product K={K} N={N} counts={counts[:9]} fp8={fp8} swiglu={swiglu} exact={exact}")
         x, xs, xv = draw_x(rng, cap, K, fp8, exact, off, counts)
         wt, w = draw_w(rng, counts, N, K, exact)
         out = torch.full((cap, N // 2 if swiglu else N), 99.0, dtype=torch.bfloat16, device="cuda")
@@ -136,12 +151,13 @@ def test_product(K, N, counts, fp8, swiglu):
         assert np.all(np.abs(g - want)[~dead] <= tol[~dead])
 
 
-@pytest.mark.parametrize("K,N,counts", SHAPES + [(40, 33, [5, 70]), (1001, 131, [3, 129])])
+@pytest.mark.parametrize("K,N,counts", SHAPES + [(40, 33, [5, 70]), (1001, 131, [3, 129])],
+                         ids=name)
 def test_rows_gradient(K, N, counts):
     rng = np.random.default_rng(K + N + 1)
     off, cap = layout_of(counts, 1)
     for exact in (True, False):
-        say(f"rows' gradient K={K} N={N} counts={counts} exact={exact}")
+        say(f"rows' gradient K={K} N={N} counts={counts[:9]} exact={exact}")
         gv = draw_rows(rng, cap, N, exact)
         g = ref.to_bf16(only_experts(gv, off, counts)).cuda()
         wt, w = draw_w(rng, counts, N, K, exact)
@@ -150,7 +166,8 @@ def test_rows_gradient(K, N, counts):
         check_rows(out, *ref.rows_grad(gv, w, off, counts), N, exact)
 
 
-@pytest.mark.parametrize("K,N,counts", SHAPES + [(40, 33, [5, 70]), (1001, 131, [3, 129])])
+@pytest.mark.parametrize("K,N,counts", SHAPES + [(40, 33, [5, 70]), (1001, 131, [3, 129])],
+                         ids=name)
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("add", ["none", "apart", "in place"])
@@ -161,7 +178,7 @@ def test_weights_gradient(K, N, counts, fp8, dtype, add):
     off, cap = layout_of(counts, 3)
     E = len(counts)
     for exact in (True, False):
-        say(f"weights' gradient K={K} N={N} counts={counts} fp8={fp8} {dtype} add={add} "
+        say(f"weights' gradient K={K} N={N} counts={counts[:9]} fp8={fp8} {dtype} add={add} "
             f"exact={exact}")
         gv = draw_rows(rng, cap, N, exact)
         g = ref.to_bf16(only_experts(gv, off, counts)).cuda()
