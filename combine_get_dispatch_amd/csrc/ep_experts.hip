@@ -251,7 +251,6 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 // "Rows" is the side of m, "columns" that of n.  The matrix instruction takes
 // columns first, so that a lane's results are consecutive columns of one row.
 
-typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 256;            // rows and columns of a tile
 constexpr int kDepth = 64;            // of the sum, per stage
@@ -296,22 +295,13 @@ __device__ __forceinline__ bf16x8 codes_bf16(u32x2 codes) {
   return __builtin_bit_cast(bf16x8, w);
 }
 
-// Eight FP8 codes times their scales, rounded to bf16.
-__device__ __forceinline__ bf16x8 scaled_bf16(u32x2 codes, const f32x4 *scales) {
-  u32x4 w;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[i], false);
-    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[i], true);
-    w[2 * i] = pack_bf16(lo[0] * scales[i][0], lo[1] * scales[i][1]);
-    w[2 * i + 1] = pack_bf16(hi[0] * scales[i][2], hi[1] * scales[i][3]);
-  }
-  return __builtin_bit_cast(bf16x8, w);
-}
-
 template <int kLeft>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
 }
 
 __device__ __forceinline__ void lds_done() {
@@ -449,7 +439,9 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   // Which side is x in FP8.  Rows: codes enter the instructions exactly and the
   // scales are applied to the sums of 128, in accumulators of their own, for which
   // 128 rows leave the registers.  Columns (weights' gradient): x is rounded to
-  // bf16, as the scales go by the rows that are summed over.
+  // bf16, as the scales go by the rows that are summed over; each value once, a
+  // stage ahead, into a place that the instructions' operands are read from.
+  // (By each wave for itself, two of them the same values: 2500 us, so WIDE_US.)
   constexpr bool kRows8 = KIND == kProduct && FP8, kCols8 = KIND == kWeightsGrad && FP8;
   constexpr int kRowTile = SMALL || kRows8 ? kTile / 2 : kTile;
   constexpr int kColTile = SMALL ? kTile / 2 : kTile;
@@ -460,7 +452,8 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   constexpr int kRowLoads = kRowBytes / (kTileWaves * 1024);  // of a wave and stage
   constexpr int kColLoads = kColBytes / (kTileWaves * 1024);
   constexpr int kColPart = kColLoads + kCols8;  // with the scales
-  constexpr int kRowsAt = kColSlots * kColBytes, kScalesAt = kRowsAt + kRowSlots * kRowBytes;
+  constexpr int kRowsAt = kColSlots * kColBytes, kWideAt = kRowsAt + kRowSlots * kRowBytes;
+  constexpr int kScalesAt = kWideAt + (kCols8 ? kColTile * kDepth * 2 : 0);
   constexpr int kScaleBytes = 512;  // of a stage: 128 rows, or 64 of l for two blocks
   __shared__ __align__(1024) uint8_t
       stage[kScalesAt + (FP8 ? (kColSlots + 1) * kScaleBytes : 0)];
@@ -513,15 +506,12 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
     return (quad * 8 + l16 / 4) * line + ((quad & 1) << 2 | l16 / 4) * 32 + l16 % 4 * 8;
   };
   const int along8 = l16 * 64 + (quad >> 1 ^ l16 >> 2) * 16 + (quad & 1) * 8;
-  const int across8 = (quad * 8 + l16 / 2) * kColLine +
-                      across_swizzle8(kColLine, quad * 8 + l16 / 2) * 16 + l16 % 2 * 8;
   const int row_at = kRowsAt + (kRows8        ? along8 + wr * 1024
                                 : kRowsAcross ? across(kRowLine) ^ wr * 32
                                               : along + wr * 2048);
-  const int col_at = kCols8        ? across8 ^ wc * kJ * 16
-                     : kColsAcross ? across(kColLine) ^ wc * kJ * 32
-                                   : along + wc * kJ * 2048;
-  typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+  constexpr int kOperandLine = kColTile * 2;
+  const int col_at = kColsAcross ? (across(kOperandLine) ^ wc * kJ * 32) + (kCols8 ? kWideAt : 0)
+                                 : along + wc * kJ * 2048;
   const auto read_across = [&](int at, int line) {
     return read_transposed(stage + at, stage + at + 4 * line);
   };
@@ -536,20 +526,17 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
       return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 64) + f * 4096);
   };
   const auto read_col = [&](int slot, int ks, int j) {
-    const int at = slot * kColBytes + col_at;
-    if constexpr (kCols8)
-      return __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                     (lds_i32x2 *)(stage + (at ^ j * 16) + ks * 32 * kColLine)));
-    else if constexpr (kColsAcross)
-      return read_across((at ^ j * 32) + ks * 32 * kColLine, kColLine);
+    const int at = (kCols8 ? 0 : slot * kColBytes) + col_at;
+    if constexpr (kColsAcross)
+      return read_across((at ^ j * 32) + ks * 32 * kOperandLine, kOperandLine);
     else
       return *reinterpret_cast<const bf16x8 *>(stage + (at ^ ks * 64) + j * 2048);
   };
 
   // The loads run ahead of the products, through the items' ends: columns two
-  // stages ahead, in three slots, and rows one, in two.  (With two slots of both
-  // the decode share in bf16 takes 364 us, so 311.)
+  // stages ahead (FP8: three, one of them for the rounding), in three slots, and
+  // rows one, in two.  (With two slots of both the decode share in bf16 takes 364
+  // us, so 311.)
   struct Loads {
     const uint8_t *base = nullptr, *scales = nullptr;
     int bytes = 0;  // along: from the base to the last row's end
@@ -559,28 +546,33 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
     int there = 0;     // bytes of the next stage from the base on
     uint32_t off = 0;  // of this lane's first load
   };
-  Loads rows, next_rows, cols;
+  Loads rows, cols;
   const int64_t next = gridDim.x / 8;
-  int64_t load_item = from + blockIdx.x / 8;
-  AllItems load_items = items;
-  const auto start = [&]() {  // of the item that the columns are at
+  int64_t row_item = from + blockIdx.x / 8, col_item = row_item;
+  AllItems row_items = items, col_items = items;
+  const auto start_rows = [&]() {
     Item it;
-    load_items.get(load_item, &it, kOutTile);
-    cols.left = next_rows.left = it.length;
+    row_items.get(row_item, &it, kOutTile);
+    rows.left = it.length;
     if (kRowsAcross) {
-      next_rows.skip = it.row0 * 2;
-      next_rows.base = reinterpret_cast<const uint8_t *>(a.grad) +
-                       (it.first + wave * kRowPer) * (int64_t)row_pitch + next_rows.skip;
+      rows.skip = it.row0 * 2;
+      rows.base = reinterpret_cast<const uint8_t *>(a.grad) +
+                  (it.first + wave * kRowPer) * (int64_t)row_pitch + rows.skip;
     } else {
-      next_rows.base = static_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
-                       (it.first + it.row0 + wave * kRowPer) * (int64_t)row_pitch;
-      next_rows.bytes = (it.rows - wave * kRowPer) * row_pitch;
+      rows.base = static_cast<const uint8_t *>(KIND == kProduct ? a.x : a.grad) +
+                  (it.first + it.row0 + wave * kRowPer) * (int64_t)row_pitch;
+      rows.bytes = (it.rows - wave * kRowPer) * row_pitch;
     }
     if (kRows8) {
-      next_rows.scales = reinterpret_cast<const uint8_t *>(a.x_scales) +
-                         (it.first + it.row0) * (int64_t)(K / 128) * 4;
-      next_rows.scale_bytes = it.rows * (K / 128) * 4;
+      rows.scales = reinterpret_cast<const uint8_t *>(a.x_scales) +
+                    (it.first + it.row0) * (int64_t)(K / 128) * 4;
+      rows.scale_bytes = it.rows * (K / 128) * 4;
     }
+  };
+  const auto start_cols = [&]() {
+    Item it;
+    col_items.get(col_item, &it, kOutTile);
+    cols.left = it.length;
     if (kColsAcross) {
       cols.skip = it.col0 * kColElem;
       cols.base = (KIND == kRowsGrad
@@ -653,29 +645,68 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
     x->bytes -= kDepth * elem;
     x->left -= kDepth;
   };
-  const auto cols_on = [&]() {
-    on(&cols, kColsAcross, col_pitch, kColElem);
-    if (kCols8) cols.scales += (int64_t)kDepth * (K / 128) * 4;
-    while (cols.left <= 0 && load_item < to) {
-      load_item += next;
-      if (load_item < to) start();
+  // On to the next item that has a sum.
+  const auto find_cols = [&]() {
+    while (cols.left <= 0 && col_item < to) {
+      col_item += next;
+      if (col_item < to) start_cols();
     }
     see_cols();
   };
-  const auto rows_on = [&]() {  // after cols_on() of the same stage
-    on(&rows, kRowsAcross, row_pitch, kRowElem);
-    if (rows.left <= 0) rows = next_rows;
+  const auto find_rows = [&]() {
+    while (rows.left <= 0 && row_item < to) {
+      row_item += next;
+      if (row_item < to) start_rows();
+    }
     see_rows();
   };
+  const auto cols_on = [&]() {
+    on(&cols, kColsAcross, col_pitch, kColElem);
+    if (kCols8) cols.scales += (int64_t)kDepth * (K / 128) * 4;
+    find_cols();
+  };
+  const auto rows_on = [&]() {
+    on(&rows, kRowsAcross, row_pitch, kRowElem);
+    find_rows();
+  };
+  // FP8 columns: this thread's pieces of 16 codes of a stage, rounded to bf16 and
+  // put where the operands are read.
+  constexpr int kPieces = kColLine / 16, kMine = kCols8 ? kPieces / 8 : 1;
+  u32x4 wide[kMine][2];
+  const auto widen = [&](int slot) {
+    if constexpr (kCols8) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int l = wave * 8 + i * (64 / kPieces) + lane / kPieces, p = lane % kPieces;
+        const u32x4 codes = *reinterpret_cast<const u32x4 *>(
+            stage + slot * kColBytes + l * kColLine + (p ^ across_swizzle8(kColLine, l)) * 16);
+        const float scale = *reinterpret_cast<const float *>(
+            stage + kScalesAt + slot * kScaleBytes + p / 8 * 256 + l * 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          wide[i][h] = scaled_bf16(u32x2{codes[2 * h], codes[2 * h + 1]}, scale);
+      }
+    }
+  };
+  const auto put_wide = [&]() {
+    if constexpr (kCols8) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int l = wave * 8 + i * (64 / kPieces) + lane / kPieces, p = lane % kPieces;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<u32x4 *>(stage + kWideAt + l * kOperandLine +
+                                     (p ^ across_swizzle(l)) * 32 + h * 16) = wide[i][h];
+      }
+    }
+  };
 
-  if (load_item < to) start();
-  while (cols.left <= 0 && load_item < to) {  // to the first item that has a sum
-    load_item += next;
-    if (load_item < to) start();
+  if (col_item < to) {
+    start_cols();
+    start_rows();
   }
-  rows = next_rows;
-  see_cols();
-  see_rows();
+  find_cols();
+  find_rows();
 #pragma unroll
   for (int i = 0; i < kColLoads; ++i) load_cols(0, i);
   cols_on();
@@ -685,7 +716,17 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
 #pragma unroll
   for (int i = 0; i < kColLoads; ++i) load_cols(1, i);
   cols_on();
-  stage_barrier<kColPart>();
+  if constexpr (kCols8) {
+#pragma unroll
+    for (int i = 0; i < kColLoads; ++i) load_cols(2, i);
+    cols_on();
+    stage_barrier<kColPart>();
+    widen(0);
+    put_wide();
+    lds_barrier();
+  } else {
+    stage_barrier<kColPart>();
+  }
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) load_rows(1, i);
   rows_on();
@@ -706,36 +747,18 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
 #pragma unroll
         for (int j = 0; j < kJ; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
       typedef typename std::conditional<kRows8, u32x2, bf16x8>::type RowRaw;
-      typedef typename std::conditional<kCols8, u32x2, bf16x8>::type ColRaw;
-      bf16x8 c[kJ];
-      ColRaw c_raw[2][kJ];
+      bf16x8 c[2][kJ];
       RowRaw r[2][kM];
-      f32x4 col_scale[2];          // of the lane's 8 l
       float row_scale[2][kM];
       const auto read_cols = [&](int slot, int ks) {
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) c_raw[ks][j] = read_col(slot, ks, j);
-        if constexpr (kCols8) {
-          const f32x4 *s = reinterpret_cast<const f32x4 *>(
-              stage + kScalesAt + slot * kScaleBytes + wc * kJ / 8 * 256 + ks * 128 + quad * 32);
-          col_scale[0] = s[0];
-          col_scale[1] = s[1];
-        }
-      };
-      const auto take_cols = [&](int ks) {
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          if constexpr (kCols8)
-            c[j] = scaled_bf16(c_raw[ks][j], col_scale);
-          else
-            c[j] = c_raw[ks][j];
-        }
+        for (int j = 0; j < kJ; ++j) c[ks][j] = read_col(slot, ks, j);
       };
       const auto read_rows = [&](int slot, int ks, int h) {
 #pragma unroll
         for (int f = 0; f < kM; ++f) r[h][f] = read_row(slot, ks, h * kM + f);
       };
-      const auto products = [&](bool fresh, int h, auto loads, auto load_one) {
+      const auto products = [&](bool fresh, int ks, int h, auto loads, auto load_one) {
         constexpr int kCount = decltype(loads)::value;
 #pragma unroll
         for (int f = 0; f < kM; ++f) {
@@ -748,9 +771,9 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
           for (int j = 0; j < kJ; ++j) {
             if constexpr (kRows8)
               part[h * kM + f][j] =
-                  mul(c[j], x, fresh ? f32x4{0, 0, 0, 0} : part[h * kM + f][j]);
+                  mul(c[ks][j], x, fresh ? f32x4{0, 0, 0, 0} : part[h * kM + f][j]);
             else
-              acc[h * kM + f][j] = mul(c[j], x, acc[h * kM + f][j]);
+              acc[h * kM + f][j] = mul(c[ks][j], x, acc[h * kM + f][j]);
           }
 #pragma unroll
           for (int i = f * kCount / kM; i < (f + 1) * kCount / kM; ++i) load_one(i);
@@ -778,14 +801,16 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
         constexpr bool kSecond = decltype(second)::value, kFresh = !kSecond;
         constexpr int kEarly = (kColLoads + 1) / 2;
         const int next_col = col_slot == 2 ? 0 : col_slot + 1;
-        const int free_col = col_slot == 0 ? 2 : col_slot - 1;  // of the stage before
+        // the next columns go where the last stage's were, or, as FP8 columns have
+        // been put elsewhere, this one's
+        const int free_col = kCols8 ? col_slot : col_slot == 0 ? 2 : col_slot - 1;
         read_rows(row_slot, 0, 1);
-        take_cols(0);
-        products(kFresh, 0, std::integral_constant<int, kEarly>{},
+        products(kFresh, 0, 0, std::integral_constant<int, kEarly>{},
                  [&](int i) { load_cols(free_col, i); });
         read_cols(col_slot, 1);
         read_rows(row_slot, 1, 0);
-        products(kFresh, 1, std::integral_constant<int, kColLoads - kEarly>{},
+        widen(next_col);
+        products(kFresh, 0, 1, std::integral_constant<int, kColLoads - kEarly>{},
                  [&](int i) { load_cols(free_col, i + kEarly); });
         cols_on();
         read_rows(row_slot, 1, 1);
@@ -795,17 +820,25 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
             row_scale[f / kM][f % kM] = *reinterpret_cast<const float *>(
                 stage + kScalesAt + row_slot * kScaleBytes + (f * 32 + wr * 16 + l16) * 4);
         }
-        take_cols(1);
-        products(false, 0, none, nothing);
+        products(false, 1, 0, none, nothing);
         // the next stage is there, and this one's slots are free
         if (s == 0 && stored == kStores * (kRowTile / 64))
           stage_barrier<kColPart + kStores * (kRowTile / 64)>();
         else
           stage_barrier<kColPart>();
-        read_cols(next_col, 0);
-        read_rows(row_slot ^ 1, 0, 0);
-        products(false, 1, std::integral_constant<int, kRowLoads>{},
-                 [&](int i) { load_rows(row_slot, i); });
+        if constexpr (kCols8) {
+          put_wide();
+          products(false, 1, 1, std::integral_constant<int, kRowLoads>{},
+                   [&](int i) { load_rows(row_slot, i); });
+          lds_barrier();
+          read_cols(next_col, 0);
+          read_rows(row_slot ^ 1, 0, 0);
+        } else {
+          read_cols(next_col, 0);
+          read_rows(row_slot ^ 1, 0, 0);
+          products(false, 1, 1, std::integral_constant<int, kRowLoads>{},
+                   [&](int i) { load_rows(row_slot, i); });
+        }
         rows_on();
         if constexpr (kRows8 && kSecond) {
           add_scaled(0);
