@@ -60,7 +60,7 @@ __device__ __forceinline__ void store_bf16(uint16_t *p, int n, const float *y) {
   u32x4 v;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v[i] = f32_to_bf16(y[2 * i]) | (uint32_t)f32_to_bf16(y[2 * i + 1]) << 16;
+    v[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
   if (n >= 8) {
     reinterpret_cast<Any16 *>(p)->v = v;
     return;

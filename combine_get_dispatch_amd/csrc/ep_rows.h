@@ -23,6 +23,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// Two of them, by one instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // 1 / (1 + exp(-y)) and 1 minus it, by exp(-|y|): neither loses bits where it
