@@ -345,7 +345,7 @@ struct Item {
 // row tiles that take the columns one after the other.  A wave finds its items
 // in ascending order by itself: it holds the row tiles of 64 experts, one per
 // lane, and goes on to the next 64 when it is past them.
-template <Kind KIND, int kRowTile>
+template <Kind KIND, int kRowTile, typename OUT>
 struct Items {
   const ProductArgs &a;
   int row_tiles, col_tiles;  // of the weights' gradient; of all kinds
@@ -353,22 +353,70 @@ struct Items {
   int32_t before = 0, end = 0;     // row tiles before the chunk's, and through it
   int32_t first_tile = 0, tiles = 0;  // of this lane's expert
 
-  __device__ __forceinline__ int lane_tiles(int c) const {
+  __device__ __forceinline__ int64_t lane_rows(int c) const {  // of expert 64 c + lane
     const int e = c * 64 + (threadIdx.x & 63);
     int64_t first, rows = 0;
     if (e < a.rows.E)
       rows_inside(a.rows.offsets[e], a.rows.counts[e], a.rows.capacity, &first, &rows);
-    return (int)((rows + kRowTile - 1) / kRowTile);
+    return rows;
   }
-  __device__ __forceinline__ int64_t count() const {
-    if (KIND == kWeightsGrad) return (int64_t)a.rows.E * row_tiles * col_tiles;
-    int total = 0;
-    for (int c = 0; c * 64 < a.rows.E; ++c) total += lane_tiles(c);
+  __device__ __forceinline__ int lane_tiles(int c) const {
+    return (int)((lane_rows(c) + kRowTile - 1) / kRowTile);
+  }
+  static __device__ __forceinline__ uint32_t scan(uint32_t v) {  // of the lanes up to this one
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
-    return (int64_t)uniform(total) * col_tiles;
+    for (int d = 1; d < 64; d *= 2) {
+      const uint32_t up = (uint32_t)__shfl_up((int)v, d);
+      v += (int)(threadIdx.x & 63) >= d ? up : 0;
+    }
+    return v;
   }
-  // item is less than count(), and not less than at the call before
+  static __device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, l);
+  }
+  // The first items of an XCD and of the next one.  An item of the products costs
+  // about the same whatever its rows, as its columns are loaded all the same:
+  // eighths of the items.  (By rows the prefill share in FP8 takes 515 us, so 450.)
+  // An item of the weights' gradient goes by its expert's rows: eighths of the
+  // steps, with the end of an item by what it loads and stores.  (32 experts whose
+  // rows differ by a third, 4096 x 7168: 1796 us, by items 1914; FP8 rows 2067,
+  // 2303; fp32 added up, 8 experts of 2048 x 7168: 252, 269.)
+  __device__ __forceinline__ void eighth(int part, int64_t *from, int64_t *to) const {
+    const int lane = threadIdx.x & 63;
+    if constexpr (KIND != kWeightsGrad) {
+      uint32_t tiles = 0;
+      for (int c = 0; c * 64 < a.rows.E; ++c) tiles += lane_tiles(c);
+      const int64_t all = (int64_t)lane_of(scan(tiles), 63) * col_tiles, per = (all + 7) / 8;
+      *from = part * per < all ? part * per : all;
+      *to = *from + per < all ? *from + per : all;
+    } else {
+      const uint32_t end = (sizeof(OUT) == 4 ? 6 : 4) * (a.add != nullptr ? 2 : 1);
+      const auto cost = [&](int c) -> uint32_t {
+        return c * 64 + lane < a.rows.E ? (uint32_t)((lane_rows(c) + 63) / 64) + end : 0;
+      };
+      uint32_t all = 0;
+      for (int c = 0; c * 64 < a.rows.E; ++c) all += cost(c);
+      all = lane_of(scan(all), 63);
+      const int64_t items = (int64_t)row_tiles * col_tiles;  // of an expert
+      const uint64_t p0 = (uint64_t)all * part / 8, p1 = (uint64_t)all * (part + 1) / 8;
+      *from = *to = a.rows.E * items;
+      uint32_t before_chunk = 0;
+      for (int c = 0; c * 64 < a.rows.E; ++c) {
+        const uint32_t w = cost(c), through = before_chunk + scan(w), w0 = through - w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t p = i == 0 ? p0 : p1;
+          const uint64_t here = __ballot(w0 <= p && p < through);
+          if (here == 0) continue;
+          const int l = __builtin_ctzll(here);
+          *(i == 0 ? from : to) =
+              (c * 64 + l) * items + (int64_t)(p - lane_of(w0, l)) * items / lane_of(w, l);
+        }
+        before_chunk = lane_of(through, 63);
+      }
+    }
+  }
+  // item is one of them, and not less than at the call before
   __device__ __forceinline__ void get(int64_t item, Item *it, int out_cols_per_tile) {
     const int32_t block = uniform((int)(item / col_tiles));  // as if rows came first
     int e, high, start;
@@ -465,13 +513,12 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   const int wr = wave >> 2, wc = wave & 3;  // of the wave's rows and columns
   const int K = a.K, N = a.N;
   const int out_cols = KIND == kProduct ? (SWIGLU ? N / 2 : N) : K;
-  typedef Items<KIND, kRowTile> AllItems;
+  typedef Items<KIND, kRowTile, OUT> AllItems;
   AllItems items{a, (N + kRowTile - 1) / kRowTile, (out_cols + kOutTile - 1) / kOutTile};
   // The items of an XCD (workgroups id % 8) are consecutive, so that the
   // workgroups that share its L2 share rows and columns.
-  const int64_t count = items.count(), per_xcd = (count + 7) / 8;
-  const int64_t from = (blockIdx.x % 8) * per_xcd;
-  const int64_t to = from + per_xcd < count ? from + per_xcd : count;
+  int64_t from, to;
+  items.eighth(blockIdx.x % 8, &from, &to);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_byte *)stage;
 
   // Where a lane's 16 bytes of a side's first load come from, from the wave's
