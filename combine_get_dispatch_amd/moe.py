@@ -252,14 +252,20 @@ def _product(w4, ref, x, x_scales, weights, expert_offsets, num_tokens_per_exper
 
 def _expert_rows(t, cols, name):
     """Rows of a tensor [capacity, cols]."""
-    if t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {cols})")
-    return t.shape[0]
+    s = t.shape
+    if len(s) != 2 or s[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(s)}, expected (rows, {cols})")
+    return s[0]
 
 
-def _at_least(t, rows, cols, name):
-    if t is not None and (t.dim() != 2 or t.shape[1] != cols or t.shape[0] < rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (>= {rows}, {cols})")
+def _rows_at(t, dev, dtype, rows, cols, name):
+    """Device pointer of a contiguous tensor of at least these rows; None passes NULL."""
+    if t is None:
+        return None
+    s = t.shape
+    if len(s) != 2 or s[1] != cols or s[0] < rows:
+        raise ValueError(f"{name} has shape {tuple(s)}, expected (>= {rows}, {cols})")
+    return _at(t, dev, dtype, s, name)
 
 
 def _expert_at(expert_offsets, num_tokens_per_expert, E, d):
@@ -278,9 +284,9 @@ def _x_at(x, x_scales, K, d):
     """Type and pointers of bf16 rows, or of E4M3 codes and their scales."""
     import torch
 
-    fp8 = x_scales is not None
-    return (EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16,
-            _at(x, d, torch.uint8 if fp8 else torch.bfloat16, None, "x"),
+    if x_scales is None:
+        return EP_DTYPE_BF16, _at(x, d, torch.bfloat16, None, "x"), None
+    return (EP_DTYPE_FP8_E4M3, _at(x, d, torch.uint8, None, "x"),
             _at(x_scales, d, torch.float32, (x.shape[0], K // 128), "x_scales"))
 
 
@@ -288,36 +294,65 @@ def _weight_shape(experts):
     return experts.num_experts, experts.out_features, experts.in_features
 
 
+def _weights_at(w, experts):
+    """Their device, and the pointer."""
+    import torch
+
+    d = _device(w, "w")
+    return d, _at(w, d, torch.bfloat16, _weight_shape(experts), "w")
+
+
+def _here(t, name, other, what):
+    """The device of a call whose weights or checkpoint are on `other`."""
+    d = _device(t, name)
+    if d != other:
+        raise ValueError(f"{what} not on the current device")
+    return d
+
+
 def ep_expert_product(experts: ep_experts_t, x, x_scales, w, swiglu, expert_offsets,
                       num_tokens_per_expert, out, stream=None):
     """x: bf16 [capacity, K], or uint8 E4M3 codes with x_scales."""
+    _device(x, "x")
+    _expert_product(experts, ctypes.byref(experts), x, x_scales, _weights_at(w, experts),
+                    1 if swiglu else 0, expert_offsets, num_tokens_per_expert, out, stream)
+
+
+def _expert_product(experts, ref, x, x_scales, w, swiglu, expert_offsets, num_tokens_per_expert,
+                    out, stream):
     import torch
 
     K, N = experts.in_features, experts.out_features
     cap = _expert_rows(x, K, "x")
-    _at_least(out, cap, N // 2 if swiglu else N, "out")
-    d = _device(x, "x")
+    d = _here(x, "x", w[0], "the weights are")
     st = lib().ep_expert_product(
-        ctypes.byref(experts), *_x_at(x, x_scales, K, d),
-        _at(w, d, torch.bfloat16, _weight_shape(experts), "w"), 1 if swiglu else 0,
+        ref, *_x_at(x, x_scales, K, d), w[1], swiglu,
         *_expert_at(expert_offsets, num_tokens_per_expert, experts.num_experts, d), cap,
-        _at(out, d, torch.bfloat16, None, "out"), _stream(stream))
-    _check(st, "ep_expert_product")
+        _rows_at(out, d, torch.bfloat16, cap, N // 2 if swiglu else N, "out"), _stream(stream))
+    if st:
+        _check(st, "ep_expert_product")
 
 
 def ep_expert_product_backward_rows(experts: ep_experts_t, grad_out, w, expert_offsets,
                                     num_tokens_per_expert, grad_x, stream=None):
+    _device(grad_out, "grad_out")
+    _backward_rows(experts, ctypes.byref(experts), grad_out, _weights_at(w, experts),
+                   expert_offsets, num_tokens_per_expert, grad_x, stream)
+
+
+def _backward_rows(experts, ref, grad_out, w, expert_offsets, num_tokens_per_expert, grad_x,
+                   stream):
     import torch
 
-    cap = _expert_rows(grad_out, experts.out_features, "grad_out")
-    _at_least(grad_x, cap, experts.in_features, "grad_x")
-    d = _device(grad_out, "grad_out")
+    N = experts.out_features
+    cap = _expert_rows(grad_out, N, "grad_out")
+    d = _here(grad_out, "grad_out", w[0], "the weights are")
     st = lib().ep_expert_product_backward_rows(
-        ctypes.byref(experts), _at(grad_out, d, torch.bfloat16, None, "grad_out"),
-        _at(w, d, torch.bfloat16, _weight_shape(experts), "w"),
+        ref, _at(grad_out, d, torch.bfloat16, None, "grad_out"), w[1],
         *_expert_at(expert_offsets, num_tokens_per_expert, experts.num_experts, d), cap,
-        _at(grad_x, d, torch.bfloat16, None, "grad_x"), _stream(stream))
-    _check(st, "ep_expert_product_backward_rows")
+        _rows_at(grad_x, d, torch.bfloat16, cap, experts.in_features, "grad_x"), _stream(stream))
+    if st:
+        _check(st, "ep_expert_product_backward_rows")
 
 
 def ep_expert_product_backward_weights(experts: ep_experts_t, x, x_scales, grad_out,
@@ -331,58 +366,82 @@ def ep_expert_product_backward_weights(experts: ep_experts_t, x, x_scales, grad_
     cap = _expert_rows(grad_out, N, "grad_out")
     if _expert_rows(x, K, "x") != cap:
         raise ValueError(f"x has {x.shape[0]} rows, grad_out {cap}")
-    if grad_w.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"grad_w must be float32 or bfloat16, not {grad_w.dtype}")
+    dtype = grad_w.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"grad_w must be float32 or bfloat16, not {dtype}")
     d, shape = _device(grad_out, "grad_out"), _weight_shape(experts)
     st = lib().ep_expert_product_backward_weights(
         ctypes.byref(experts), *_x_at(x, x_scales, K, d),
         _at(grad_out, d, torch.bfloat16, None, "grad_out"),
         *_expert_at(expert_offsets, num_tokens_per_expert, experts.num_experts, d), cap,
-        EP_DTYPE_F32 if grad_w.dtype == torch.float32 else EP_DTYPE_BF16,
-        _at(add, d, grad_w.dtype, shape, "add"), _at(grad_w, d, grad_w.dtype, shape, "grad_w"),
+        EP_DTYPE_F32 if dtype is torch.float32 else EP_DTYPE_BF16,
+        _at(add, d, dtype, shape, "add"), _at(grad_w, d, dtype, shape, "grad_w"),
         _stream(stream))
-    _check(st, "ep_expert_product_backward_weights")
+    if st:
+        _check(st, "ep_expert_product_backward_weights")
 
 
 def _checkpoint_shape(cap, features):
     return cap, 2 * -(-features // 128)
 
 
+def _checkpoint_at(codes, scales, features):
+    """Their device, rows and pointers."""
+    import torch
+
+    rows = _expert_rows(codes, 2 * features, "codes")
+    if scales.shape[0] < rows:
+        rows = scales.shape[0]
+    d = _device(codes, "codes")
+    return (d, rows, _at(codes, d, torch.uint8, None, "codes"),
+            _rows_at(scales, d, torch.float32, 0, _checkpoint_shape(0, features)[1], "scales"))
+
+
 def ep_swiglu_checkpoint(num_experts, features, gate_up, expert_offsets, num_tokens_per_expert, h,
                          codes, scales, stream=None):
+    _device(gate_up, "gate_up")
+    _save(num_experts, features, gate_up, expert_offsets, num_tokens_per_expert, h,
+          _checkpoint_at(codes, scales, features), stream)
+
+
+def _save(num_experts, features, gate_up, expert_offsets, num_tokens_per_expert, h, kept, stream):
     import torch
 
     cap = _expert_rows(gate_up, 2 * features, "gate_up")
-    for t, cols, name in ((h, features, "h"), (codes, 2 * features, "codes"),
-                          (scales, _checkpoint_shape(cap, features)[1], "scales")):
-        _at_least(t, cap, cols, name)
-    d = _device(gate_up, "gate_up")
+    if kept[1] < cap:
+        raise ValueError(f"gate_up has {cap} rows, the checkpoint {kept[1]}")
+    d = _here(gate_up, "gate_up", kept[0], "the checkpoint is")
     st = lib().ep_swiglu_checkpoint(
-        int(num_experts), int(features), _at(gate_up, d, torch.bfloat16, None, "gate_up"),
+        num_experts, features, _at(gate_up, d, torch.bfloat16, None, "gate_up"),
         *_expert_at(expert_offsets, num_tokens_per_expert, num_experts, d), cap,
-        _at(h, d, torch.bfloat16, None, "h"), _at(codes, d, torch.uint8, None, "codes"),
-        _at(scales, d, torch.float32, None, "scales"), _stream(stream))
-    _check(st, "ep_swiglu_checkpoint")
+        _rows_at(h, d, torch.bfloat16, cap, features, "h"), kept[2], kept[3], _stream(stream))
+    if st:
+        _check(st, "ep_swiglu_checkpoint")
 
 
 def ep_swiglu_checkpoint_backward(num_experts, features, codes, scales, grad_h, expert_offsets,
                                   num_tokens_per_expert, grad_gate_up, h, stream=None):
+    _device(grad_h, "grad_h")
+    _use(num_experts, features, _checkpoint_at(codes, scales, features), grad_h, expert_offsets,
+         num_tokens_per_expert, grad_gate_up, h, stream)
+
+
+def _use(num_experts, features, kept, grad_h, expert_offsets, num_tokens_per_expert, grad_gate_up,
+         h, stream):
     import torch
 
     cap = _expert_rows(grad_h, features, "grad_h")
-    for t, cols, name in ((h, features, "h"), (grad_gate_up, 2 * features, "grad_gate_up"),
-                          (codes, 2 * features, "codes"),
-                          (scales, _checkpoint_shape(cap, features)[1], "scales")):
-        _at_least(t, cap, cols, name)
-    d = _device(grad_h, "grad_h")
+    if kept[1] < cap:
+        raise ValueError(f"grad_h has {cap} rows, the checkpoint {kept[1]}")
+    d = _here(grad_h, "grad_h", kept[0], "the checkpoint is")
     st = lib().ep_swiglu_checkpoint_backward(
-        int(num_experts), int(features), _at(codes, d, torch.uint8, None, "codes"),
-        _at(scales, d, torch.float32, None, "scales"),
+        num_experts, features, kept[2], kept[3],
         _at(grad_h, d, torch.bfloat16, None, "grad_h"),
         *_expert_at(expert_offsets, num_tokens_per_expert, num_experts, d), cap,
-        _at(grad_gate_up, d, torch.bfloat16, None, "grad_gate_up"),
-        _at(h, d, torch.bfloat16, None, "h"), _stream(stream))
-    _check(st, "ep_swiglu_checkpoint_backward")
+        _rows_at(grad_gate_up, d, torch.bfloat16, cap, 2 * features, "grad_gate_up"),
+        _rows_at(h, d, torch.bfloat16, cap, features, "h"), _stream(stream))
+    if st:
+        _check(st, "ep_swiglu_checkpoint_backward")
 
 
 class EpRouter:
@@ -541,16 +600,25 @@ class Bf16Experts:
     are the gate's, then the up projection's, and ``product`` gives
     silu(gate) * up; the gradients are those of the plain product (gate and
     up), which an object without swiglu on the same weights gives.  The
-    weights are read in place at each call."""
+    weights are read in place at each call, and may be rewritten in place;
+    other tensors are another Bf16Experts."""
 
     def __init__(self, weights, swiglu=False):
         import torch
 
         if weights.dim() != 3 or weights.dtype != torch.bfloat16:
             raise ValueError("weights must be bf16 [experts, out_features, in_features]")
-        self.weights, self.swiglu = weights, bool(swiglu)
+        if not weights.is_contiguous():
+            raise ValueError("weights must be contiguous")
+        self._weights, self.swiglu = weights, bool(swiglu)
         E, N, K = weights.shape
         self.cfg = ep_experts_t(E, K, N)
+        self._ref = ctypes.byref(self.cfg)
+        self._at = weights.get_device(), weights.data_ptr()
+
+    @property
+    def weights(self):
+        return self._weights
 
     def product(self, x, x_scales, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, out_features] (half of them with swiglu): each expert's
@@ -562,8 +630,8 @@ class Bf16Experts:
         if out is None:
             N = self.cfg.out_features // (2 if self.swiglu else 1)
             out = _empty(stream, (x.shape[0], N), dtype=torch.bfloat16, device=x.device)
-        ep_expert_product(self.cfg, x, x_scales, self.weights, self.swiglu, expert_offsets,
-                          num_tokens_per_expert, out, stream=stream)
+        _expert_product(self.cfg, self._ref, x, x_scales, self._at, 1 if self.swiglu else 0,
+                        expert_offsets, num_tokens_per_expert, out, stream)
         return out
 
     def backward_rows(self, grad_out, expert_offsets, num_tokens_per_expert, out=None,
@@ -574,8 +642,8 @@ class Bf16Experts:
         if out is None:
             out = _empty(stream, (grad_out.shape[0], self.cfg.in_features), dtype=torch.bfloat16,
                          device=grad_out.device)
-        ep_expert_product_backward_rows(self.cfg, grad_out, self.weights, expert_offsets,
-                                        num_tokens_per_expert, out, stream=stream)
+        _backward_rows(self.cfg, self._ref, grad_out, self._at, expert_offsets,
+                       num_tokens_per_expert, out, stream)
         return out
 
     def backward_weights(self, x, x_scales, grad_out, expert_offsets, num_tokens_per_expert,
@@ -586,7 +654,7 @@ class Bf16Experts:
 
         if out is None:
             dtype = dtype or (torch.bfloat16 if add is None else add.dtype)
-            out = _empty(stream, tuple(self.weights.shape), dtype=dtype,
+            out = _empty(stream, tuple(self._weights.shape), dtype=dtype,
                          device=grad_out.device)
         ep_expert_product_backward_weights(self.cfg, x, x_scales, grad_out, expert_offsets,
                                            num_tokens_per_expert, add, out, stream=stream)
@@ -605,10 +673,20 @@ class SwigluCheckpoint:
         dev = torch.device(device)
         self.capacity, self.features = int(capacity), int(features)
         self.num_experts = int(num_experts)
-        self.codes = torch.empty((self.capacity, 2 * self.features), dtype=torch.uint8,
-                                 device=dev)
-        self.scales = torch.empty(_checkpoint_shape(self.capacity, self.features),
-                                  dtype=torch.float32, device=dev)
+        self._codes = torch.empty((self.capacity, 2 * self.features), dtype=torch.uint8,
+                                  device=dev)
+        self._scales = torch.empty(_checkpoint_shape(self.capacity, self.features),
+                                   dtype=torch.float32, device=dev)
+        self._kept = (self._codes.get_device(), self.capacity, self._codes.data_ptr(),
+                      self._scales.data_ptr())
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @property
+    def scales(self):
+        return self._scales
 
     def save(self, gate_up, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, features]: silu(gate) * up; keeps gate and up."""
@@ -617,8 +695,8 @@ class SwigluCheckpoint:
         if out is None:
             out = _empty(stream, (gate_up.shape[0], self.features), dtype=torch.bfloat16,
                          device=gate_up.device)
-        ep_swiglu_checkpoint(self.num_experts, self.features, gate_up, expert_offsets,
-                             num_tokens_per_expert, out, self.codes, self.scales, stream=stream)
+        _save(self.num_experts, self.features, gate_up, expert_offsets, num_tokens_per_expert, out,
+              self._kept, stream)
         return out
 
     def backward(self, grad_h, expert_offsets, num_tokens_per_expert, out=None, h=None,
@@ -632,7 +710,6 @@ class SwigluCheckpoint:
             out = _empty(stream, (rows, 2 * self.features), **kw)
         if h is None:
             h = _empty(stream, (rows, self.features), **kw)
-        ep_swiglu_checkpoint_backward(self.num_experts, self.features, self.codes, self.scales,
-                                      grad_h, expert_offsets, num_tokens_per_expert, out, h,
-                                      stream=stream)
+        _use(self.num_experts, self.features, self._kept, grad_h, expert_offsets,
+             num_tokens_per_expert, out, h, stream)
         return out, h

@@ -120,7 +120,7 @@ def test_python_checks():
     w = torch.zeros(2, 32, 128, dtype=torch.bfloat16)
     x, g = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(4, 32, dtype=torch.bfloat16)
     at = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
-    for bad in (w.float(), w[0], w[0, 0]):
+    for bad in (w.float(), w[0], w[0, 0], w[:, :, :64], w.transpose(1, 2)):
         with pytest.raises(ValueError):
             ep.Bf16Experts(bad)
     e = ep.Bf16Experts(w)
@@ -154,10 +154,10 @@ def test_results_come_from_the_calls_stream(monkeypatch, stream):
     from combine_get_dispatch_amd import moe
 
     seen = []
-    for name in ("ep_expert_product", "ep_expert_product_backward_rows",
-                 "ep_expert_product_backward_weights", "ep_swiglu_checkpoint",
-                 "ep_swiglu_checkpoint_backward"):
-        monkeypatch.setattr(moe, name, lambda *a, **k: seen.append(k["stream"]))
+    for name in ("_expert_product", "_backward_rows", "_save", "_use"):
+        monkeypatch.setattr(moe, name, lambda *a: seen.append(a[-1]))
+    monkeypatch.setattr(moe, "ep_expert_product_backward_weights",
+                        lambda *a, **k: seen.append(k["stream"]))
 
     def empty(s, *size, **kw):
         seen.append(s)
