@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kBlockCols = 128;  // columns that share a scale: 16 lanes x 8
 constexpr int kUnroll = 4;       // blocks of gate and up in flight per 16 lanes
-constexpr int kItemBlocks = 16 * kUnroll;  // at least; 16 x 16 lanes per workgroup
+constexpr int kItemBlocks = 16 * kUnroll;  // at least, in large calls; 16 x 16 lanes
 constexpr int kGrid = 256 * 8;
 
 struct CheckpointArgs {
@@ -183,8 +183,8 @@ __global__ __launch_bounds__(256) void swiglu_checkpoint_kernel(CheckpointArgs a
       [&](int u, int64_t row, int b) {
         const int c = b * kBlockCols + l16 * 8;
         const uint16_t *p = a.gate_up + row * 2 * F + c;
-        gate[u] = load_bf16(p, F - c);
-        up[u] = load_bf16(p + F, F - c);
+        gate[u] = load_bf16(p, F - c, c);
+        up[u] = load_bf16(p + F, F - c, c);
       },
       [&](int u, int64_t row, int b) {
         const int c = b * kBlockCols + l16 * 8;
@@ -216,11 +216,11 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(CheckpointArgs a) 
         const int c = b * kBlockCols + l16 * 8;
         const uint8_t *codes = a.codes + row * 2 * F + c;
         const float *scales = a.scales + row * 2 * blocks + b;
-        gate[u] = load_codes(codes, F - c);
-        up[u] = load_codes(codes + F, F - c);
+        gate[u] = load_codes(codes, F - c, c);
+        up[u] = load_codes(codes + F, F - c, c);
         gate_scale[u] = scales[0];
         up_scale[u] = scales[blocks];
-        grad[u] = load_bf16(a.grad_h + row * F + c, F - c);
+        grad[u] = load_bf16(a.grad_h + row * F + c, F - c, c);
       },
       [&](int u, int64_t row, int b) {
         const int c = b * kBlockCols + l16 * 8;
@@ -260,8 +260,10 @@ CheckpointArgs checkpoint_args(int32_t E, int32_t F, const int32_t *offsets,
   a.rows = ExpertRows{offsets, counts, capacity, E};
   a.F = F;
   a.blocks = (F + kBlockCols - 1) / kBlockCols;
-  a.item_rows = (kItemBlocks + a.blocks - 1) / a.blocks;
-  if (a.item_rows < 4) a.item_rows = 4;
+  // where they do not fill the chip otherwise, items of one block per 16 lanes
+  const int item = capacity * a.blocks < 512 * kItemBlocks ? 16 : kItemBlocks;
+  a.item_rows = (item + a.blocks - 1) / a.blocks;
+  if (item == kItemBlocks && a.item_rows < 4) a.item_rows = 4;
   return a;
 }
 

@@ -121,11 +121,11 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
       const int at = i >> 3, p = (i & 7) * 8;
       if (kRowsAcross) {
         if (l0 + at >= length) return u32x4{0, 0, 0, 0};
-        return load_bf16(a.grad + (first + l0 + at) * N + m0 + p, there(N - m0 - p));
+        return load_bf16(a.grad + (first + l0 + at) * N + m0 + p, there(N - m0 - p), m0 + p);
       }
       if (at >= rows) return u32x4{0, 0, 0, 0};
       const uint16_t *from = KIND == kProduct ? x16 + (first + at) * K : a.grad + (first + at) * N;
-      return load_bf16(from + l0 + p, there(length - l0 - p));
+      return load_bf16(from + l0 + p, there(length - l0 - p), (int)l0 + p);
     };
     const auto col_piece = [&](int64_t l0, int i) -> u32x4 {
       const int at = i >> 3, p = (i & 7) * 8;
@@ -133,18 +133,18 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
         const int c = n0 + at % kCols;
         if (c >= out_cols) return u32x4{0, 0, 0, 0};
         return load_bf16(w + (int64_t)(c + at / kCols * out_cols) * K + l0 + p,
-                         there(length - l0 - p));
+                         there(length - l0 - p), (int)l0 + p);
       }
       if (l0 + at >= length) return u32x4{0, 0, 0, 0};
       if (KIND == kRowsGrad)
-        return load_bf16(w + (l0 + at) * K + n0 + p, there(K - n0 - p));
+        return load_bf16(w + (l0 + at) * K + n0 + p, there(K - n0 - p), n0 + p);
       const int64_t r = first + l0 + at;
       if (FP8) {  // K is a multiple of 128
         if (n0 + p >= K) return u32x4{0, 0, 0, 0};
-        return scaled_bf16(load_codes(x8 + r * K + n0 + p, 8),
+        return scaled_bf16(load_codes(x8 + r * K + n0 + p, 8, 0),
                            a.x_scales[r * (K / 128) + (n0 + p) / 128]);
       }
-      return load_bf16(x16 + r * K + n0 + p, there(K - n0 - p));
+      return load_bf16(x16 + r * K + n0 + p, there(K - n0 - p), n0 + p);
     };
     const auto place = [](bool across, int i) {  // of piece i in LDS
       const int at = i >> 3, p = i & 7;

@@ -55,21 +55,38 @@ struct __attribute__((packed, aligned(1))) Any8 {
   u32x2 v;
 };
 
-// Eight columns of a row, of which there are n.
-__device__ __forceinline__ u32x4 load_bf16(const uint16_t *p, int n) {
-  if (n >= 8) return reinterpret_cast<const Any16 *>(p)->v;
+// Eight columns of a row, of which there are n, zeros for the others; `before`
+// columns of the row come before them.  A row's last columns come with the ones
+// before them, in one load.
+__device__ __forceinline__ u32x4 load_bf16(const uint16_t *p, int n, int before) {
   u32x4 v = {0, 0, 0, 0};
+  if (n >= 8) return reinterpret_cast<const Any16 *>(p)->v;
+  if (n <= 0) return v;
+  if (before + n >= 8) {
+    const u32x4 all = reinterpret_cast<const Any16 *>(p - (8 - n))->v;
+    const int drop = (8 - n) * 16;
+    uint64_t lo = all[0] | (uint64_t)all[1] << 32, hi = all[2] | (uint64_t)all[3] << 32;
+    lo = drop >= 64 ? hi >> (drop - 64) : lo >> drop | hi << 1 << (63 - drop);
+    hi = drop >= 64 ? 0 : hi >> drop;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 7; ++i)
     if (i < n) v[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
   return v;
 }
 
-__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n) {
-  if (n >= 8) return reinterpret_cast<const Any8 *>(p)->v;
+__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n, int before) {
   u32x2 v = {0, 0};
+  if (n >= 8) return reinterpret_cast<const Any8 *>(p)->v;
+  if (n <= 0) return v;
+  if (before + n >= 8) {
+    const u32x2 all = reinterpret_cast<const Any8 *>(p - (8 - n))->v;
+    const uint64_t w = (all[0] | (uint64_t)all[1] << 32) >> (8 - n) * 8;
+    return u32x2{(uint32_t)w, (uint32_t)(w >> 32)};
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 7; ++i)
     if (i < n) v[i / 4] |= (uint32_t)p[i] << (i % 4 * 8);
   return v;
 }
