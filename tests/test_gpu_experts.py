@@ -101,7 +101,7 @@ def many(seed, experts, *large):
 
 SHAPES = [  # K, N, counts
     (128, 80, many(1, 180, 513, 64, 65)), (264, 272, many(2, 190, 300, 129)),
-    (384, 48, many(3, 200, 255, 192, 128)), (72, 536, many(4, 170, 257, 700)),
+    (384, 48, many(3, 200, 255, 192, 128)), (64, 48, many(5, 1024, 300)), (72, 536, many(4, 170, 257, 700)),
     (1, 1, [1]), (8, 8, [1]), (33, 18, [3, 0]), (128, 40, [0, 1, 17]), (256, 130, [65, 1, 0, 64]),
     (1024, 100, [0, 7]), (640, 264, [33, 1, 0, 129, 2]), (384, 96, [9, 8, 7, 6, 5, 4, 3, 200]),
     (512, 520, [300]), (136, 1002, [257, 31]), (384, 512, [130, 256, 0, 511]), (72, 64, [16] * 9),
@@ -283,6 +283,35 @@ def test_rows_that_are_not_finite_stay_by_themselves(K, N):
         bad[[3, 64, 89]] = True
         assert torch.equal(got[~bad], clean[~bad])
         assert not torch.isfinite(got[bad]).any()
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_results_between_16_byte_boundaries(swiglu):
+    """Results may begin anywhere: by tiles, few rows and gradients."""
+    rng = np.random.default_rng(8)
+    K, N = 128, 80
+    for counts in ([3], [40, 100], many(4, 180, 200)):
+        off, cap = layout_of(counts, 0)
+        at = dev(off), dev(np.array(counts, np.int32))
+        wt, _ = draw_w(rng, counts, N, K, False)
+        wt = wt.nan_to_num()
+        x = ref.to_bf16(draw_rows(rng, cap, K, False)).cuda()
+        e = ep.Bf16Experts(wt, swiglu=swiglu)
+        say(f"results between 16-byte boundaries, {len(counts)} experts")
+        want = e.product(x, None, *at)
+        for by in (1, 3, 4):
+            flat = torch.full((want.numel() + 8,), 99.0, dtype=torch.bfloat16, device="cuda")
+            out = flat[by:by + want.numel()].view(want.shape)
+            assert torch.equal(e.product(x, None, *at, out=out), want)
+            assert (flat[:by] == 99.0).all() and (flat[by + want.numel():] == 99.0).all()
+        g = ref.to_bf16(draw_rows(rng, cap, N, False)).cuda()
+        want = e.backward_rows(g, *at)
+        flat = torch.full((want.numel() + 8,), 99.0, dtype=torch.bfloat16, device="cuda")
+        out = flat[1:1 + want.numel()].view(want.shape)
+        # another order of the same sums
+        d = (e.backward_rows(g, *at, out=out).double() - want.double()).abs()
+        size = 2 * ref.sum_error(N, 6 * 4 * N ** 0.5) + want.double().abs() * 2 * UBF16
+        assert (d <= size).all() and flat[0] == 99.0 and (flat[1 + want.numel():] == 99.0).all()
 
 
 def test_large_and_small_values():
