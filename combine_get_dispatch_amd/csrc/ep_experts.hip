@@ -246,6 +246,26 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 // c[m, n] = sum_l a[m, l] b[n, l] in tiles of 256 x 256, 64 of l at a time.
 // "Rows" is the side of m, "columns" that of n.  The matrix instruction takes
 // columns first, so that a lane's results are consecutive columns of one row.
+//
+// A persistent workgroup per compute unit; eight waves of 128 x 64 each, two per
+// SIMD, one of which multiplies while the other waits.  Both sides go from memory
+// to LDS without registers, whole 128-byte lines (32 of l at a time, half lines,
+// need twice the requests: 1018 us in the first case below), and from there to
+// the 16 x 16 x 32 instruction, which needs less power than 32 x 32 x 16 for the
+// same sums (of random numbers, alone: 2159 and 1885 TFLOP/s).
+//   32768 rows of 32 experts, 2048 x 7168        860 us, 1120 TFLOP/s
+//   one expert, 4096 x 4096                      800 us, 1370 TFLOP/s
+//   rows' gradient of 32, 4096 x 7168           1720 us, 1120 TFLOP/s
+//   weights' gradient of 32, 4096 x 7168        1796 us, 1070 TFLOP/s
+//     with FP8 rows                             2060 us,  934 TFLOP/s
+//   128 FP8 rows of 32, 7168 x 2 x 2048          310 us, 6.1 TB/s of weights
+// What bounds it: of one expert's time the matrix instructions are busy 70 %; the
+// clock is then at 1.9 GHz, by power (2.4 with rows and weights of zeros).  With
+// 32 uneven experts they are busy 60 %: last tiles of few rows, items that do not
+// come out even, and the end of a tile, 8 % of the time.  Tried and slower: four
+// waves of 128 x 128 (a third less LDS traffic, but no second wave: 947 us for
+// 791), loads all together after the barrier, raised priority of waves that
+// multiply, compute units that start apart.
 
 
 constexpr int kTile = 256;            // rows and columns of a tile
@@ -253,7 +273,9 @@ constexpr int kDepth = 64;            // of the sum, per stage
 constexpr int kColSlots = 3, kRowSlots = 2;  // stages in LDS: 160 KB, all of it, in bf16
 constexpr int kTileWaves = 8;
 constexpr int kTileWorkgroups = 256;  // one per compute unit, by its LDS
-constexpr int kBand = 8;              // row tiles that go through the columns together
+// Row tiles that go through the columns together (32768 rows, 4096 x 4096, one
+// expert: 848 us; 4: 852, 16: 966; 32 experts, 2048 x 7168: 888, 905, 888).
+constexpr int kBand = 8;
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -485,7 +507,8 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   // 128 rows leave the registers.  Columns (weights' gradient): x is rounded to
   // bf16, as the scales go by the rows that are summed over; each value once, a
   // stage ahead, into a place that the instructions' operands are read from.
-  // (By each wave for itself, two of them the same values: 2500 us, so WIDE_US.)
+  // (By each wave for itself, two of them the same values, 32 experts, 4096 x 7168:
+  // 2503 us, so 2412.)
   constexpr bool kRows8 = KIND == kProduct && FP8, kCols8 = KIND == kWeightsGrad && FP8;
   constexpr int kRowTile = SMALL || kRows8 ? kTile / 2 : kTile;
   constexpr int kColTile = SMALL ? kTile / 2 : kTile;
@@ -714,8 +737,8 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   };
   // FP8 columns: this thread's pieces of 8 codes of a stage, rounded to bf16 and
   // put where the operands are read.  A wave writes whole lines, so that its
-  // writes cover all banks (16 codes per lane, with gaps of 16 bytes: 2412 us for
-  // 2250 in the case above).
+  // writes cover all banks (in the case above 5.05 M cycles; with 16 codes per
+  // lane, and so gaps of 16 bytes between lanes, 5.40 M).
   constexpr int kPieces = kColLine / 8, kMine = kCols8 ? kPieces / 8 : 1;
   u32x4 wide[kMine];
   const auto widen = [&](int slot) {
@@ -1062,8 +1085,10 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
 // A workgroup has 32 rows of one expert's weights (SwiGLU: 16 of the gate and 16
 // of up), all of the sum and 16 rows of x at a time; the sum is dealt to its
 // waves in chunks, and theirs are added in LDS at the end.  Each wave loads for
-// itself, three chunks ahead and without barriers: reading the weights is the
-// bound, and what counts is how much of it is on its way (STREAM_NOTE).
+// itself, two chunks ahead and without barriers: reading the weights is the
+// bound, and what counts is how much of it is on its way.  One token, 8 of 64
+// experts, 4096 x 2 x 1024: 24.5 us, 5.5 TB/s (by tiles 53); FP8 rows, 7168 x 2 x
+// 2048: 84 us (110).
 constexpr int kStreamWaves = 4, kStreamStages = 3, kStreamRows = 16, kStreamCols = 32;
 
 template <bool FP8, bool SWIGLU>
@@ -1212,7 +1237,11 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
 // Calls f with the tiles' size: 128 x 128, two workgroups per compute unit,
 // where tiles of 256 x 256 would leave half the chip idle (kSmallTiles).  Of the
 // experts' rows only the buffer's are known.
-//   SMALL_NOTE
+//   tiles of 256       64         96        128        192        256
+//   bf16, 8 experts, 2048 x 512 .. 2048, us of 128 and of 256:
+//                   32, 47     24, 42                32, 47     47, 48
+//   rows' gradient                       24, 44                 48, 51
+//   weights' gradient, 2048 x 2048       44, 57     47, 45     48, 39
 constexpr int64_t kSmallTiles = 160;
 
 template <typename F>
@@ -1323,6 +1352,10 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
   const auto launch = [&](auto f, auto s) {
     const int64_t columns = s.value ? N / 2 : N, tile_cols = s.value ? kTile / 2 : kTile;
     const int64_t hit = capacity < experts->num_experts ? capacity : experts->num_experts;
+    // Streamed and tiled, us: 16 rows of 32 experts, 4096 x 2048 54, 73; 24 of 32
+    // 79, 95; 64 of 16, 2048 x 2048 27, 32; 64 of 8, 4096 x 2048 33, 56; 64 of 2
+    // 24, 46.  Past 64 rows, or where tiles fill the chip, rows by 16 read the
+    // weights again and again.
     const bool few = capacity <= kStreamRows ||
                      (capacity <= 4 * kStreamRows &&
                       hit * ((columns + tile_cols - 1) / tile_cols) < kTileWorkgroups);
