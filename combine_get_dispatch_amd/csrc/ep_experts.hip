@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 //   rows' gradient of 32, 4096 x 7168           1720 us, 1120 TFLOP/s
 //   weights' gradient of 32, 4096 x 7168        1796 us, 1070 TFLOP/s
 //     with FP8 rows                             2060 us,  934 TFLOP/s
-//   128 FP8 rows of 32, 7168 x 2 x 2048          310 us, 6.1 TB/s of weights
+//   128 FP8 rows of 32, 7168 x 2 x 2048          272 us, 6.9 TB/s of weights
 // What bounds it: of one expert's time the matrix instructions are busy 70 %; the
 // clock is then at 1.9 GHz, by power (2.4 with rows and weights of zeros).  With
 // 32 uneven experts they are busy 60 %: last tiles of few rows, items that do not
@@ -283,12 +283,21 @@ typedef __attribute__((address_space(3))) uint8_t lds_byte;
 // the offset is outside the buffer.  Written in assembly because the compiler
 // has every LDS read wait for all of its own such loads.  Nothing comes back in
 // registers; stage_barrier() waits.
+// ONCE: non-temporal, for what no other workgroup and no later call reads again.
+template <bool ONCE = false>
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-      :
-      : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
-      : "memory");
+  if constexpr (ONCE)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+        :
+        : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
+        : "memory");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
+        : "memory");
 }
 
 // 4 bytes per lane, at lds + 4 * lane.
@@ -374,6 +383,7 @@ struct Items {
   int chunk = -1;            // experts 64 chunk .. + 63
   int32_t before = 0, end = 0;     // row tiles before the chunk's, and through it
   int32_t first_tile = 0, tiles = 0;  // of this lane's expert
+  static constexpr int64_t kManyItems = 4 * kTileWorkgroups;
 
   __device__ __forceinline__ int64_t lane_rows(int c) const {  // of expert 64 c + lane
     const int e = c * 64 + (threadIdx.x & 63);
@@ -402,7 +412,8 @@ struct Items {
   // An item of the weights' gradient goes by its expert's rows: eighths of the
   // steps, with the end of an item by what it loads and stores.  (32 experts whose
   // rows differ by a third, 4096 x 7168: 1796 us, by items 1914; FP8 rows 2067,
-  // 2303; fp32 added up, 8 experts of 2048 x 7168: 252, 269.)
+  // 2303; fp32 added up, 8 experts of 2048 x 7168: 252, 269; but 256 items, 4
+  // experts of 2048 x 2048: 56, 39.)
   __device__ __forceinline__ void eighth(int part, int64_t *from, int64_t *to) const {
     const int lane = threadIdx.x & 63;
     if constexpr (KIND != kWeightsGrad) {
@@ -412,6 +423,13 @@ struct Items {
       *from = part * per < all ? part * per : all;
       *to = *from + per < all ? *from + per : all;
     } else {
+      const int64_t items = (int64_t)row_tiles * col_tiles;  // of an expert
+      if (a.rows.E * items < kManyItems) {  // few rounds: these have to come out even
+        const int64_t all = a.rows.E * items, per = (all + 7) / 8;
+        *from = part * per < all ? part * per : all;
+        *to = *from + per < all ? *from + per : all;
+        return;
+      }
       const uint32_t end = (sizeof(OUT) == 4 ? 6 : 4) * (a.add != nullptr ? 2 : 1);
       const auto cost = [&](int c) -> uint32_t {
         return c * 64 + lane < a.rows.E ? (uint32_t)((lane_rows(c) + 63) / 64) + end : 0;
@@ -419,7 +437,6 @@ struct Items {
       uint32_t all = 0;
       for (int c = 0; c * 64 < a.rows.E; ++c) all += cost(c);
       all = lane_of(scan(all), 63);
-      const int64_t items = (int64_t)row_tiles * col_tiles;  // of an expert
       const uint64_t p0 = (uint64_t)all * part / 8, p1 = (uint64_t)all * (part + 1) / 8;
       *from = *to = a.rows.E * items;
       uint32_t before_chunk = 0;
@@ -498,7 +515,7 @@ __device__ __forceinline__ int across_swizzle8(int line, int l) {
   return line == 256 ? l & 15 : l >> 1 & 7;
 }
 
-template <Kind KIND, bool FP8, bool SWIGLU, typename OUT, bool SMALL>
+template <Kind KIND, bool FP8, bool SWIGLU, typename OUT, bool SMALL, bool ONCE>
 __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_kernel(
     ProductArgs a) {
   constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
@@ -602,7 +619,7 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   // The loads run ahead of the products, through the items' ends: columns two
   // stages ahead (FP8: three, one of them for the rounding), in three slots, and
   // rows one, in two.  (With two slots of both the decode share in bf16 takes 364
-  // us, so 311.)
+  // us, so 311, both without non-temporal loads.)
   struct Loads {
     const uint8_t *base = nullptr, *scales = nullptr;
     int bytes = 0;  // along: from the base to the last row's end
@@ -663,9 +680,6 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   };
   // Loads go out one at a time between products: together they would hold up
   // every wave until the last was taken.
-  const auto load = [&](const Loads &x, int at, uint32_t step, int i) {
-    load_to_lds(lds0 + at + wave * 1024 + i * 8192, x.off + i * step, buffer_of(x.base, x.there));
-  };
   const auto see = [&](Loads *x, bool is_across, int pitch, uint32_t off, int per) {
     const int l2 = x->left - wave * per < kDepth ? x->left - wave * per : kDepth;
     const int n = x->left <= 0 ? 0 : is_across ? l2 * pitch - x->skip : x->bytes;
@@ -699,11 +713,13 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
     }
   };
   const auto load_rows = [&](int slot, int i) {
-    load(rows, kRowsAt + slot * kRowBytes, row_step, i);
+    load_to_lds(lds0 + kRowsAt + slot * kRowBytes + wave * 1024 + i * 8192,
+                rows.off + i * row_step, buffer_of(rows.base, rows.there));
     if (i == kRowLoads - 1) load_row_scales(slot);
   };
   const auto load_cols = [&](int slot, int i) {
-    load(cols, slot * kColBytes, col_step, i);
+    load_to_lds<ONCE>(lds0 + slot * kColBytes + wave * 1024 + i * 8192, cols.off + i * col_step,
+                      buffer_of(cols.base, cols.there));
     if (i == kColLoads - 1) load_col_scales(slot);
   };
   const auto on = [&](Loads *x, bool is_across, int pitch, int elem) {
@@ -1088,10 +1104,10 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
 // itself, two chunks ahead and without barriers: reading the weights is the
 // bound, and what counts is how much of it is on its way.  One token, 8 of 64
 // experts, 4096 x 2 x 1024: 24.5 us, 5.5 TB/s (by tiles 53); FP8 rows, 7168 x 2 x
-// 2048: 84 us (110).
+// 2048: 76 us (110).
 constexpr int kStreamWaves = 4, kStreamStages = 3, kStreamRows = 16, kStreamCols = 32;
 
-template <bool FP8, bool SWIGLU>
+template <bool FP8, bool SWIGLU, bool ONCE>
 __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(ProductArgs a) {
   // 128 bytes of each row of x are a chunk
   constexpr int kChunk = FP8 ? 128 : 64;
@@ -1139,8 +1155,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
         const int bytes = have <= 0 || k_left <= 0
                               ? 0 : (have < 8 ? have : 8) * w_pitch - (k0 + part * 64) * 2;
         const bool in = part * 64 + p * 8 < k_left;
-        load_to_lds(lds + i * 1024, in ? (uint32_t)(at_row * w_pitch + p * 16) : kNowhere,
-                    buffer_of(base, bytes < 0 ? 0 : bytes));
+        load_to_lds<ONCE>(lds + i * 1024,
+                          in ? (uint32_t)(at_row * w_pitch + p * 16) : kNowhere,
+                          buffer_of(base, bytes < 0 ? 0 : bytes));
       }
 #pragma unroll
       for (int i = 0; i < kXLoads; ++i) {
@@ -1245,11 +1262,30 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
 constexpr int64_t kSmallTiles = 160;
 
 template <typename F>
-void with_tiles(int64_t tiles, F f) {
+void with_tiles(int64_t tiles, bool once, F f) {
   if (tiles <= kSmallTiles)
-    f(std::true_type{}, dim3(2 * kTileWorkgroups));
+    f(std::true_type{}, std::false_type{}, dim3(2 * kTileWorkgroups));
+  else if (once)
+    f(std::false_type{}, std::true_type{}, dim3(kTileWorkgroups));
   else
-    f(std::false_type{}, dim3(kTileWorkgroups));
+    f(std::false_type{}, std::false_type{}, dim3(kTileWorkgroups));
+}
+
+// The weights that a call reads are past the Infinity Cache, where the next call
+// finds nothing of them again, and most experts have one row tile, so that one
+// workgroup reads them.
+constexpr int64_t kInfinityCache = int64_t{256} << 20;
+// Non-temporal and not, us (32 experts, 7168 x 2 x 2048, but where it says):
+//   tiles of 256 rows   4 rows each 280, 311   32 289, 314   128 400, 419
+//     rows' gradient, 4096 x 7168   128 396, 399      2048 x 7168   16 139, 159
+//     one of 2048 x 7168 with 1024 rows each 964, 907
+//   FP8 rows, tiles of 128          4 272, 309    128 503, 471
+//   streamed: one token's 8 experts, FP8 rows 76, 83
+//     64 rows of 2 experts, 4096 x 2048, in the cache and read four times 26, 24
+bool read_once(const ProductArgs &a, int row_tile) {
+  const int64_t hit = a.rows.capacity < a.rows.E ? a.rows.capacity : a.rows.E;
+  return hit * a.N * a.K * 2 > kInfinityCache &&
+         a.rows.capacity * 2 <= (int64_t)a.rows.E * row_tile;
 }
 
 int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
@@ -1361,15 +1397,20 @@ ep_status_t ep_expert_product(const ep_experts_t *experts, ep_dtype_t x_dtype, c
                       hit * ((columns + tile_cols - 1) / tile_cols) < kTileWorkgroups);
     if (few && (f.value || K % 8 == 0)) {
       constexpr int kCols = s.value ? kStreamCols / 2 : kStreamCols;
-      hipLaunchKernelGGL((product_stream_kernel<f.value, s.value>),
-                         dim3((unsigned)((columns + kCols - 1) / kCols),
-                              (unsigned)experts->num_experts),
-                         dim3(kStreamWaves * 64), 0, stream, a);
+      const dim3 grid((unsigned)((columns + kCols - 1) / kCols), (unsigned)experts->num_experts);
+      if (read_once(a, kStreamRows))
+        hipLaunchKernelGGL((product_stream_kernel<f.value, s.value, true>), grid,
+                           dim3(kStreamWaves * 64), 0, stream, a);
+      else
+        hipLaunchKernelGGL((product_stream_kernel<f.value, s.value, false>), grid,
+                           dim3(kStreamWaves * 64), 0, stream, a);
     } else if (f.value || K % 8 == 0) {
-      with_tiles(row_tiles_of(a) * tiles_of(N), [&](auto small, dim3 grid) {
-        hipLaunchKernelGGL((product_tile_kernel<kProduct, f.value, s.value, uint16_t, small.value>),
-                           grid, dim3(kTileWaves * 64), 0, stream, a);
-      });
+      with_tiles(row_tiles_of(a) * tiles_of(N), read_once(a, f.value ? kTile / 2 : kTile),
+                 [&](auto small, auto once, dim3 grid) {
+                   hipLaunchKernelGGL((product_tile_kernel<kProduct, f.value, s.value, uint16_t,
+                                                           small.value, once.value>),
+                                      grid, dim3(kTileWaves * 64), 0, stream, a);
+                 });
     } else
       hipLaunchKernelGGL((product_any_kernel<kProduct, false, s.value, uint16_t>),
                          dim3(kAnyGrid), dim3(256), 0, stream, a);
@@ -1408,10 +1449,12 @@ ep_status_t ep_expert_product_backward_rows(const ep_experts_t *experts, const u
   a.grad = grad_out;
   a.out = grad_x;
   if (a.K % 8 == 0 && a.N % 8 == 0 && aligned_to(grad_x, 16))
-    with_tiles(row_tiles_of(a) * tiles_of(a.K), [&](auto small, dim3 grid) {
-      hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, false, uint16_t, small.value>), grid,
-                         dim3(kTileWaves * 64), 0, stream, a);
-    });
+    with_tiles(row_tiles_of(a) * tiles_of(a.K), read_once(a, kTile),
+               [&](auto small, auto once, dim3 grid) {
+                 hipLaunchKernelGGL((product_tile_kernel<kRowsGrad, false, false, uint16_t,
+                                                         small.value, once.value>),
+                                    grid, dim3(kTileWaves * 64), 0, stream, a);
+               });
   else
     hipLaunchKernelGGL((product_any_kernel<kRowsGrad, false, false, uint16_t>), dim3(kAnyGrid),
                        dim3(256), 0, stream, a);
@@ -1448,10 +1491,10 @@ ep_status_t ep_expert_product_backward_weights(
   const bool tiled = K % 8 == 0 && N % 8 == 0;
   const auto launch = [&](auto f, auto value) {
     if (tiled)
-      with_tiles(a.rows.E * tiles_of(N) * tiles_of(K), [&](auto small, dim3 grid) {
+      with_tiles(a.rows.E * tiles_of(N) * tiles_of(K), false, [&](auto small, auto, dim3 grid) {
         hipLaunchKernelGGL(
-            (product_tile_kernel<kWeightsGrad, f.value, false, decltype(value), small.value>), grid,
-            dim3(kTileWaves * 64), 0, stream, a);
+            (product_tile_kernel<kWeightsGrad, f.value, false, decltype(value), small.value, false>),
+            grid, dim3(kTileWaves * 64), 0, stream, a);
       });
     else
       hipLaunchKernelGGL((product_any_kernel<kWeightsGrad, f.value, false, decltype(value)>),

@@ -327,6 +327,71 @@ def test_large_and_small_values():
         assert np.array_equal(got.double().cpu().numpy(), np.full((70, N), want))
 
 
+@pytest.mark.parametrize("K,N,counts", [(384, 272, many(6, 260, 300, 65)), (264, 528, many(7, 175, 129))],
+                         ids=name)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weights_gradient_of_many_tiles(K, N, counts, fp8):
+    """More than a thousand tiles, several of each expert, shared by the steps they take."""
+    if fp8 and K % 128:
+        pytest.skip("FP8 rows come in blocks of 128")
+    rng = np.random.default_rng(K)
+    off, cap = layout_of(counts, 1)
+    say(f"weights' gradient of many tiles K={K} N={N} fp8={fp8}")
+    x, xs, xv = draw_x(rng, cap, K, fp8, True, off, counts, True)
+    dyv = draw_rows(rng, cap, N, True)
+    dy = ref.to_bf16(only_experts(dyv, off, counts)).cuda()
+    w = torch.zeros(len(counts), N, K, dtype=torch.bfloat16, device="cuda")
+    got = ep.Bf16Experts(w).backward_weights(x, xs, dy, dev(off), dev(np.array(counts, np.int32)),
+                                             dtype=torch.float32).cpu().numpy()
+    for e, lo, hi in ref.expert_rows(off, counts, cap):
+        assert np.array_equal(got[e], dyv[lo:hi].T @ xv[lo:hi]), e
+
+
+# (experts, K, N, the rows of each hit expert): all have more than 256 MiB of weights
+PAST_CACHE = [(40, 2048, 2048, [3] * 40), (40, 2048, 2040, [70] + [0, 20] * 19 + [129]),
+              (20, 4096, 2064, [1] * 16 + [0] * 4), (33, 2176, 2048, [0] + [17] * 32)]
+
+
+@pytest.mark.parametrize("E,K,N,counts", PAST_CACHE, ids=["3", "uneven", "one", "17"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weights_past_the_cache(E, K, N, counts, fp8):
+    """Small integers: sums are exact, so every form of the kernel has to give
+    the same bits, with SwiGLU too, as calls over a few experts at a time."""
+    rng = np.random.default_rng(E + K)
+    off, cap = layout_of(counts, 1)
+    say(f"weights past the cache E={E} K={K} N={N} fp8={fp8}")
+    x, xs, xv = draw_x(rng, cap, K, fp8, True, off, counts)
+    w = torch.randint(-4, 5, (E, N, K), device="cuda").to(torch.bfloat16)
+    dyv = draw_rows(rng, cap, N, True)
+    dy = ref.to_bf16(only_experts(dyv, off, counts)).cuda()
+    n = np.array(counts, np.int32)
+
+    def run(swiglu, from_expert, to_expert):
+        part = ep.Bf16Experts(w[from_expert:to_expert], swiglu=swiglu)
+        o = dev(off[from_expert:to_expert + 1])
+        k = dev(n[from_expert:to_expert])
+        out = torch.full((cap, N // 2 if swiglu else N), 99.0, dtype=torch.bfloat16, device="cuda")
+        part.product(x, xs, o, k, out=out)
+        dx = torch.full((cap, K), 99.0, dtype=torch.bfloat16, device="cuda")
+        part.backward_rows(dy, o, k, out=dx)
+        return out, dx
+
+    y, dx = run(False, 0, E)
+    h, _ = run(True, 0, E)
+    y_want = torch.full_like(y, 99.0)
+    dx_want = torch.full_like(dx, 99.0)
+    xd, dyd = torch.from_numpy(xv).cuda(), torch.from_numpy(dyv).cuda()
+    for e, lo, hi in ref.expert_rows(off, counts, cap):
+        y_want[lo:hi] = (xd[lo:hi] @ w[e].double().T).float().bfloat16()
+        dx_want[lo:hi] = (dyd[lo:hi] @ w[e].double()).float().bfloat16()
+    assert torch.equal(y, y_want) and torch.equal(dx, dx_want)
+    for e in range(0, E, 7):
+        to = min(E, e + 7)
+        lo, hi = int(off[e]), int(off[to])
+        h_part, dx_part = run(True, e, to)
+        assert torch.equal(h[lo:hi], h_part[lo:hi]) and torch.equal(dx[lo:hi], dx_part[lo:hi])
+
+
 def test_python_refusals():
     e = ep.Bf16Experts(torch.zeros(2, 32, 128, dtype=torch.bfloat16, device="cuda"))
     x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
