@@ -620,6 +620,13 @@ class Bf16Experts:
     def weights(self):
         return self._weights
 
+    def _where(self):
+        """Device and pointer, looked at again where the tensor's storage was
+        replaced (by ``.data``, say)."""
+        if self._weights.data_ptr() != self._at[1]:
+            self._at = _weights_at(self._weights, self.cfg)
+        return self._at
+
     def product(self, x, x_scales, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, out_features] (half of them with swiglu): each expert's
         rows times its weights.  Rows that are no expert's are left as they
@@ -630,7 +637,7 @@ class Bf16Experts:
         if out is None:
             N = self.cfg.out_features // (2 if self.swiglu else 1)
             out = _empty(stream, (x.shape[0], N), dtype=torch.bfloat16, device=x.device)
-        _expert_product(self.cfg, self._ref, x, x_scales, self._at, 1 if self.swiglu else 0,
+        _expert_product(self.cfg, self._ref, x, x_scales, self._where(), 1 if self.swiglu else 0,
                         expert_offsets, num_tokens_per_expert, out, stream)
         return out
 
@@ -642,7 +649,7 @@ class Bf16Experts:
         if out is None:
             out = _empty(stream, (grad_out.shape[0], self.cfg.in_features), dtype=torch.bfloat16,
                          device=grad_out.device)
-        _backward_rows(self.cfg, self._ref, grad_out, self._at, expert_offsets,
+        _backward_rows(self.cfg, self._ref, grad_out, self._where(), expert_offsets,
                        num_tokens_per_expert, out, stream)
         return out
 

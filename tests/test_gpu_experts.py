@@ -392,6 +392,23 @@ def test_weights_past_the_cache(E, K, N, counts, fp8):
         assert torch.equal(h[lo:hi], h_part[lo:hi]) and torch.equal(dx[lo:hi], dx_part[lo:hi])
 
 
+def test_weights_with_another_storage():
+    """A tensor's storage may be replaced between calls; what does not fit is refused."""
+    t = torch.zeros(2, 32, 128, dtype=torch.bfloat16, device="cuda")
+    e = ep.Bf16Experts(t)
+    x = torch.ones(4, 128, dtype=torch.bfloat16, device="cuda")
+    g = torch.ones(4, 32, dtype=torch.bfloat16, device="cuda")
+    off, n = dev(np.array([0, 2, 4], np.int32)), dev(np.array([2, 2], np.int32))
+    assert (e.product(x, None, off, n) == 0).all()
+    t.data = torch.ones_like(t)
+    assert (e.product(x, None, off, n) == 128).all()
+    assert (e.backward_rows(g, off, n) == 32).all()
+    t.data = torch.ones(2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: e.product(x, None, off, n), lambda: e.backward_rows(g, off, n)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_python_refusals():
     e = ep.Bf16Experts(torch.zeros(2, 32, 128, dtype=torch.bfloat16, device="cuda"))
     x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
