@@ -94,7 +94,7 @@ __device__ __forceinline__ void sigmoids8(const float *y, float *s, float *rest)
   float most = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(y[i]));
-  if (__any(most > 80.0f)) {
+  if (most > 80.0f) {  // not by the wave: a row's results are the same beside any other
 #pragma unroll
     for (int i = 0; i < 8; ++i) sigmoids(y[i], &s[i], &rest[i]);
     return;

@@ -267,7 +267,6 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 // 791), loads all together after the barrier, raised priority of waves that
 // multiply, compute units that start apart.
 
-
 constexpr int kTile = 256;            // rows and columns of a tile
 constexpr int kDepth = 64;            // of the sum, per stage
 constexpr int kColSlots = 3, kRowSlots = 2;  // stages in LDS: 160 KB, all of it, in bf16

@@ -196,3 +196,22 @@ def test_rows_past_the_capacity():
     got = h.double().cpu().numpy()
     assert (got[:cap][~live] == 99.0).all() and (got[cap:] == 99.0).all()
     assert (got[:cap][live] != 99.0).all()
+
+
+@pytest.mark.parametrize("F", [40, 136])
+def test_a_row_is_the_same_beside_any_other(F):
+    """Large gates take another form of the exponential: for their own values alone."""
+    rng = np.random.default_rng(F)
+    n = 64
+    v = ref.rounded(rng.normal(size=(n, 2 * F)) * 9)
+    beside = v.copy()
+    beside[::2] = ref.rounded(rng.normal(size=(n // 2, 2 * F)) * 400)
+    grad = ref.to_bf16(ref.rounded(rng.normal(size=(n, F)))).cuda()
+    at = dev(np.array([0], np.int32)), dev(np.array([n], np.int32))
+    got = []
+    for rows in (v, beside):
+        c = ep.SwigluCheckpoint(n, F, 1)
+        h = c.save(ref.to_bf16(rows).cuda(), *at)
+        got.append([t[1::2] for t in (h, c.codes, c.scales, *c.backward(grad, *at))])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
