@@ -25,13 +25,15 @@
  * A layer's step: ep_route, ep_get_dispatch_layout, ep_dispatch, the product
  * (gate and up, SwiGLU), the product (down), ep_combine.
  *
- * A training step keeps no activation in bf16: ep_dispatch (FP8),
- * ep_expert_product (gate and up), ep_swiglu_checkpoint, ep_expert_product
- * (down), ep_combine; then ep_combine_backward,
+ * A training step keeps of the rows inside the experts only what is in 8
+ * bits: ep_dispatch (FP8), ep_expert_product (gate and up),
+ * ep_swiglu_checkpoint, ep_expert_product (down), ep_combine; then ep_combine_backward,
  * ep_expert_product_backward_rows (down), ep_swiglu_checkpoint_backward,
  * ep_expert_product_backward_weights (down, from the h that the checkpoint
  * gives again; gate and up, from dispatch's FP8 rows),
- * ep_expert_product_backward_rows (gate and up), ep_dispatch_backward.
+ * ep_expert_product_backward_rows (gate and up), ep_dispatch_backward.  (For the
+ * gates' gradient ep_combine_backward takes the rows that were combined: they
+ * are kept, or the down product of the checkpoint's h once more.)
  *
  * Every result is deterministic: sums have a fixed order.  Nothing is
  * allocated and nothing waits, so every call can be captured in a graph; the
