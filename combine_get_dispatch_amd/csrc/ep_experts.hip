@@ -269,7 +269,6 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 
 constexpr int kTile = 256;            // rows and columns of a tile
 constexpr int kDepth = 64;            // of the sum, per stage
-constexpr int kColSlots = 3, kRowSlots = 2;  // stages in LDS: 160 KB, all of it, in bf16
 constexpr int kTileWaves = 8;
 constexpr int kTileWorkgroups = 256;  // one per compute unit, by its LDS
 // Row tiles that go through the columns together (32768 rows, 4096 x 4096, one
@@ -530,11 +529,18 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   constexpr int kColTile = SMALL ? kTile / 2 : kTile;
   constexpr int kOutTile = SWIGLU ? kColTile / 2 : kColTile;
   constexpr int kJ = kColTile / 64;  // 16 columns each, of a wave
+  // Stages in LDS: 160 KB, all of it, in bf16.  FP8 rows leave place for one more
+  // of both sides (32768 rows of 32 experts, 7168 x 4096: 2125 us, without 2178).
+  constexpr bool kDeep = kRows8 && !SMALL;
+  constexpr int kColSlots = kDeep ? 4 : 3, kRowSlots = kDeep ? 3 : 2;
   constexpr int kRowElem = kRows8 ? 1 : 2, kColElem = kCols8 ? 1 : 2;
   constexpr int kRowBytes = kRowTile * kDepth * kRowElem, kColBytes = kColTile * kDepth * kColElem;
   constexpr int kRowLoads = kRowBytes / (kTileWaves * 1024);  // of a wave and stage
   constexpr int kColLoads = kColBytes / (kTileWaves * 1024);
   constexpr int kColPart = kColLoads + kCols8;  // with the scales
+  constexpr int kRowPart = kRowLoads + kRows8;
+  // loads that are newer than the next stage's, before this one's of rows
+  constexpr int kNewer = kDeep ? 2 * kColPart + kRowPart : kColPart;
   constexpr int kRowsAt = kColSlots * kColBytes, kWideAt = kRowsAt + kRowSlots * kRowBytes;
   constexpr int kScalesAt = kWideAt + (kCols8 ? kColTile * kDepth * 2 : 0);
   constexpr int kScaleBytes = 512;  // of a stage: 128 rows, or 64 of l for two blocks
@@ -616,8 +622,8 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
   };
 
   // The loads run ahead of the products, through the items' ends: columns two
-  // stages ahead (FP8: three, one of them for the rounding), in three slots, and
-  // rows one, in two.  (With two slots of both the decode share in bf16 takes 364
+  // stages ahead (FP8 columns: three, one of them for the rounding), in three
+  // slots, and rows one, in two; with FP8 rows one more.  (With two slots of both the decode share in bf16 takes 364
   // us, so 311, both without non-temporal loads.)
   struct Loads {
     const uint8_t *base = nullptr, *scales = nullptr;
@@ -804,16 +810,24 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
     widen(0);
     put_wide();
     lds_barrier();
+  } else if constexpr (kDeep) {
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i) load_rows(1, i);
+    rows_on();
+#pragma unroll
+    for (int i = 0; i < kColLoads; ++i) load_cols(2, i);
+    cols_on();
+    stage_barrier<kNewer>();
   } else {
     stage_barrier<kColPart>();
   }
 #pragma unroll
-  for (int i = 0; i < kRowLoads; ++i) load_rows(1, i);
+  for (int i = 0; i < kRowLoads; ++i) load_rows(kRowSlots - 1, i);
   rows_on();
   int col_slot = 0, row_slot = 0;  // of the next stage
   int stored = 0;                  // stores behind the newest loads
   // Here and at the end of each item: the next stage is there, and the columns
-  // and rows of the one after it are on their way.
+  // and rows of the one after it (FP8 rows: the two) are on their way.
   for (int64_t item = from + blockIdx.x / 8; item < to; item += next) {
     Item it;
     items.get(item, &it, kOutTile);
@@ -880,10 +894,11 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
       const auto step = [&](int s, auto second) {
         constexpr bool kSecond = decltype(second)::value, kFresh = !kSecond;
         constexpr int kEarly = (kColLoads + 1) / 2;
-        const int next_col = col_slot == 2 ? 0 : col_slot + 1;
+        const int next_col = col_slot == kColSlots - 1 ? 0 : col_slot + 1;
+        const int next_row = row_slot == kRowSlots - 1 ? 0 : row_slot + 1;
         // the next columns go where the last stage's were, or, as FP8 columns have
         // been put elsewhere, this one's
-        const int free_col = kCols8 ? col_slot : col_slot == 0 ? 2 : col_slot - 1;
+        const int free_col = kCols8 ? col_slot : col_slot == 0 ? kColSlots - 1 : col_slot - 1;
         read_rows(row_slot, 0, 1);
         products(kFresh, 0, 0, std::integral_constant<int, kEarly>{},
                  [&](int i) { load_cols(free_col, i); });
@@ -902,20 +917,20 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
         }
         products(false, 1, 0, none, nothing);
         // the next stage is there, and this one's slots are free
-        if (s == 0 && stored == kStores * (kRowTile / 64))
-          stage_barrier<kColPart + kStores * (kRowTile / 64)>();
+        if (s < (kDeep ? 2 : 1) && stored == kStores * (kRowTile / 64))
+          stage_barrier<kNewer + kStores * (kRowTile / 64)>();
         else
-          stage_barrier<kColPart>();
+          stage_barrier<kNewer>();
         if constexpr (kCols8) {
           put_wide();
           products(false, 1, 1, std::integral_constant<int, kRowLoads>{},
                    [&](int i) { load_rows(row_slot, i); });
           lds_barrier();
           read_cols(next_col, 0);
-          read_rows(row_slot ^ 1, 0, 0);
+          read_rows(next_row, 0, 0);
         } else {
           read_cols(next_col, 0);
-          read_rows(row_slot ^ 1, 0, 0);
+          read_rows(next_row, 0, 0);
           products(false, 1, 1, std::integral_constant<int, kRowLoads>{},
                    [&](int i) { load_rows(row_slot, i); });
         }
@@ -925,7 +940,7 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
           add_scaled(1);
         }
         col_slot = next_col;
-        row_slot ^= 1;
+        row_slot = next_row;
       };
       if constexpr (kRows8) {
         for (int s = 0; s < steps; s += 2) {  // rows of whole blocks of 128
