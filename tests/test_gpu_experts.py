@@ -347,6 +347,38 @@ def test_weights_gradient_of_many_tiles(K, N, counts, fp8):
         assert np.array_equal(got[e], dyv[lo:hi].T @ xv[lo:hi]), e
 
 
+@pytest.mark.parametrize("K,fp8", [(64, False), (72, False), (128, False), (192, False), (128, True),
+                                   (256, True), (384, True)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_short_sums_of_many_full_tiles(K, fp8, swiglu):
+    """A stage or a few per tile, several tiles one after the other: a tile's
+    stores are on their way while the next ones' rows and columns come."""
+    rng = np.random.default_rng(K)
+    N = 1040
+    counts = [int(n) for n in rng.choice([128, 256, 65, 300], size=180)]
+    off, cap = layout_of(counts, 0)
+    say(f"short sums K={K} fp8={fp8} swiglu={swiglu}")
+    x, xs, xv = draw_x(rng, cap, K, fp8, True, off, counts)
+    w = torch.randint(-4, 5, (len(counts), N, K), device="cuda").to(torch.bfloat16)
+    n = dev(np.array(counts, np.int32))
+    y = ep.Bf16Experts(w).product(x, xs, dev(off), n)
+    xd = torch.from_numpy(xv).cuda()
+    sums = torch.empty(cap, N, dtype=torch.float64, device="cuda")
+    for e, lo, hi in ref.expert_rows(off, counts, cap):
+        sums[lo:hi] = xd[lo:hi] @ w[e].double().T
+    assert torch.equal(y, sums.float().bfloat16())
+    if swiglu:
+        # sums are exact: an exponential, a division and two products, then bf16
+        h = ep.Bf16Experts(w, swiglu=True).product(x, xs, dev(off), n).double()
+        g, u = sums[:, :N // 2], sums[:, N // 2:]
+        want = g / (1 + torch.exp(-g)) * u
+        tol = want.abs() * (12 * U32 + UBF16 * (1 + 12 * U32)) + 1e-37
+        assert ((h - want).abs() <= tol).all()
+    elif not fp8:  # the rows' gradient of the product turned over
+        dx = ep.Bf16Experts(w.transpose(1, 2).contiguous()).backward_rows(x, dev(off), n)
+        assert torch.equal(dx, y)
+
+
 # (experts, K, N, the rows of each hit expert): all have more than 256 MiB of weights
 PAST_CACHE = [(40, 2048, 2048, [3] * 40), (40, 2048, 2040, [70] + [0, 20] * 19 + [129]),
               (20, 4096, 2064, [1] * 16 + [0] * 4), (33, 2176, 2048, [0] + [17] * 32)]
