@@ -280,19 +280,25 @@ typedef __attribute__((address_space(3))) uint8_t lds_byte;
 // 16 bytes per lane from global memory to LDS, at lds + 16 * lane; zeros where
 // the offset is outside the buffer.  Written in assembly because the compiler
 // has every LDS read wait for all of its own such loads.  Nothing comes back in
-// registers; stage_barrier() waits.
+// registers; stage_barrier() waits.  The buffer's words come out of vector
+// instructions, after which a vector memory instruction may not read them for
+// five wait states; the hardware does not wait, and the compiler does so for its
+// own instructions alone.  s_mov_b32 and s_nop 3 are five, whatever comes before
+// (and m0's one); in the tiles that takes up to 1.4 % (rows' gradient of 32
+// experts, 4096 x 7168: 1730 us, with s_nop 0 1712).  m0 is reserved and no clobber can name it: nothing else in
+// these kernels may use it, which a test of the built library holds.
 // ONCE: non-temporal, for what no other workgroup and no later call reads again.
 template <bool ONCE = false>
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
   if constexpr (ONCE)
     asm volatile(
-        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+        "s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
         :
         : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
         : "memory");
   else
     asm volatile(
-        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+        "s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
         :
         : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
         : "memory");
@@ -301,7 +307,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4
 // 4 bytes per lane, at lds + 4 * lane.
 __device__ __forceinline__ void load_word_to_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+      "s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
       :
       : "s"(uniform((int)lds)), "v"(offset), "s"(buffer)
       : "memory");
