@@ -302,6 +302,16 @@ def _weights_at(w, experts):
     return d, _at(w, d, torch.bfloat16, _weight_shape(experts), "w")
 
 
+def _kept_at(t, dtype, shape, name):
+    """Device and pointer of a tensor that an object holds from call to call:
+    its storage, shape, strides and type may have been replaced (by ``.data``),
+    the address left as it was."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} is now {t.dtype} {tuple(t.shape)} with strides {t.stride()}, "
+                         f"expected contiguous {dtype} {tuple(shape)}")
+    return t.get_device(), t.data_ptr()
+
+
 def _here(t, name, other, what):
     """The device of a call whose weights or checkpoint are on `other`."""
     d = _device(t, name)
@@ -614,18 +624,17 @@ class Bf16Experts:
         E, N, K = weights.shape
         self.cfg = ep_experts_t(E, K, N)
         self._ref = ctypes.byref(self.cfg)
-        self._at = weights.get_device(), weights.data_ptr()
+        self._shape = weights.shape
 
     @property
     def weights(self):
         return self._weights
 
     def _where(self):
-        """Device and pointer, looked at again where the tensor's storage was
-        replaced (by ``.data``, say)."""
-        if self._weights.data_ptr() != self._at[1]:
-            self._at = _weights_at(self._weights, self.cfg)
-        return self._at
+        """Device and pointer at this call."""
+        import torch
+
+        return _kept_at(self._weights, torch.bfloat16, self._shape, "w")
 
     def product(self, x, x_scales, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, out_features] (half of them with swiglu): each expert's

@@ -220,3 +220,26 @@ def test_plain_gradients_against_differences():
         d[i] = step
         a, b = (np.sum(ref.swiglu_grad(v + t, gh)[1] * gh) for t in (d, -d))
         assert abs((a - b) / (2 * step) - gv[i]) < 1e-7
+
+
+@pytest.mark.parametrize("N,K", [(64, 64), (32, 128)])
+def test_weights_are_looked_at_at_each_call(N, K):
+    """A tensor's storage, shape, strides and type may be replaced with the
+    address unchanged."""
+    def other(change):
+        t = torch.zeros(2, N, K, dtype=torch.bfloat16)
+        e, at = ep.Bf16Experts(t), t.data_ptr()
+        t.data = change(t)
+        assert t.data_ptr() == at
+        return e
+
+    for change in (lambda t: t.transpose(1, 2), lambda t: t[:1], lambda t: t[:, :N // 2],
+                   lambda t: t[:, :, :K // 2], lambda t: t[:, ::2], lambda t: t.view(2, K, N)
+                   if N != K else t.view(4, N // 2, K), lambda t: t.view(torch.float16),
+                   lambda t: t.view(torch.int16)):
+        with pytest.raises(ValueError, match="^w "):
+            other(change)._where()
+    t = torch.zeros(2, N, K, dtype=torch.bfloat16)
+    e = ep.Bf16Experts(t)
+    t.data = torch.zeros_like(t)
+    assert e._where() == (-1, t.data_ptr())

@@ -441,6 +441,27 @@ def test_weights_with_another_storage():
             call()
 
 
+def test_weights_changed_at_the_same_address():
+    """What the calls would read another way than the tensor now says is refused."""
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
+    off, n = dev(np.array([0, 2, 4], np.int32)), dev(np.array([2, 2], np.int32))
+    for change in (lambda t: t.transpose(1, 2), lambda t: t[:1], lambda t: t[:, :32],
+                   lambda t: t.view(torch.float16)):
+        t = torch.ones(2, 64, 64, dtype=torch.bfloat16, device="cuda")
+        e, at = ep.Bf16Experts(t), t.data_ptr()
+        assert (e.product(x, None, off, n) == 64).all()
+        t.data = change(t)
+        assert t.data_ptr() == at
+        for call in (lambda: e.product(x, None, off, n), lambda: e.backward_rows(x, off, n)):
+            with pytest.raises(ValueError):
+                call()
+    t.data = torch.zeros(2, 64, 64, dtype=torch.bfloat16, device="cuda")
+    assert (e.product(x, None, off, n) == 0).all()
+    t.data = t.cpu()
+    with pytest.raises(ValueError):
+        e.product(x, None, off, n)
+
+
 def test_python_refusals():
     e = ep.Bf16Experts(torch.zeros(2, 32, 128, dtype=torch.bfloat16, device="cuda"))
     x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
