@@ -693,8 +693,6 @@ class SwigluCheckpoint:
                                   device=dev)
         self._scales = torch.empty(_checkpoint_shape(self.capacity, self.features),
                                    dtype=torch.float32, device=dev)
-        self._kept = (self._codes.get_device(), self.capacity, self._codes.data_ptr(),
-                      self._scales.data_ptr())
 
     @property
     def codes(self):
@@ -704,6 +702,17 @@ class SwigluCheckpoint:
     def scales(self):
         return self._scales
 
+    def _where(self):
+        """Device, rows and pointers at this call."""
+        import torch
+
+        cap, F = self.capacity, self.features
+        d, codes = _kept_at(self._codes, torch.uint8, (cap, 2 * F), "codes")
+        other, scales = _kept_at(self._scales, torch.float32, _checkpoint_shape(cap, F), "scales")
+        if other != d:
+            raise ValueError(f"scales is on {self._scales.device}, codes on {self._codes.device}")
+        return d, cap, codes, scales
+
     def save(self, gate_up, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, features]: silu(gate) * up; keeps gate and up."""
         import torch
@@ -712,7 +721,7 @@ class SwigluCheckpoint:
             out = _empty(stream, (gate_up.shape[0], self.features), dtype=torch.bfloat16,
                          device=gate_up.device)
         _save(self.num_experts, self.features, gate_up, expert_offsets, num_tokens_per_expert, out,
-              self._kept, stream)
+              self._where(), stream)
         return out
 
     def backward(self, grad_h, expert_offsets, num_tokens_per_expert, out=None, h=None,
@@ -726,6 +735,6 @@ class SwigluCheckpoint:
             out = _empty(stream, (rows, 2 * self.features), **kw)
         if h is None:
             h = _empty(stream, (rows, self.features), **kw)
-        _use(self.num_experts, self.features, self._kept, grad_h, expert_offsets,
+        _use(self.num_experts, self.features, self._where(), grad_h, expert_offsets,
              num_tokens_per_expert, out, h, stream)
         return out, h

@@ -243,3 +243,18 @@ def test_weights_are_looked_at_at_each_call(N, K):
     e = ep.Bf16Experts(t)
     t.data = torch.zeros_like(t)
     assert e._where() == (-1, t.data_ptr())
+
+
+def test_checkpoint_is_looked_at_at_each_call():
+    """Its tensors' storage may be replaced; what does not fit is refused."""
+    c = ep.SwigluCheckpoint(4, 200, 2, device="cpu")
+    for t, name in ((c.codes, "codes"), (c.scales, "scales")):
+        was = t.data
+        t.data = torch.ones_like(was)  # moved: the calls take it where it is
+        assert c._where() == (-1, 4, c.codes.data_ptr(), c.scales.data_ptr())
+        for other in (was[:3], was.t().contiguous().t(), was.view(torch.int8), was[:, :1]):
+            t.data = other
+            with pytest.raises(ValueError, match=f"^{name} "):
+                c._where()
+        t.data = was
+    assert c._where() == (-1, 4, c.codes.data_ptr(), c.scales.data_ptr())

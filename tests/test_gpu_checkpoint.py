@@ -215,3 +215,33 @@ def test_a_row_is_the_same_beside_any_other(F):
         got.append([t[1::2] for t in (h, c.codes, c.scales, *c.backward(grad, *at))])
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_a_checkpoint_moved_away_and_back():
+    """Codes and scales kept in host memory between save and backward, and other
+    tensors in their old places."""
+    rng = np.random.default_rng(4)
+    n, F = 32, 200
+    v = ref.to_bf16(ref.rounded(rng.normal(size=(n, 2 * F)))).cuda()
+    grad = ref.to_bf16(ref.rounded(rng.normal(size=(n, F)))).cuda()
+    at = dev(np.array([0], np.int32)), dev(np.array([n], np.int32))
+    c = ep.SwigluCheckpoint(n, F, 1)
+    say("a checkpoint moved away and back")
+    c.save(v, *at)
+    want = c.backward(grad, *at)
+    olds = c.codes.data, c.scales.data
+    for t in (c.codes, c.scales):
+        t.data = t.cpu()
+    olds[0].fill_(0x7F)
+    olds[1].fill_(float("nan"))
+    for call in (lambda: c.backward(grad, *at), lambda: c.save(v, *at)):
+        with pytest.raises(ValueError):
+            call()
+    for t in (c.codes, c.scales):
+        t.data = t.cuda()
+    for a, b in zip(c.backward(grad, *at), want):
+        assert torch.equal(a, b)
+    for t in olds:
+        t.zero_()
+    c.save(v, *at)
+    assert not olds[0].any() and not olds[1].any()
