@@ -327,6 +327,64 @@ def test_large_and_small_values():
         assert np.array_equal(got.double().cpu().numpy(), np.full((70, N), want))
 
 
+# Row tiles of an expert go through the columns in bands of eight: more than
+# eight tiles of 256 rows and of 128 (few tiles in all), a last band of one and
+# of more, and beside them experts of one tile and of none.
+BANDS = [(128, 520, many(8, 180, 2500, 2049)), (256, 264, [1100, 3, 0, 40]),
+         (384, 776, [2, 2304, 0, 1, 1025] + [1, 0, 257] * 30), (128, 40, [0, 1030, 2200])]
+
+
+@pytest.mark.parametrize("K,N,counts", BANDS, ids=name)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_product_over_bands_of_row_tiles(K, N, counts, fp8):
+    rng = np.random.default_rng(N + len(counts))
+    off, cap = layout_of(counts, 1)
+    say(f"bands K={K} N={N} counts={counts[:5]} fp8={fp8}")
+    x, xs, xv = draw_x(rng, cap, K, fp8, True, off, counts)
+    wt, w = draw_w(rng, counts, N, K, True)
+    at = dev(off), dev(np.array(counts, np.int32))
+    out = torch.full((cap, N), 99.0, dtype=torch.bfloat16, device="cuda")
+    ep.Bf16Experts(wt).product(x, xs, *at, out=out)
+    y, size = ref.product(xv, w, off, counts)
+    check_rows(out, y, size, K, True)
+    if fp8:
+        return
+    say("rows' gradient")  # of the product turned over: the same sums
+    out.fill_(99.0)
+    ep.Bf16Experts(wt.transpose(1, 2).contiguous()).backward_rows(x, *at, out=out)
+    check_rows(out, y, size, K, True)
+
+
+# rows of the weights: 19, 10 and 9 tiles of 128 or 256, by few tiles in all, some, many
+@pytest.mark.parametrize("K,N,counts", [(384, 2312, [70, 3]), (640, 2312, [5, 0, 64, 1, 130, 9]),
+                                        (264, 2056, [1, 2, 70, 0] * 16)], ids=name)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("add", [False, True])
+def test_weights_gradient_over_bands_of_row_tiles(K, N, counts, fp8, dtype, add):
+    if fp8 and K % 128:
+        pytest.skip("FP8 rows come in blocks of 128")
+    rng = np.random.default_rng(K + N)
+    off, cap = layout_of(counts, 2)
+    E = len(counts)
+    say(f"bands of the weights' gradient K={K} N={N} counts={counts[:6]} fp8={fp8} {dtype} "
+        f"add={add}")
+    gv = draw_rows(rng, cap, N, True)
+    g = ref.to_bf16(only_experts(gv, off, counts)).cuda()
+    x, xs, xv = draw_x(rng, cap, K, fp8, True, off, counts, round_to_bf16=True)
+    want = torch.zeros(E, N, K, dtype=torch.float64, device="cuda")
+    for e, lo, hi in ref.expert_rows(off, counts, cap):
+        want[e] = torch.from_numpy(gv[lo:hi].T @ xv[lo:hi]).cuda()
+    out = torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda")
+    if add:
+        out = torch.randint(-64, 65, (E, N, K), device="cuda").to(dtype)
+        want += out.double()
+    w = torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda")
+    ep.Bf16Experts(w).backward_weights(x, xs, g, dev(off), dev(np.array(counts, np.int32)),
+                                       out=out, add=out if add else None)
+    assert torch.equal(out, want.float().to(dtype))
+
+
 @pytest.mark.parametrize("K,N,counts", [(384, 272, many(6, 260, 300, 65)), (264, 528, many(7, 175, 129))],
                          ids=name)
 @pytest.mark.parametrize("fp8", [False, True])
