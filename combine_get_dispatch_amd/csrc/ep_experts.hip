@@ -313,15 +313,31 @@ __device__ __forceinline__ void load_word_to_lds(uint32_t lds, uint32_t offset, 
       : "memory");
 }
 
-// Eight FP8 codes as bf16, which holds every E4M3 number.
-__device__ __forceinline__ bf16x8 codes_bf16(u32x2 codes) {
+// FP8 rows: codes enter the products times a power of two, and their sums of 128
+// leave them times the scale over that power, so that sums are in fp32's range
+// where the result is, for weights of any size (by raw codes, those of 2^112 and
+// more gave infinities).  Both are exact.  2^-16: 128 codes below 2^9, so scaled,
+// sum up to less than the largest weight.  Products then lose what is below
+// 2^-133 of the scale (matrix instructions keep fp32's denormal numbers), which
+// for scales from 2^32 on would be too much; those take 2^10, with which sums past
+// the range are of results past it.
+__device__ __forceinline__ bool large_scale(float scale) {  // at least 2^32 and finite
+  const uint32_t lo = (127u + 32u) << 23;
+  return (__float_as_uint(scale) & 0x7FFFFFFFu) - lo < 0x7F800000u - lo;
+}
+
+__device__ __forceinline__ float codes_power(bool large) { return large ? 0x1p10f : 0x1p-16f; }
+__device__ __forceinline__ float sums_power(bool large) { return large ? 0x1p-10f : 0x1p16f; }
+
+// Eight FP8 codes times a power of two as bf16.
+__device__ __forceinline__ bf16x8 codes_bf16(u32x2 codes, float power) {
   u32x4 w;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w[2 * i] = __builtin_bit_cast(
-        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], 1.0f, false));
+        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], power, false));
     w[2 * i + 1] = __builtin_bit_cast(
-        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], 1.0f, true));
+        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], power, true));
   }
   return __builtin_bit_cast(bf16x8, w);
 }
@@ -523,7 +539,7 @@ template <Kind KIND, bool FP8, bool SWIGLU, typename OUT, bool SMALL, bool ONCE>
 __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_kernel(
     ProductArgs a) {
   constexpr bool kRowsAcross = KIND == kWeightsGrad, kColsAcross = KIND != kProduct;
-  // Which side is x in FP8.  Rows: codes enter the instructions exactly and the
+  // Which side is x in FP8.  Rows: codes enter the instructions exactly, and
   // scales are applied to the sums of 128, in accumulators of their own, for which
   // 128 rows leave the registers.  Columns (weights' gradient): x is rounded to
   // bf16, as the scales go by the rows that are summed over; each value once, a
@@ -850,6 +866,23 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
       bf16x8 c[2][kJ];
       RowRaw r[2][kM];
       float row_scale[2][kM];
+      // Of a block of 128, for the codes' power: whether a scale of the wave's rows
+      // is.  (A power per row does not fit the registers of the small tiles: 4096
+      // rows of 8 experts, 2048 x 2048: 70 us.  So 58.5, all by 2^-16 55.5, by raw
+      // codes 56; 32768 rows of 32, 7168 x 4096: 2248, 2244, 2215 and 2191.)
+      bool large = false;
+      const auto scale_of = [&](int slot, int f) {  // of row fragment f
+        return *reinterpret_cast<const float *>(stage + kScalesAt + slot * kScaleBytes +
+                                                (f * 32 + wr * 16 + l16) * 4);
+      };
+      const auto look_at_scales = [&](int slot) {
+        if constexpr (kRows8) {
+          bool any = false;
+#pragma unroll
+          for (int f = 0; f < 2 * kM; ++f) any |= large_scale(scale_of(slot, f));
+          large = __any(any);
+        }
+      };
       const auto read_cols = [&](int slot, int ks) {
 #pragma unroll
         for (int j = 0; j < kJ; ++j) c[ks][j] = read_col(slot, ks, j);
@@ -864,7 +897,7 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
         for (int f = 0; f < kM; ++f) {
           bf16x8 x;
           if constexpr (kRows8)
-            x = codes_bf16(r[h][f]);
+            x = codes_bf16(r[h][f], codes_power(large));
           else
             x = r[h][f];
 #pragma unroll
@@ -894,6 +927,7 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
       if (steps > 0) {
         read_cols(col_slot, 0);
         read_rows(row_slot, 0, 0);
+        look_at_scales(row_slot);
       }
       // A stage.  Each quarter's operands are read during the one before.
       // second: of the two that share a scale of FP8 rows.
@@ -918,8 +952,7 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
         if constexpr (kRows8 && kSecond) {
 #pragma unroll
           for (int f = 0; f < 2 * kM; ++f)
-            row_scale[f / kM][f % kM] = *reinterpret_cast<const float *>(
-                stage + kScalesAt + row_slot * kScaleBytes + (f * 32 + wr * 16 + l16) * 4);
+            row_scale[f / kM][f % kM] = scale_of(row_slot, f) * sums_power(large);
         }
         products(false, 1, 0, none, nothing);
         // the next stage is there, and this one's slots are free
@@ -944,6 +977,7 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
         if constexpr (kRows8 && kSecond) {
           add_scaled(0);
           add_scaled(1);
+          look_at_scales(next_row);
         }
         col_slot = next_col;
         row_slot = next_row;
@@ -1208,12 +1242,15 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
       };
       if constexpr (FP8) {
         f32x4 part[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+        float scale = *reinterpret_cast<const float *>(here + kWBytes + kXBytes + l16 * 4);
+        const bool large = large_scale(scale);
+        scale *= sums_power(large);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           // 16 codes are a piece
           const u32x2 raw = *reinterpret_cast<const u32x2 *>(
               here + kWBytes + l16 * 128 + ((ks * 2 + (quad >> 1)) ^ (l16 >> 1)) * 16 + (quad & 1) * 8);
-          const bf16x8 x = codes_bf16(raw);
+          const bf16x8 x = codes_bf16(raw, codes_power(large));
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // rows 8 g .. + 7 of the weights: part 0 at 2048 g, part 1 1024 on
@@ -1223,7 +1260,6 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
             part[j] = mul(w, x, part[j]);
           }
         }
-        const float scale = *reinterpret_cast<const float *>(here + kWBytes + kXBytes + l16 * 4);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll

@@ -262,7 +262,8 @@ typedef struct ep_experts {
  * bf16(silu(y[r, n]) * y[r, N / 2 + n]), the gate's rows of w before the up
  * projection's.  Codes and rows enter the matrix instructions exactly, the
  * scales of FP8 rows are applied in fp32 to the sums of 128; the output's is
- * the only rounding below fp32.
+ * the only rounding below fp32.  Sums are in fp32's range where the result is;
+ * beside rows whose scales are 2^32 or more, for weights below 2^102.
  *
  *   x_dtype       EP_DTYPE_BF16: x bf16 [capacity, K]
  *                 EP_DTYPE_FP8_E4M3: x uint8 [capacity, K] and x_scales fp32

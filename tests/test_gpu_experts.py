@@ -385,6 +385,86 @@ def test_weights_gradient_over_bands_of_row_tiles(K, N, counts, fp8, dtype, add)
     assert torch.equal(out, want.float().to(dtype))
 
 
+@pytest.mark.parametrize("counts", [[5], [70], [3, 70] * 90], ids=["few", "tiles", "many"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_over_the_whole_range(counts, fp8, swiglu):
+    """Rows, scales and weights at the top and the bottom of their types, that
+    bring the result back: finite wherever the result is.  Exact: a row is one
+    power of two, times 1.5 by its scales, with any signs, and a matrix another
+    one times -3 .. 3, so a sum is at most 256 x 9 steps of a power of two."""
+    rng = np.random.default_rng(42)
+    K, N = 256, 40
+    if fp8:  # power of the codes, of the rows' scales, of the weights
+        cases = [(8, -30, 118), (8, 119, -30), (-9, 115, 12), (8, -110, 120), (-9, -60, 120),
+                 (8, -126, 20), (0, 127, -120), (-9, 127, -126), (8, -10, -110), (8, 118, -126)]
+    else:
+        cases = [(127, 0, -30), (127, 0, -120), (-100, 0, 120), (-126, 0, 120), (0, 0, 110),
+                 (0, 0, -110)]
+    off, cap = layout_of(counts, 0)
+    at = dev(off), dev(np.array(counts, np.int32))
+    sign = torch.from_numpy(rng.choice([-1.0, 1.0], size=(cap, K))).cuda()
+    small = torch.from_numpy(rng.integers(-3, 4, size=(len(counts), N, K)).astype(float)).cuda()
+    sums = torch.cat([sign[lo:hi] @ small[e].T for e, lo, hi in ref.expert_rows(off, counts, cap)])
+    for px, ps, pw in cases:
+        say(f"range counts={counts[:2]} fp8={fp8} swiglu={swiglu} powers={px, ps, pw}")
+        v = sign * 2.0 ** px
+        x, xs, by = v.bfloat16(), None, 1.0
+        if fp8:
+            x, by = v.to(torch.float8_e4m3fn), 1.5
+            xs = torch.full((cap, K // 128), by * 2.0 ** ps, device="cuda")
+        assert torch.equal(x.double(), v)
+        w = (small * 2.0 ** pw).bfloat16()
+        assert torch.equal(w.double(), small * 2.0 ** pw)
+        y = sums * by * 2.0 ** (px + ps + pw)
+        got = ep.Bf16Experts(w, swiglu=swiglu).product(x.view(torch.uint8) if fp8 else x, xs, *at)
+        if not swiglu:
+            want = y.float().bfloat16()
+            assert torch.isfinite(want).all() and torch.equal(got, want)
+            continue
+        # 12 half steps, as in test_product, and a step of fp32's smallest numbers
+        # in the exponential; a result past fp32's range is infinite and one below
+        # its normal numbers may lose bits
+        g, u = y[:, :N // 2], y[:, N // 2:]
+        want = g / (1 + torch.exp(-g)) * u
+        inside = want.abs() < 2.0 ** 127
+        err = want.abs() * 12 * U32 + (g * u).abs() * 2.0 ** -149
+        tol = err + (want.abs() + err) * UBF16 + 2.0 ** -125
+        assert ((got.double() - want).abs() <= tol)[inside].all()
+        assert not torch.isnan(got).any()
+
+
+@pytest.mark.parametrize("counts", [[5], [70], [3, 70, 129] * 60], ids=["few", "tiles", "many"])
+def test_fp8_rows_beside_rows_of_other_scales(counts):
+    """Any scale beside any other, on both sides of those that the kernels treat
+    another way; and scales that are not finite stay by themselves.  Exact: small
+    integers times one power of two per row."""
+    rng = np.random.default_rng(43)
+    K, N = 256, 72
+    off, cap = layout_of(counts, 0)
+    at = dev(off), dev(np.array(counts, np.int32))
+    x, _, xv = draw_fp8(rng, cap, K, True, False)
+    v = x.view(torch.float8_e4m3fn).double()
+    w, wv = draw_w(rng, counts, N, K, True)
+    scales = 2.0 ** rng.choice([-126, -100, -30, -2, 0, 1, 31, 32, 33, 60, 100], size=cap)
+    say(f"scales beside others, counts={counts[:3]}")
+
+    def product(s):
+        xs = torch.from_numpy(np.repeat(s[:, None], K // 128, axis=1)).float().cuda()
+        return ep.Bf16Experts(w).product(x, xs, *at)
+
+    sums = torch.cat([v[lo:hi] @ torch.from_numpy(wv[e].T).cuda()
+                      for e, lo, hi in ref.expert_rows(off, counts, cap)])
+    want = (sums * torch.from_numpy(scales).cuda()[:, None]).float().bfloat16()
+    assert torch.equal(product(scales), want)
+    bad = rng.random(cap) < 0.2
+    bad[0] = True
+    dirty = np.where(bad, rng.choice([np.inf, -np.inf, np.nan], size=cap), scales)
+    got = product(dirty)
+    assert torch.equal(got[torch.from_numpy(~bad).cuda()], want[torch.from_numpy(~bad).cuda()])
+    assert not torch.isfinite(got[torch.from_numpy(bad).cuda()]).any()
+
+
 @pytest.mark.parametrize("K,N,counts", [(384, 272, many(6, 260, 300, 65)), (264, 528, many(7, 175, 129))],
                          ids=name)
 @pytest.mark.parametrize("fp8", [False, True])
