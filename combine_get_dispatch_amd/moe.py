@@ -548,9 +548,19 @@ class W4Experts:
         _sized(w_codes, nb, "w_codes")
         _sized(w_scales, ns, "w_scales")
         _sized(w_zeros, ns, "w_zeros")
-        self._tensors = w_codes, w_scales, w_zeros  # held as long as their pointers
+        _weight_ptrs(w_codes, w_scales, w_zeros)  # checks types and places
+        self._tensors = w_codes, w_scales, w_zeros
         self._ref = ctypes.byref(self.cfg)
-        self._weights = _weight_ptrs(w_codes, w_scales, w_zeros)
+        self._given = [(t, t.dtype, t.shape, name) for t, name in
+                       zip(self._tensors, ("w_codes", "w_scales", "w_zeros")) if t is not None]
+
+    def _where(self):
+        """Device and pointers at this call."""
+        at = [_kept_at(*t) for t in self._given]
+        for t, (d, _) in zip(self._given, at):
+            if d != at[0][0]:
+                raise ValueError(f"{t[3]} is on {t[0].device}, w_codes on {self.w_codes.device}")
+        return at[0][0], (at[0][1], at[1][1], at[2][1] if len(at) == 3 else None)
 
     @property
     def w_codes(self):
@@ -599,7 +609,7 @@ class W4Experts:
         if out is None:
             out = _empty(stream, (x.shape[0], self.cfg.out_features), dtype=torch.bfloat16,
                          device=x.device)
-        _product(self.cfg, self._ref, x, x_scales, self._weights, expert_offsets,
+        _product(self.cfg, self._ref, x, x_scales, self._where(), expert_offsets,
                  num_tokens_per_expert, out, stream)
         return out
 
@@ -624,7 +634,7 @@ class Bf16Experts:
         E, N, K = weights.shape
         self.cfg = ep_experts_t(E, K, N)
         self._ref = ctypes.byref(self.cfg)
-        self._shape = weights.shape
+        self._given = weights, weights.dtype, weights.shape, "w"
 
     @property
     def weights(self):
@@ -632,9 +642,7 @@ class Bf16Experts:
 
     def _where(self):
         """Device and pointer at this call."""
-        import torch
-
-        return _kept_at(self._weights, torch.bfloat16, self._shape, "w")
+        return _kept_at(*self._given)
 
     def product(self, x, x_scales, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, out_features] (half of them with swiglu): each expert's
@@ -693,6 +701,8 @@ class SwigluCheckpoint:
                                   device=dev)
         self._scales = torch.empty(_checkpoint_shape(self.capacity, self.features),
                                    dtype=torch.float32, device=dev)
+        self._given = [(t, t.dtype, t.shape, name)
+                       for t, name in ((self._codes, "codes"), (self._scales, "scales"))]
 
     @property
     def codes(self):
@@ -704,14 +714,11 @@ class SwigluCheckpoint:
 
     def _where(self):
         """Device, rows and pointers at this call."""
-        import torch
-
-        cap, F = self.capacity, self.features
-        d, codes = _kept_at(self._codes, torch.uint8, (cap, 2 * F), "codes")
-        other, scales = _kept_at(self._scales, torch.float32, _checkpoint_shape(cap, F), "scales")
+        d, codes = _kept_at(*self._given[0])
+        other, scales = _kept_at(*self._given[1])
         if other != d:
             raise ValueError(f"scales is on {self._scales.device}, codes on {self._codes.device}")
-        return d, cap, codes, scales
+        return d, self.capacity, codes, scales
 
     def save(self, gate_up, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, features]: silu(gate) * up; keeps gate and up."""

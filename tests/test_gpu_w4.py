@@ -706,3 +706,35 @@ def test_rows_that_are_not_finite_keep_to_themselves(fp8, swiglu):
     bad = bad.cuda()
     assert not bool(torch.isfinite(got[bad]).any())
     assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+def test_weights_with_another_storage(zeros):
+    """The packed tensors' storage may be replaced between calls, also by way of
+    the host; what does not fit is refused."""
+    rng = np.random.default_rng(51)
+    E, K, N, counts = 2, 256, 48, [3, 20]
+    q, s, z = draw(rng, E, K, N, 128, zeros, False, True)
+    x, _, _ = draw_rows(rng, sum(counts), K, False, True)
+    at = dev(offsets_of(counts)), dev(np.array(counts, np.int32))
+    w = packed(q, s, z, False)
+    say(f"4-bit weights with another storage zeros={zeros}")
+    want = w.product(x, None, *at)
+    kept = [t for t in (w.w_codes, w.w_scales, w.w_zeros) if t is not None]
+    olds = [t.data for t in kept]
+    for t in kept:
+        t.data = t.cpu()
+    with pytest.raises(ValueError):
+        w.product(x, None, *at)
+    for t, old in zip(kept, olds):
+        t.data = t.cuda()
+        old.zero_()
+    assert torch.equal(w.product(x, None, *at), want)
+    for t in kept:
+        was = t.data
+        for other in (was[:1], was.transpose(2, 3)):
+            t.data = other
+            with pytest.raises(ValueError):
+                w.product(x, None, *at)
+        t.data = was
+    assert torch.equal(w.product(x, None, *at), want)

@@ -169,3 +169,33 @@ def test_python_checks():
 def test_status_names():
     assert ep.lib().ep_status_string(ep.EP_ERR_SEQS) != b"unknown status"
     assert ep.lib().ep_status_string(ep.EP_ERR_SEQS + 1) == b"unknown status"
+
+
+def test_packed_weights_are_looked_at_at_each_call(monkeypatch):
+    """Their tensors' storage may be replaced; what does not fit is refused."""
+    from combine_get_dispatch_amd import moe
+
+    monkeypatch.setattr(moe, "_device", lambda t, name: t.get_device())  # host tensors here
+    E, K, N = 2, 256, 32
+    for zeros in (False, True):
+        codes = torch.zeros(E, 1, 2, 2, 1024, dtype=torch.uint8)
+        scales = torch.zeros(E, 1, 2, 2, 16, dtype=torch.bfloat16)
+        z = torch.zeros(E, 1, 2, 2, 16, dtype=torch.uint8) if zeros else None
+        w = ep.W4Experts(codes, scales, z, N, K, 128)
+
+        def at():
+            return -1, tuple(t if t is None else t.data_ptr() for t in (codes, scales, z))
+
+        assert w._where() == at()
+        for t, name in ((codes, "w_codes"), (scales, "w_scales"), (z, "w_zeros")):
+            if t is None:
+                continue
+            was = t.data
+            t.data = torch.ones_like(was)  # moved: the calls take it where it is
+            assert w._where() == at()
+            for other in (was[:1], was.transpose(2, 3), was.view(torch.int8)):
+                t.data = other
+                with pytest.raises(ValueError, match=f"^{name} "):
+                    w._where()
+            t.data = was
+        assert w._where() == at()
