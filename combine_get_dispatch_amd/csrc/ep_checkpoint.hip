@@ -293,17 +293,7 @@ struct Range {
   int64_t bytes;
 };
 
-bool apart(const Range &a, const Range &b) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-  return a.p == nullptr || b.p == nullptr || p >= q + (uintptr_t)b.bytes ||
-         q >= p + (uintptr_t)a.bytes;
-}
-
-#define EP_TRY(expr)                \
-  do {                              \
-    const ep_status_t st_ = (expr); \
-    if (st_ != EP_OK) return st_;   \
-  } while (0)
+bool apart(const Range &a, const Range &b) { return !overlap(a.p, a.bytes, b.p, b.bytes); }
 
 }  // namespace
 }  // namespace ep

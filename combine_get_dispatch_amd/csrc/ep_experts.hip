@@ -1301,12 +1301,6 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
   }
 }
 
-#define EP_TRY(expr)                \
-  do {                              \
-    const ep_status_t st_ = (expr); \
-    if (st_ != EP_OK) return st_;   \
-  } while (0)
-
 // Calls f with the tiles' size: 128 x 128, two workgroups per compute unit,
 // where tiles of 256 x 256 would leave half the chip idle (kSmallTiles).  Of the
 // experts' rows only the buffer's are known.
@@ -1389,11 +1383,6 @@ ep_status_t check_x(const ep_experts_t *experts, ep_dtype_t dtype, const void *x
   if (!aligned_to(x, 16) || !aligned_to(x_scales, 4))
     return failf(EP_ERR_INVALID_ARG, "x must be 16-byte, x_scales 4-byte aligned");
   return EP_OK;
-}
-
-bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && p < q + (uintptr_t)b_bytes && q < p + (uintptr_t)a_bytes;
 }
 
 int64_t weight_values(const ep_experts_t *x) {

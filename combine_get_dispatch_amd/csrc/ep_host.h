@@ -35,4 +35,16 @@ inline bool aligned_to(const void *p, uintptr_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
+// Whether two arrays share bytes; NULL shares none.
+inline bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && p < q + (uintptr_t)b_bytes && q < p + (uintptr_t)a_bytes;
+}
+
 }  // namespace ep
+
+#define EP_TRY(expr)                \
+  do {                              \
+    const ep_status_t st_ = (expr); \
+    if (st_ != EP_OK) return st_;   \
+  } while (0)

@@ -1474,12 +1474,6 @@ ep_status_t check_seqs(int32_t num_seqs) {
   return EP_OK;
 }
 
-#define EP_TRY(expr)                \
-  do {                              \
-    const ep_status_t st_ = (expr); \
-    if (st_ != EP_OK) return st_;   \
-  } while (0)
-
 }  // namespace
 }  // namespace ep
 

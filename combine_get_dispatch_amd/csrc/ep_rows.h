@@ -1,5 +1,6 @@
-// What the kernels on expert-major rows share: an expert's rows inside the
-// buffers, their blocks, and a few conversions.  Not installed.
+// What the kernels on expert-major rows share (the products with 4-bit and with
+// bf16 weights, the checkpoint): an expert's rows inside the buffers, their
+// blocks, and a few conversions.  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -24,35 +24,15 @@
 #include "ep.h"
 #include "ep_host.h"
 #include "ep_moe.h"
+#include "ep_rows.h"
 
 namespace ep {
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTileN = 16;       // output columns of a weight tile
 constexpr int kTileK = 128;      // columns of the sum in a weight tile
 constexpr int kTileBytes = 1024;
 constexpr int kRows = 16;        // rows of x per matrix instruction
-
-__device__ __forceinline__ float bf16_to_f32(uint16_t v) {
-  return __uint_as_float((uint32_t)v << 16);
-}
-
-// Nearest even; NaN stays NaN.
-__device__ __forceinline__ uint16_t f32_to_bf16(float v) {
-  return __builtin_bit_cast(uint16_t, (__bf16)v);
-}
-
-// By exp(-|y|): exp(-y) of a y below -88 is infinite while silu(y) is still a
-// fp32 number.
-__device__ __forceinline__ float silu(float y) {
-  const float t = expf(-fabsf(y));
-  return y * ((y < 0.0f ? t : 1.0f) / (1.0f + t));
-}
 
 // --------------------------------------------------------------------------
 // Packing
@@ -99,8 +79,6 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(PackArgs a) {
 // Product
 // --------------------------------------------------------------------------
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 struct ProductArgs {
   const void *x;
   const float *x_scales;
@@ -113,19 +91,10 @@ struct ProductArgs {
   int32_t stream_rows;  // experts with more rows are tiled
 };
 
-// Rows of an expert inside the buffers.
-__device__ __forceinline__ void rows_between(int32_t offset, int32_t count, int64_t capacity,
-                                             int64_t *first, int64_t *rows) {
-  *first = offset;
-  *rows = 0;
-  if (offset < 0 || count <= 0 || offset >= capacity) return;
-  *rows = count < capacity - offset ? count : capacity - offset;
-}
-
-// The same for an expert that the whole wave works on.
+// Rows of an expert that the whole wave works on.
 __device__ __forceinline__ void expert_rows(const ProductArgs &a, int e, int64_t *first,
                                             int64_t *rows) {
-  rows_between(uniform(a.offsets[e]), uniform(a.counts[e]), a.capacity, first, rows);
+  rows_inside(uniform(a.offsets[e]), uniform(a.counts[e]), a.capacity, first, rows);
 }
 
 // The pairs of codes of one word as bf16 pairs u (1 + q/16): a shift and one
@@ -344,7 +313,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void product_stream_kernel(Pr
         if (SWIGLU) up += part[s][kOut + i][at];
       }
       y *= kUnit;
-      if (SWIGLU) y = silu(y) * (up * kUnit);
+      if (SWIGLU) y = silu_of(y) * (up * kUnit);
       if (m < left && n < a.N) a.out[(first + r0 + m) * a.N + n] = f32_to_bf16(y);
     }
     __syncthreads();
@@ -399,7 +368,7 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
     for (int i = 0; i < 4; ++i) {
       const int e = tid * 4 + i;
       int64_t first = 0, rows = 0;
-      if (e < E) rows_between(a.offsets[e], a.counts[e], a.capacity, &first, &rows);
+      if (e < E) rows_inside(a.offsets[e], a.counts[e], a.capacity, &first, &rows);
       mine[i] = rows > a.stream_rows ? (int32_t)((rows + kBlockRows - 1) / kBlockRows) : 0;
       total += mine[i];
     }
@@ -591,7 +560,7 @@ __global__ __launch_bounds__(256, kTileWaves) void product_tile_kernel(ProductAr
 #pragma unroll
           for (int i = 0; i < kOut; ++i) {
             float y = acc[m][i][v] * kUnit;
-            if (SWIGLU) y = silu(y) * (acc[m][kOut + i][v] * kUnit);
+            if (SWIGLU) y = silu_of(y) * (acc[m][kOut + i][v] * kUnit);
             if ((ot + i) * kTileN + col < a.N) row[at + i * kTileN] = f32_to_bf16(y);
           }
         }
@@ -620,12 +589,6 @@ ep_status_t check_w4(const ep_w4_t *w) {
     return failf(EP_ERR_INVALID_ARG, "out_features %d outside [1, 2^20)", w->out_features);
   return EP_OK;
 }
-
-#define EP_TRY(expr)                \
-  do {                              \
-    const ep_status_t st_ = (expr); \
-    if (st_ != EP_OK) return st_;   \
-  } while (0)
 
 // Calls f with the compile-time forms of the four choices.
 template <typename F>
