@@ -66,8 +66,9 @@ __device__ __forceinline__ u32x4 scaled_bf16(u32x2 codes, float scale) {
 // 64 x 64, 64 of the sum at a time, through registers, two stages ahead of their
 // use.  Layouts in LDS as in the large tiles: "along", where l is consecutive,
 // 64 rows of 128 bytes; "across", where m or n is, 64 l of 128 bytes.
-// 333 rows of 11 experts, rows' gradient of 1480 x 1001: 19 us, bound by the
-// latency of 16 stages; 32768 rows of 32 experts, 2047 x 7168: 3.94 ms, 244 TFLOP/s.
+// 333 rows of 11 experts, rows' gradient of 1480 x 1001: 18.3 us, bound by the
+// latency of 16 stages; 32768 rows of 32 experts, 2047 x 7168: 3.73 ms, 258 TFLOP/s
+// (rows' gradient 6.75 ms, weights' 6.86 ms, 140).
 constexpr int kAnyTile = 64, kAnyDepth = 64, kAnyGrid = 1024;
 constexpr int kAnySide = kAnyTile * kAnyDepth * 2;
 
@@ -253,12 +254,13 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 // need twice the requests: 1018 us in the first case below), and from there to
 // the 16 x 16 x 32 instruction, which needs less power than 32 x 32 x 16 for the
 // same sums (of random numbers, alone: 2159 and 1885 TFLOP/s).
-//   32768 rows of 32 experts, 2048 x 7168        860 us, 1120 TFLOP/s
-//   one expert, 4096 x 4096                      800 us, 1370 TFLOP/s
-//   rows' gradient of 32, 4096 x 7168           1720 us, 1120 TFLOP/s
-//   weights' gradient of 32, 4096 x 7168        1796 us, 1070 TFLOP/s
-//     with FP8 rows                             2060 us,  934 TFLOP/s
-//   128 FP8 rows of 32, 7168 x 2 x 2048          272 us, 6.9 TB/s of weights
+//   32768 rows of 32 experts, 2048 x 7168        860 to 900 us, 1070 to 1120 TFLOP/s
+//   one expert, 4096 x 4096                      800 to 835 us, 1320 to 1370 TFLOP/s
+//   rows' gradient of 32, 4096 x 7168           1730 to 1795 us, 1070 to 1110 TFLOP/s
+//   weights' gradient of 32, 4096 x 7168        1775 to 1853 us, 1040 to 1080 TFLOP/s
+//     with FP8 rows                             2057 to 2160 us,  890 to  935 TFLOP/s
+//   128 FP8 rows of 32, 7168 x 2 x 2048          273 us, 6.9 TB/s of weights
+// (medians on two boxes: by their power, large cases differ by 5 %)
 // What bounds it: of one expert's time the matrix instructions are busy 70 %; the
 // clock is then at 1.9 GHz, by power (2.4 with rows and weights of zeros).  With
 // 32 uneven experts they are busy 60 %: last tiles of few rows, items that do not
@@ -285,8 +287,9 @@ typedef __attribute__((address_space(3))) uint8_t lds_byte;
 // five wait states; the hardware does not wait, and the compiler does so for its
 // own instructions alone.  s_mov_b32 and s_nop 3 are five, whatever comes before
 // (and m0's one); in the tiles that takes up to 1.4 % (rows' gradient of 32
-// experts, 4096 x 7168: 1730 us, with s_nop 0 1712).  m0 is reserved and no clobber can name it: nothing else in
-// these kernels may use it, which a test of the built library holds.
+// experts, 4096 x 7168: 1730 us, with s_nop 0 1712).  m0 is reserved and no
+// clobber can name it: nothing else in these kernels may use it, which a test of
+// the built library holds.
 // ONCE: non-temporal, for what no other workgroup and no later call reads again.
 template <bool ONCE = false>
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
@@ -432,8 +435,10 @@ struct Items {
   // An item of the weights' gradient goes by its expert's rows: eighths of the
   // steps, with the end of an item by what it loads and stores.  (32 experts whose
   // rows differ by a third, 4096 x 7168: 1796 us, by items 1914; FP8 rows 2067,
-  // 2303; fp32 added up, 8 experts of 2048 x 7168: 252, 269; but 256 items, 4
-  // experts of 2048 x 2048: 56, 39.)
+  // 2303; fp32 added up, 8 experts of 2048 x 7168: 252, 269.)  Few items have to
+  // come out even instead (experts of 2048 x 2048, 64 items and 1024 rows each, by
+  // steps and by items: 4 experts 55, 39; 8 82, 72; 12 116, 113; 16 140, 138; 24
+  // 203, 214; of 128 rows each 12 experts 38, 33 and 16 47, 44).
   __device__ __forceinline__ void eighth(int part, int64_t *from, int64_t *to) const {
     const int lane = threadIdx.x & 63;
     if constexpr (KIND != kWeightsGrad) {
@@ -645,8 +650,8 @@ __global__ __launch_bounds__(kTileWaves * 64, SMALL ? 4 : 2) void product_tile_k
 
   // The loads run ahead of the products, through the items' ends: columns two
   // stages ahead (FP8 columns: three, one of them for the rounding), in three
-  // slots, and rows one, in two; with FP8 rows one more.  (With two slots of both the decode share in bf16 takes 364
-  // us, so 311, both without non-temporal loads.)
+  // slots, and rows one, in two; with FP8 rows one more.  (With two slots of both
+  // the decode share in bf16 takes 364 us, so 311, both without non-temporal loads.)
   struct Loads {
     const uint8_t *base = nullptr, *scales = nullptr;
     int bytes = 0;  // along: from the base to the last row's end
@@ -1309,6 +1314,10 @@ __global__ __launch_bounds__(kStreamWaves * 64) void product_stream_kernel(Produ
 //                   32, 47     24, 42                32, 47     47, 48
 //   rows' gradient                       24, 44                 48, 51
 //   weights' gradient, 2048 x 2048       44, 57     47, 45     48, 39
+//     with FP8 rows  38, 63              62, 78     94, 85    122, 84
+// FP8 rows' larger tile is of 128 x 256; 8 experts, 2048 x N, of 128 and of 128 x 256:
+//   1024 rows       29, 39               50, 43
+//   4096 rows, tiles   40 29, 39   80 41, 39   120 42, 40   160 57, 72   200 61, 73
 constexpr int64_t kSmallTiles = 160;
 
 template <typename F>
@@ -1328,8 +1337,13 @@ constexpr int64_t kInfinityCache = int64_t{256} << 20;
 // Non-temporal and not, us (32 experts, 7168 x 2 x 2048, but where it says):
 //   tiles of 256 rows   4 rows each 280, 311   32 289, 314   128 400, 419
 //     rows' gradient, 4096 x 7168   128 396, 399      2048 x 7168   16 139, 159
-//     one of 2048 x 7168 with 1024 rows each 964, 907
+//     2048 x 7168, rows each   64 190, 190   128 220, 222   192 262, 265
+//                              256 346, 321   512 535, 485   1024 964, 907
+//     its rows' gradient       64 148, 167   128 224, 243   256 338, 343
 //   FP8 rows, tiles of 128          4 272, 309    128 503, 471
+//     2048 x 7168              32 194, 202   64 195, 198   96 253, 237   128 293, 249
+//   4096 rows of few of 256 experts, 2048 x 2048: of 32 61, 70; of 8, whose weights
+//     the cache would hold, 55, 54; FP8 rows 88, 87 and 80, 77
 //   streamed: one token's 8 experts, FP8 rows 76, 83
 //     64 rows of 2 experts, 4096 x 2048, in the cache and read four times 26, 24
 bool read_once(const ProductArgs &a, int row_tile) {
