@@ -210,18 +210,29 @@ def ep_expert_product_w4(w4: ep_w4_t, x, x_scales, w_codes, w_scales, w_zeros, e
     _sized(w_codes, nb, "w_codes")
     _sized(w_scales, ns, "w_scales")
     _sized(w_zeros, ns, "w_zeros")
-    _product(w4, ctypes.byref(w4), x, x_scales, _weight_ptrs(w_codes, w_scales, w_zeros),
+    _product(w4, ctypes.byref(w4), x, x_scales, _packed(w_codes, w_scales, w_zeros),
              expert_offsets, num_tokens_per_expert, out, stream)
 
 
-def _weight_ptrs(w_codes, w_scales, w_zeros):
-    """Their device, and the pointers."""
+def _packed(w_codes, w_scales, w_zeros):
+    """What _kept_at takes for each of the packed tensors, or None."""
     import torch
 
-    d = _device(w_codes, "w_codes")
-    return d, (_at(w_codes, d, torch.uint8, None, "w_codes"),
-               _at(w_scales, d, torch.bfloat16, None, "w_scales"),
-               _at(w_zeros, d, torch.uint8, None, "w_zeros"))
+    return [None if t is None else (t, dtype, t.shape, name) for t, dtype, name in
+            ((w_codes, torch.uint8, "w_codes"), (w_scales, torch.bfloat16, "w_scales"),
+             (w_zeros, torch.uint8, "w_zeros"))]
+
+
+def _packed_at(packed):
+    """Their device, and the pointers, at this call."""
+    dev, codes = _kept_at(*packed[0])
+    pointers = [codes]
+    for p in packed[1:]:
+        d, at = (dev, None) if p is None else _kept_at(*p)
+        if d != dev:
+            raise ValueError(f"{p[3]} is on {p[0].device}, w_codes on {packed[0][0].device}")
+        pointers.append(at)
+    return dev, pointers
 
 
 def _product(w4, ref, x, x_scales, weights, expert_offsets, num_tokens_per_expert, out, stream):
@@ -238,12 +249,13 @@ def _product(w4, ref, x, x_scales, weights, expert_offsets, num_tokens_per_exper
         raise ValueError(f"expert_offsets has shape {tuple(expert_offsets.shape)}, "
                          f"expected ({E},) or ({E + 1},)")
     d = _device(x, "x")
-    if d != weights[0]:
+    at, pointers = _packed_at(weights)
+    if d != at:
         raise ValueError("the weights are not on the current device")
     st = lib().ep_expert_product_w4(
         ref, EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16,
         _at(x, d, torch.uint8 if fp8 else torch.bfloat16, None, "x"),
-        _at(x_scales, d, torch.float32, (cap, K // 128), "x_scales"), *weights[1],
+        _at(x_scales, d, torch.float32, (cap, K // 128), "x_scales"), *pointers,
         _at(expert_offsets, d, torch.int32, None, "expert_offsets"),
         _at(num_tokens_per_expert, d, torch.int32, (E,), "num_tokens_per_expert"), cap,
         _at(out, d, torch.bfloat16, None, "out"), _stream(stream))
@@ -303,11 +315,11 @@ def _weights_at(w, experts):
 
 
 def _kept_at(t, dtype, shape, name):
-    """Device and pointer of a tensor that an object holds from call to call:
-    its storage, shape, strides and type may have been replaced (by ``.data``),
-    the address left as it was."""
+    """Device and pointer of a contiguous tensor of this type and shape.  For
+    tensors that an object holds from call to call: their storage, shape, strides
+    and type may have been replaced (by ``.data``), the address left as it was."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} is now {t.dtype} {tuple(t.shape)} with strides {t.stride()}, "
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} with strides {t.stride()}, "
                          f"expected contiguous {dtype} {tuple(shape)}")
     return t.get_device(), t.data_ptr()
 
@@ -548,19 +560,11 @@ class W4Experts:
         _sized(w_codes, nb, "w_codes")
         _sized(w_scales, ns, "w_scales")
         _sized(w_zeros, ns, "w_zeros")
-        _weight_ptrs(w_codes, w_scales, w_zeros)  # checks types and places
         self._tensors = w_codes, w_scales, w_zeros
         self._ref = ctypes.byref(self.cfg)
-        self._given = [(t, t.dtype, t.shape, name) for t, name in
-                       zip(self._tensors, ("w_codes", "w_scales", "w_zeros")) if t is not None]
-
-    def _where(self):
-        """Device and pointers at this call."""
-        at = [_kept_at(*t) for t in self._given]
-        for t, (d, _) in zip(self._given, at):
-            if d != at[0][0]:
-                raise ValueError(f"{t[3]} is on {t[0].device}, w_codes on {self.w_codes.device}")
-        return at[0][0], (at[0][1], at[1][1], at[2][1] if len(at) == 3 else None)
+        self._weights = _packed(w_codes, w_scales, w_zeros)
+        _device(w_codes, "w_codes")
+        _packed_at(self._weights)
 
     @property
     def w_codes(self):
@@ -609,7 +613,7 @@ class W4Experts:
         if out is None:
             out = _empty(stream, (x.shape[0], self.cfg.out_features), dtype=torch.bfloat16,
                          device=x.device)
-        _product(self.cfg, self._ref, x, x_scales, self._where(), expert_offsets,
+        _product(self.cfg, self._ref, x, x_scales, self._weights, expert_offsets,
                  num_tokens_per_expert, out, stream)
         return out
 

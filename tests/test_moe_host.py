@@ -184,18 +184,18 @@ def test_packed_weights_are_looked_at_at_each_call(monkeypatch):
         w = ep.W4Experts(codes, scales, z, N, K, 128)
 
         def at():
-            return -1, tuple(t if t is None else t.data_ptr() for t in (codes, scales, z))
+            return -1, [t if t is None else t.data_ptr() for t in (codes, scales, z)]
 
-        assert w._where() == at()
+        assert moe._packed_at(w._weights) == at()
         for t, name in ((codes, "w_codes"), (scales, "w_scales"), (z, "w_zeros")):
             if t is None:
                 continue
             was = t.data
             t.data = torch.ones_like(was)  # moved: the calls take it where it is
-            assert w._where() == at()
+            assert moe._packed_at(w._weights) == at()
             for other in (was[:1], was.transpose(2, 3), was.view(torch.int8)):
                 t.data = other
                 with pytest.raises(ValueError, match=f"^{name} "):
-                    w._where()
+                    moe._packed_at(w._weights)
             t.data = was
-        assert w._where() == at()
+        assert moe._packed_at(w._weights) == at()
