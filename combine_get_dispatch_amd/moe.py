@@ -215,7 +215,7 @@ def ep_expert_product_w4(w4: ep_w4_t, x, x_scales, w_codes, w_scales, w_zeros, e
 
 
 def _packed(w_codes, w_scales, w_zeros):
-    """What _kept_at takes for each of the packed tensors, or None."""
+    """What _weights_kept_at takes for each of the packed tensors, or None."""
     import torch
 
     return [None if t is None else (t, dtype, t.shape, name) for t, dtype, name in
@@ -225,10 +225,10 @@ def _packed(w_codes, w_scales, w_zeros):
 
 def _packed_at(packed):
     """Their device, and the pointers, at this call."""
-    dev, codes = _kept_at(*packed[0])
+    dev, codes = _weights_kept_at(*packed[0])
     pointers = [codes]
     for p in packed[1:]:
-        d, at = (dev, None) if p is None else _kept_at(*p)
+        d, at = (dev, None) if p is None else _weights_kept_at(*p)
         if d != dev:
             raise ValueError(f"{p[3]} is on {p[0].device}, w_codes on {packed[0][0].device}")
         pointers.append(at)
@@ -322,6 +322,14 @@ def _kept_at(t, dtype, shape, name):
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} with strides {t.stride()}, "
                          f"expected contiguous {dtype} {tuple(shape)}")
     return t.get_device(), t.data_ptr()
+
+
+def _weights_kept_at(t, dtype, shape, name):
+    """The same of weights, which may be a part of a larger tensor whose storage
+    is given back for a while: a part of none still has an address."""
+    if t.untyped_storage().nbytes() < (t.storage_offset() + t.numel()) * t.itemsize:
+        raise ValueError(f"{name} reaches past the end of its storage")
+    return _kept_at(t, dtype, shape, name)
 
 
 def _here(t, name, other, what):
@@ -546,8 +554,9 @@ class EpRouter:
 
 class W4Experts:
     """Packed 4-bit weights of a set of experts (W4Experts.pack lays out
-    row-major ones) and their product.  Their values may be rewritten in place;
-    other tensors are another W4Experts."""
+    row-major ones) and their product.  They are read in place at each call, and
+    may be rewritten in place or moved (by ``.data``); other tensors are another
+    W4Experts."""
 
     def __init__(self, w_codes, w_scales, w_zeros, out_features, in_features, group):
         if w_codes.dim() < 2:
@@ -624,8 +633,9 @@ class Bf16Experts:
     are the gate's, then the up projection's, and ``product`` gives
     silu(gate) * up; the gradients are those of the plain product (gate and
     up), which an object without swiglu on the same weights gives.  The
-    weights are read in place at each call, and may be rewritten in place;
-    other tensors are another Bf16Experts."""
+    weights are read in place at each call, and may be rewritten in place or
+    moved (by ``.data``) in their shape and type; other tensors are another
+    Bf16Experts."""
 
     def __init__(self, weights, swiglu=False):
         import torch
@@ -646,7 +656,7 @@ class Bf16Experts:
 
     def _where(self):
         """Device and pointer at this call."""
-        return _kept_at(*self._given)
+        return _weights_kept_at(*self._given)
 
     def product(self, x, x_scales, expert_offsets, num_tokens_per_expert, out=None, stream=None):
         """bf16 [rows, out_features] (half of them with swiglu): each expert's
@@ -693,7 +703,8 @@ class SwigluCheckpoint:
     """The 8-bit checkpoint of a layer's gate and up rows: codes
     [capacity, 2 features], scales [capacity, 2 ceil(features / 128)].  They
     are allocated once, on the current stream (another stream waits for it
-    before its first call), and the next ``save`` overwrites them."""
+    before its first call), and the next ``save`` overwrites them.  Between the
+    calls they may be elsewhere (``codes.data = codes.cpu()``, and back)."""
 
     def __init__(self, capacity, features, num_experts, device="cuda"):
         import torch

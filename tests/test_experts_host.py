@@ -258,3 +258,27 @@ def test_checkpoint_is_looked_at_at_each_call():
                 c._where()
         t.data = was
     assert c._where() == (-1, 4, c.codes.data_ptr(), c.scales.data_ptr())
+
+
+def test_weights_whose_storage_was_freed():
+    """Views of a flat tensor whose storage is given back between steps."""
+    from combine_get_dispatch_amd import moe
+
+    flat = torch.zeros(4, 32, 128, dtype=torch.bfloat16)
+    codes, scales = torch.zeros(4, 1, 2, 1, 1024, dtype=torch.uint8), torch.zeros(
+        4, 1, 2, 1, 16, dtype=torch.bfloat16)
+    experts = [ep.Bf16Experts(flat), ep.Bf16Experts(flat[2:])]
+    packed = moe._packed(codes[2:], scales[2:], None)
+    calls = [e._where for e in experts] + [lambda: moe._packed_at(packed)]
+    for call in calls:
+        call()
+    for t in (flat, codes, scales):
+        for n in (0, 16):
+            size = t.untyped_storage().nbytes()
+            t.untyped_storage().resize_(n)
+            for call in calls[:2] if t is flat else calls[2:]:
+                with pytest.raises(ValueError, match="storage"):
+                    call()
+            t.untyped_storage().resize_(size)
+            for call in calls:
+                call()
